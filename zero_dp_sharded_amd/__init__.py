@@ -502,3 +502,12 @@ def reduce_buckets(h: int, contribs: Sequence, shard_elems: int, bucket_elems: i
     for off in range(0, shard_elems, bucket_elems):
         ln = min(bucket_elems, shard_elems - off)
         zero_bucket_reduce(h, [p + off * esz for p in ptrs], off, ln, stream)
+
+
+# the training operators (libzeroops.so), under their C names too
+from .ops import (AdamWTensor, zero_adamw_destroy, zero_adamw_get_counters,  # noqa: E402
+                  zero_adamw_init, zero_adamw_result, zero_adamw_set_counters,
+                  zero_adamw_set_grads, zero_adamw_step, zero_layernorm_backward,
+                  zero_layernorm_forward, zero_layernorm_workspace, zero_moments_pack,
+                  zero_moments_unpack, zero_ops_abi_version, zero_ops_last_error,
+                  zero_vocab_loss, zero_vocab_loss_workspace)

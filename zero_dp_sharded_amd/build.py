@@ -1,4 +1,5 @@
-"""Build libzeroshard.so for gfx950 with hipcc, in-tree.
+"""Build libzeroshard.so (the owner's step) and libzeroops.so (the training
+operators) for gfx950 with hipcc, in-tree.
 
 Floating-point flags: no contraction into fused multiply-adds, correctly
 rounded fp32 divide and square root, fp32 denormals kept, and no packed-fp32
@@ -23,6 +24,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzeroshard.so")
 SOURCES = ["zero_kernels.hip", "zero_shard.cpp", "zero_state_bytes.cpp"]
+# the training operators (include/zero_ops.h)
+OPS_LIB = os.path.join(HERE, "libzeroops.so")
+OPS_SOURCES = ["ops_norm.hip", "ops_loss.hip", "ops_adamw.hip", "zero_ops.cpp"]
 # benchmark helper: plain HBM copy (ceiling and counter calibration)
 COPY_LIB = os.path.join(HERE, "libhbmcopy.so")
 COPY_SOURCES = ["hbm_copy.hip"]
@@ -91,6 +95,7 @@ def build(verbose: bool = False) -> str:
     objdir = os.path.join(ROOT, "_build", "zeroshard")
     os.makedirs(objdir, exist_ok=True)
     _link(_compile(SOURCES, objdir, verbose), LIB, verbose)
+    _link(_compile(OPS_SOURCES, objdir, verbose), OPS_LIB, verbose)
     _link(_compile(COPY_SOURCES, objdir, verbose), COPY_LIB, verbose)
     build_variant(SPLIT_LAUNCH_DEFINES, SPLIT_LAUNCH_DIR, verbose,
                   objdir=os.path.join(ROOT, "_build", "split_launch"))

@@ -1,0 +1,58 @@
+// Shared by the training operators' kernels (ops_*.hip): storage types, vectors
+// of 16 bytes at any address, and sums over a wave in a fixed order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace zo {
+
+constexpr int kWave = 64;
+constexpr int kCUs = 256;    // compute units of an MI355X: launch shapes are cut for it
+
+template <typename T> struct Vec;    // W elements of T in 16 bytes
+template <> struct Vec<_Float16> { static constexpr int W = 8; };
+template <> struct Vec<__bf16> { static constexpr int W = 8; };
+template <> struct Vec<float> { static constexpr int W = 4; };
+
+template <typename T, int W> using vec_t = T __attribute__((ext_vector_type(W)));
+
+// The same vector at an address aligned to one element only: the card loads and
+// stores 16 bytes at any element's address, so rows of odd widths need no path
+// of their own.
+template <typename T, int W>
+struct __attribute__((packed, aligned(sizeof(T)))) unaligned_vec {
+    vec_t<T, W> v;
+};
+
+template <typename T, int W>
+__device__ __forceinline__ vec_t<T, W> load_vec(const T* p)
+{
+    return reinterpret_cast<const unaligned_vec<T, W>*>(p)->v;
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_vec(T* p, vec_t<T, W> x)
+{
+    reinterpret_cast<unaligned_vec<T, W>*>(p)->v = x;
+}
+
+// Sum over the 64 lanes, the same in every lane (xor butterfly).
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, kWave);
+    return x;
+}
+
+__device__ __forceinline__ double wave_sum(double x)
+{
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, kWave);
+    return x;
+}
+
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+}  // namespace zo

@@ -1,0 +1,455 @@
+// Layer norm over the last dimension, forward and backward:
+//     mean = sum x / D ;  rstd = 1 / sqrt(sum (x - mean)^2 / D + eps)
+//     xhat = (x - mean) rstd ;  y = xhat w + b
+//     g = dy w ;  dx = rstd (g - mean(g) - xhat mean(g xhat))
+//     dw = sum_rows dy xhat ;  db = sum_rows dy
+// All of it in fp32, rounded once at the end.
+//
+// Both directions are bound by memory: 2 (forward) or 3 (backward) rows of D
+// elements, each moved once.  A row stays in registers between its sums and its
+// results; it belongs to one wave where it fits (no barrier at all), else to 4 or
+// 16 waves that join their sums through LDS; a row of more than 16384 elements (of
+// 2 bytes; 8192 of 4) is read again from cache instead.
+//
+// The weight's and bias's gradients are sums over all rows: each workgroup keeps
+// the sums of the rows it walks in registers, adds its waves' in LDS, and writes
+// one row of partial sums; a second kernel adds those in their order.  No atomics,
+// so the same input gives the same bits.
+
+#include "ops_common.h"
+#include "ops_internal.h"
+
+namespace zo {
+namespace {
+
+// Sum of a and b over the NW waves of a row, the same in each.
+template <int NW>
+__device__ __forceinline__ void row_sum(float& a, float& b, float2* sh)
+{
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (NW > 1) {
+        const int wave = threadIdx.x >> 6;
+        __syncthreads();                       // the last sums have been read
+        if ((threadIdx.x & 63) == 0) sh[wave] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            a += sh[k].x;
+            b += sh[k].y;
+        }
+    }
+}
+
+// The W elements from column c on, as fp32, zeros past the width.
+template <typename T, int W>
+__device__ __forceinline__ void load_part(const T* row, int64_t c, int64_t width, float (&x)[W])
+{
+    if (c + W <= width) {
+        const vec_t<T, W> v = load_vec<T, W>(row + c);
+#pragma unroll
+        for (int k = 0; k < W; ++k) x[k] = (float)v[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) x[k] = c + k < width ? (float)row[c + k] : 0.0f;
+    }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store_part(T* row, int64_t c, int64_t width, const float (&x)[W])
+{
+    if (c + W <= width) {
+        vec_t<T, W> v;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v[k] = static_cast<T>(x[k]);
+        store_vec<T, W>(row + c, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            if (c + k < width) row[c + k] = static_cast<T>(x[k]);
+    }
+}
+
+// ------------------------------------------------------------------ forward
+
+// NW waves a row, K vectors a lane; with NW == 1 a workgroup has 4 rows.
+template <typename T, typename A, int NW, int K>
+__global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void forward_kernel(NormForward a)
+{
+    constexpr int W = Vec<T>::W;
+    __shared__ float2 sh[NW];
+    const int lane = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = NW == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (row >= a.rows) return;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    float v[K][W];
+    float s = 0.0f, unused = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_part<T, W>(x, (int64_t)(k * NW * 64 + lane) * W, a.width, v[k]);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < W; ++e) s += v[k][e];
+    row_sum<NW>(s, unused, sh);
+    const float mean = s / (float)a.width;
+    float q = 0.0f;
+    unused = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            v[k][e] = c + e < a.width ? v[k][e] - mean : 0.0f;
+            q += v[k][e] * v[k][e];
+        }
+    }
+    row_sum<NW>(q, unused, sh);
+    const float rstd = 1.0f / sqrtf(q / (float)a.width + a.eps);
+    if (lane == 0) {
+        if (a.mean != nullptr) a.mean[row] = mean;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    T* y = static_cast<T*>(a.y) + row * a.y_stride;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
+        if (c >= a.width) continue;
+        float w[W], b[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            w[e] = 1.0f;
+            b[e] = 0.0f;
+        }
+        if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
+        if (a.bias != nullptr) load_part<A, W>(static_cast<const A*>(a.bias), c, a.width, b);
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = v[k][e] * rstd * w[e] + b[e];
+        store_part<T, W>(y, c, a.width, w);
+    }
+}
+
+// Rows too long for registers: 16 waves walk the row three times.
+template <typename T, typename A>
+__global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
+{
+    constexpr int W = Vec<T>::W;
+    __shared__ float2 sh[16];
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    T* y = static_cast<T*>(a.y) + row * a.y_stride;
+    const int64_t c0 = (int64_t)threadIdx.x * W, step = 1024 * W;
+    float s = 0.0f, q = 0.0f, unused = 0.0f;
+    for (int64_t c = c0; c < a.width; c += step) {
+        float v[W];
+        load_part<T, W>(x, c, a.width, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) s += v[e];
+    }
+    row_sum<16>(s, unused, sh);
+    const float mean = s / (float)a.width;
+    for (int64_t c = c0; c < a.width; c += step) {
+        float v[W];
+        load_part<T, W>(x, c, a.width, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (c + e < a.width) q += (v[e] - mean) * (v[e] - mean);
+    }
+    unused = 0.0f;
+    row_sum<16>(q, unused, sh);
+    const float rstd = 1.0f / sqrtf(q / (float)a.width + a.eps);
+    if (threadIdx.x == 0) {
+        if (a.mean != nullptr) a.mean[row] = mean;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    for (int64_t c = c0; c < a.width; c += step) {
+        float v[W], w[W], b[W];
+        load_part<T, W>(x, c, a.width, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            w[e] = 1.0f;
+            b[e] = 0.0f;
+        }
+        if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
+        if (a.bias != nullptr) load_part<A, W>(static_cast<const A*>(a.bias), c, a.width, b);
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = (v[e] - mean) * rstd * w[e] + b[e];
+        store_part<T, W>(y, c, a.width, w);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+
+// A workgroup of WAVES waves, NW to a row, walks rows blockIdx, blockIdx + grid,
+// ... (in groups of WAVES / NW) and keeps its sums for dw and db.
+template <typename T, typename A, int NW, int WAVES, int K>
+__global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
+{
+    constexpr int W = Vec<T>::W;
+    constexpr int ROWS = WAVES / NW;
+    static_assert(ROWS == 1 || NW == 1, "several rows a workgroup: a wave each");
+    __shared__ float2 sh[NW];
+    extern __shared__ float fold[];            // ROWS > 1: [2][K * 64 * W]
+    const int lane = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
+    const int wave = threadIdx.x >> 6;
+    const float inv = 1.0f / (float)a.width;
+    float w[K][W], dw[K][W], db[K][W];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            w[k][e] = 1.0f;
+            dw[k][e] = db[k][e] = 0.0f;
+        }
+        if (a.weight != nullptr)
+            load_part<A, W>(static_cast<const A*>(a.weight), (int64_t)(k * NW * 64 + lane) * W, a.width, w[k]);
+    }
+    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.rows; first += (int64_t)gridDim.x * ROWS) {
+        const int64_t row = NW == 1 ? first + wave : first;
+        if (row >= a.rows) break;              // (only with NW == 1: no barrier is missed)
+        const T* xr = static_cast<const T*>(a.x) + row * a.x_stride;
+        const T* dyr = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        float x[K][W], g[K][W];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
+            load_part<T, W>(xr, c, a.width, x[k]);
+            load_part<T, W>(dyr, c, a.width, g[k]);
+        }
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                // (past the width g is 0, and dw, db stay out of the result)
+                x[k][e] = (x[k][e] - mean) * rstd;
+                dw[k][e] += g[k][e] * x[k][e];
+                db[k][e] += g[k][e];
+                g[k][e] *= w[k][e];
+                sg += g[k][e];
+                sgx += g[k][e] * x[k][e];
+            }
+        row_sum<NW>(sg, sgx, sh);
+        sg *= inv;
+        sgx *= inv;
+        T* dxr = static_cast<T*>(a.dx) + row * a.dx_stride;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
+            if (c >= a.width) continue;
+#pragma unroll
+            for (int e = 0; e < W; ++e) g[k][e] = rstd * (g[k][e] - sg - x[k][e] * sgx);
+            store_part<T, W>(dxr, c, a.width, g[k]);
+        }
+    }
+    if (a.partial == nullptr) return;
+    float* out = a.partial + (int64_t)blockIdx.x * 2 * a.width;
+    if constexpr (ROWS > 1) {
+        // the waves' sums, one wave after the other
+        for (int turn = 0; turn < ROWS; ++turn) {
+            if (wave == turn) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        const int at = (k * W + e) * 64 + lane;
+                        if (turn > 0) {
+                            dw[k][e] += fold[at];
+                            db[k][e] += fold[K * W * 64 + at];
+                        }
+                        fold[at] = dw[k][e];
+                        fold[K * W * 64 + at] = db[k][e];
+                    }
+            }
+            __syncthreads();
+        }
+        if (wave != ROWS - 1) return;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
+        if (c >= a.width) continue;
+        store_part<float, W>(out, c, a.width, dw[k]);
+        store_part<float, W>(out + a.width, c, a.width, db[k]);
+    }
+}
+
+// Rows too long for registers: dx row by row, and the sums for dw and db over
+// slabs of rows, a lane W columns.
+template <typename T, typename A>
+__global__ __launch_bounds__(1024) void backward_long_kernel(NormBackward a)
+{
+    constexpr int W = Vec<T>::W;
+    __shared__ float2 sh[16];
+    const int64_t row = blockIdx.x;
+    const T* xr = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* dyr = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    T* dxr = static_cast<T*>(a.dx) + row * a.dx_stride;
+    const float mean = a.mean[row], rstd = a.rstd[row], inv = 1.0f / (float)a.width;
+    const int64_t c0 = (int64_t)threadIdx.x * W, step = 1024 * W;
+    float sg = 0.0f, sgx = 0.0f;
+    for (int turn = 0; turn < 2; ++turn) {
+        for (int64_t c = c0; c < a.width; c += step) {
+            float x[W], g[W], w[W];
+            load_part<T, W>(xr, c, a.width, x);
+            load_part<T, W>(dyr, c, a.width, g);
+            if (a.weight != nullptr) {
+                load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
+#pragma unroll
+                for (int e = 0; e < W; ++e) g[e] *= w[e];
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float xhat = (x[e] - mean) * rstd;
+                if (turn == 0) {
+                    sg += g[e];
+                    sgx += g[e] * xhat;
+                } else {
+                    g[e] = rstd * (g[e] - sg - xhat * sgx);
+                }
+            }
+            if (turn == 1) store_part<T, W>(dxr, c, a.width, g);
+        }
+        if (turn == 0) {
+            row_sum<16>(sg, sgx, sh);
+            sg *= inv;
+            sgx *= inv;
+        }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void columns_long_kernel(NormBackward a, int64_t slab)
+{
+    constexpr int W = Vec<T>::W;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W;
+    if (c >= a.width) return;
+    float dw[W], db[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) dw[e] = db[e] = 0.0f;
+    const int64_t r0 = blockIdx.y * slab, r1 = r0 + slab < a.rows ? r0 + slab : a.rows;
+    for (int64_t row = r0; row < r1; ++row) {
+        float x[W], g[W];
+        load_part<T, W>(static_cast<const T*>(a.x) + row * a.x_stride, c, a.width, x);
+        load_part<T, W>(static_cast<const T*>(a.dy) + row * a.dy_stride, c, a.width, g);
+        const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            dw[e] += g[e] * ((x[e] - mean) * rstd);
+            db[e] += g[e];
+        }
+    }
+    float* out = a.partial + (int64_t)blockIdx.y * 2 * a.width;
+    store_part<float, W>(out, c, a.width, dw);
+    store_part<float, W>(out + a.width, c, a.width, db);
+}
+
+// dw and db: the partial rows, added in 16 runs by 16 waves, the runs in order.
+template <typename A>
+__global__ __launch_bounds__(1024) void fold_kernel(const float* partial, int64_t parts, int64_t width,
+                                                    A* dweight, A* dbias)
+{
+    __shared__ float sh[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;       // of 2 * width columns
+    const int64_t p0 = parts * wave / 16, p1 = parts * (wave + 1) / 16;
+    float s = 0.0f;
+    if (c < 2 * width)
+        for (int64_t p = p0; p < p1; ++p) s += partial[p * 2 * width + c];
+    sh[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= 2 * width) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += sh[k][lane];
+    if (c < width) {
+        if (dweight != nullptr) dweight[c] = static_cast<A>(s);
+    } else if (dbias != nullptr) {
+        dbias[c - width] = static_cast<A>(s);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+
+constexpr int kBackwardWaves = 8;      // rows of a workgroup where a row is a wave's
+constexpr int64_t kLongRows = 64;      // workgroups over the rows of very long ones
+
+template <typename T, typename A>
+hipError_t forward(const NormForward& a, hipStream_t s)
+{
+    constexpr int W = Vec<T>::W;
+    if (a.rows == 0) return hipSuccess;
+    const int64_t lanes = ceil_div(a.width, W);
+    const dim3 by4((unsigned)ceil_div(a.rows, 4)), by1((unsigned)a.rows);
+    if (lanes <= 64) forward_kernel<T, A, 1, 1><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 128) forward_kernel<T, A, 1, 2><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 256) forward_kernel<T, A, 1, 4><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 512) forward_kernel<T, A, 4, 2><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 1024) forward_kernel<T, A, 4, 4><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 2048) forward_kernel<T, A, 16, 2><<<by1, 1024, 0, s>>>(a);
+    else forward_long_kernel<T, A><<<by1, 1024, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, typename A>
+hipError_t backward(const NormBackward& a, hipStream_t s)
+{
+    constexpr int W = Vec<T>::W;
+    const int64_t lanes = ceil_div(a.width, W);
+    int64_t parts = 0;
+    if (a.rows > 0) {
+        auto run = [&](auto kernel, int waves, int rows, int k) {
+            parts = ceil_div(a.rows, rows);
+            if (parts > kCUs) parts = kCUs;
+            const size_t lds = rows > 1 ? (size_t)2 * k * W * 64 * sizeof(float) : 0;
+            kernel<<<dim3((unsigned)parts), waves * 64, lds, s>>>(a);
+        };
+        constexpr int B = kBackwardWaves;
+        if (lanes <= 64) run(backward_kernel<T, A, 1, B, 1>, B, B, 1);
+        else if (lanes <= 128) run(backward_kernel<T, A, 1, B, 2>, B, B, 2);
+        else if (lanes <= 256) run(backward_kernel<T, A, 1, B, 4>, B, B, 4);
+        else if (lanes <= 512) run(backward_kernel<T, A, 8, 8, 1>, 8, 1, 1);
+        else if (lanes <= 1024) run(backward_kernel<T, A, 16, 16, 1>, 16, 1, 1);
+        else if (lanes <= 2048) run(backward_kernel<T, A, 16, 16, 2>, 16, 1, 2);
+        else {
+            backward_long_kernel<T, A><<<dim3((unsigned)a.rows), 1024, 0, s>>>(a);
+            parts = a.rows < kLongRows ? a.rows : kLongRows;
+            const int64_t slab = ceil_div(a.rows, parts);
+            parts = ceil_div(a.rows, slab);
+            if (a.partial != nullptr)
+                columns_long_kernel<T><<<dim3((unsigned)ceil_div(lanes, 256), (unsigned)parts), 256, 0, s>>>(a, slab);
+        }
+    }
+    if (a.partial != nullptr)
+        fold_kernel<A><<<dim3((unsigned)ceil_div(2 * a.width, 64)), 1024, 0, s>>>(
+            a.partial, parts, a.width, static_cast<A*>(a.dweight), static_cast<A*>(a.dbias));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_partial_rows(int64_t rows, int64_t) { return rows < kCUs ? (rows < 1 ? 1 : rows) : kCUs; }
+
+hipError_t norm_forward(const NormForward& a, int type, int affine, hipStream_t s)
+{
+    switch (type * 4 + affine) {
+    case 1 * 4 + 1: return forward<_Float16, _Float16>(a, s);
+    case 1 * 4 + 3: return forward<_Float16, float>(a, s);
+    case 2 * 4 + 2: return forward<__bf16, __bf16>(a, s);
+    case 2 * 4 + 3: return forward<__bf16, float>(a, s);
+    default: return forward<float, float>(a, s);
+    }
+}
+
+hipError_t norm_backward(const NormBackward& a, int type, int affine, hipStream_t s)
+{
+    switch (type * 4 + affine) {
+    case 1 * 4 + 1: return backward<_Float16, _Float16>(a, s);
+    case 1 * 4 + 3: return backward<_Float16, float>(a, s);
+    case 2 * 4 + 2: return backward<__bf16, __bf16>(a, s);
+    case 2 * 4 + 3: return backward<__bf16, float>(a, s);
+    default: return backward<float, float>(a, s);
+    }
+}
+
+}  // namespace zo
