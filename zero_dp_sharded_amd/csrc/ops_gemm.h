@@ -32,6 +32,7 @@ constexpr int kGemmThreads = 512;
 constexpr int kWaveI = 128, kWaveJ = 64;
 constexpr int kOperandBytes = kTile * kDeep * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kLgkmDone = 0xc07f;                // s_waitcnt lgkmcnt(0) alone
 constexpr uint32_t kOutOfRange = 0x7ffffff0u;    // a byte offset past every descriptor's end
 
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -211,32 +212,53 @@ __device__ __forceinline__ void gemm_tile(const Operand& P, const Operand& Q, in
     for (int ti = 0; ti < 8; ++ti)
 #pragma unroll
         for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
-    if (steps > 0) {
-        lp.issue(smem, wave);
-        lq.issue(smem + kOperandBytes, wave);
+    if (steps <= 0) return;
+    // Fragments of half a step (32 of k) are read while the half before is
+    // multiplied; the barrier of a step stands between its two halves, where the
+    // other half's fragments are on hand to go on with.
+    s8 a0[4], b0[8], a1[4], b1[8];
+    lp.issue(smem, wave);
+    lq.issue(smem + kOperandBytes, wave);
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (steps > 1) {
+        lp.issue(smem + kStageBytes, wave);
+        lq.issue(smem + kStageBytes + kOperandBytes, wave);
     }
+#pragma unroll
+    for (int tj = 0; tj < 4; ++tj) a0[tj] = rq.get(0, tj, 0);
+#pragma unroll
+    for (int ti = 0; ti < 8; ++ti) b0[ti] = rp.get(0, ti, 0);
     for (int s = 0; s < steps; ++s) {
-        // this step's loads have arrived, for every wave; and every wave has what it
-        // read of the other stage
+        const uint32_t stage = (s & 1) ? kStageBytes : 0, other = kStageBytes - stage;
+#pragma unroll
+        for (int tj = 0; tj < 4; ++tj) a1[tj] = rq.get(stage, tj, 1);
+#pragma unroll
+        for (int ti = 0; ti < 8; ++ti) b1[ti] = rp.get(stage, ti, 1);
+#pragma unroll
+        for (int ti = 0; ti < 8; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = Mfma<T>::run(a0[tj], b0[ti], acc[ti][tj]);
+        // the next step's loads have arrived, for every wave; and every wave has all
+        // that it reads of this stage (the products above stay above: they are what
+        // the reads hide behind)
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(kLgkmDone);    // (the builtin: the compiler counts on it)
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const uint32_t stage = (s & 1) ? kStageBytes : 0;
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 2 < steps) {
+            lp.issue(smem + stage, wave);
+            lq.issue(smem + stage + kOperandBytes, wave);
+        }
         if (s + 1 < steps) {
-            const uint32_t next = smem + (kStageBytes - stage);
-            lp.issue(next, wave);
-            lq.issue(next + kOperandBytes, wave);
+#pragma unroll
+            for (int tj = 0; tj < 4; ++tj) a0[tj] = rq.get(other, tj, 0);
+#pragma unroll
+            for (int ti = 0; ti < 8; ++ti) b0[ti] = rp.get(other, ti, 0);
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            s8 a[4], b[8];
+        for (int ti = 0; ti < 8; ++ti)
 #pragma unroll
-            for (int tj = 0; tj < 4; ++tj) a[tj] = rq.get(stage, tj, kk);
-#pragma unroll
-            for (int ti = 0; ti < 8; ++ti) b[ti] = rp.get(stage, ti, kk);
-#pragma unroll
-            for (int ti = 0; ti < 8; ++ti)
-#pragma unroll
-                for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = Mfma<T>::run(a[tj], b[ti], acc[ti][tj]);
-        }
+            for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = Mfma<T>::run(a1[tj], b1[ti], acc[ti][tj]);
     }
 }
 
