@@ -1,12 +1,18 @@
 // One tile of C[i][j] = sum_k P(i,k) Q(j,k) with 2-byte operands and fp32 sums, for
 // the three products of the vocabulary loss.
 //
-// A workgroup of 8 waves takes 256 x 256 results, 64 deep at a time: both
-// operands' 256 x 64 pieces (32 KiB each) go from memory straight to LDS, double
-// buffered (128 of the CU's 160 KiB), and each wave keeps 128 x 64 results in
-// registers as 8 x 4 products of 16 x 16 x 32.  A step of 64 is 2048 cycles of
-// the matrix cores for the CU's two waves per SIMD, against about 1536 cycles of
-// LDS reads and 64 KiB of loads, which have the whole step to arrive.
+// A workgroup of 8 waves (2 by 4) takes 32 NI x 64 NJ results, 64 deep at a time:
+// both operands' pieces go from memory straight to LDS, double buffered, and each
+// wave keeps 16 NI x 16 NJ results in registers, as products of 16 x 16 x 32.
+//
+// What bounds it, for NI x NJ = 8 x 4 (256 x 256), from parts timed apart on 8192 x
+// 8192 x 8192: the products alone take 615 us (1790 TFLOP/s, at the power limit), the
+// LDS reads 320, the loads 690 (12.5 TB/s out of the L2s), all together 826.  So the
+// larger tile, 256 x 320, which loads a tenth less for each product, is taken where
+// it wastes no more at the edges; NI = 2 serves few rows, with room for more
+// workgroups in a CU.  Loads are started right behind the barrier, all of them (spread
+// among the products they arrive later: 10% slower), and never less than 64 deep
+// (pieces of 64 bytes a row: 10% slower, even with four steps under way).
 //
 // An operand lies in memory either with k contiguous (kInner: row i has its k
 // side by side) or with k as its rows (kOuter).  Both are loaded as 16-byte
@@ -16,8 +22,7 @@
 //
 // LDS banks: the chunk that a lane fetches is chosen so that chunk c of a row is
 // kept at place c ^ key(row); the keys make the rows that one read touches lie in
-// different banks (kInner: the 8 rows that read together; kOuter: the 4 or 8
-// rows of k).
+// different banks.
 #pragma once
 
 #include "ops_common.h"
@@ -26,12 +31,8 @@ namespace zo {
 
 enum Layout { kInner = 0, kOuter = 1 };
 
-constexpr int kTile = 256;      // results of a workgroup each way
 constexpr int kDeep = 64;       // k of one step
 constexpr int kGemmThreads = 512;
-constexpr int kWaveI = 128, kWaveJ = 64;
-constexpr int kOperandBytes = kTile * kDeep * 2;
-constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kLgkmDone = 0xc07f;                // s_waitcnt lgkmcnt(0) alone
 constexpr uint32_t kOutOfRange = 0x7ffffff0u;    // a byte offset past every descriptor's end
 
@@ -63,7 +64,7 @@ template <> struct Mfma<_Float16> {
 // Where an operand lies: `rows` i (or j) by `depth` k, 2-byte elements.  kInner:
 // element (i, k) at i * ld + k, `depth` a multiple of 8.  kOuter: at k * ld + i,
 // `rows` a multiple of 8.  Base 16-byte aligned, ld a multiple of 8,
-// ld <= 2^21 (an offset inside a tile stays below 2^30 bytes).
+// ld <= 2^21 (an offset inside a tile stays below 2^31 - 16 bytes).
 struct Operand {
     const void* base;
     int64_t ld;
@@ -71,65 +72,15 @@ struct Operand {
     int64_t depth;
 };
 
-// Loads of one operand: the wave's 4 of the 32 instructions of 1 KiB that fill a
-// stage.  PERMUTED marks the operand whose 16-row products interleave (below).
-template <Layout L, bool PERMUTED>
-struct Loader {
-    const char* base;        // of this tile at the current k
+// The piece of an operand that a tile reads, as it moves along k.
+struct Piece {
+    const char* base;        // at the current k
     int64_t left;            // bytes from base to the operand's end
     int64_t step;            // bytes from one step to the next
-    uint32_t voff[4];
-    int chunk_k[4];          // kInner: first k of the lane's chunk within the step
-    int64_t k_left;          // kInner: k left from the current step on
 
-    // the swizzle of a row's 8 chunks (kInner)
-    static __device__ __forceinline__ int key_inner(int row)
+    __device__ __forceinline__ u4 descriptor() const
     {
-        return PERMUTED ? (row & 3) | ((row >> 4) & 1) << 2 : row & 7;
-    }
-    // the swizzle of a k row's 32 chunks (kOuter)
-    static __device__ __forceinline__ int key_outer(int k)
-    {
-        return 2 * ((k & 3) | ((k >> 3) & 1) << 2);
-    }
-
-    __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k0, int wave, int lane)
-    {
-        if constexpr (L == kInner) {
-            base = static_cast<const char*>(o.base) + (row0 * o.ld + k0) * 2;
-            int64_t rows = o.rows - row0;
-            rows = rows < kTile ? rows : kTile;
-            left = ((rows - 1) * o.ld + o.depth - k0) * 2;
-            step = kDeep * 2;
-            k_left = o.depth - k0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = wave * 32 + q * 8 + (lane >> 3);
-                const int chunk = (lane & 7) ^ key_inner(row);
-                chunk_k[q] = chunk * 8;
-                voff[q] = (uint32_t)((row * o.ld + chunk * 8) * 2);
-            }
-        } else {
-            base = static_cast<const char*>(o.base) + (k0 * o.ld + row0) * 2;
-            left = ((o.depth - k0 - 1) * o.ld + o.rows - row0) * 2;
-            step = kDeep * o.ld * 2;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k = wave * 8 + q * 2 + (lane >> 5);
-                const int chunk = (lane & 31) ^ key_outer(k);
-                voff[q] = (uint32_t)((k * o.ld + chunk * 8) * 2);
-            }
-        }
-    }
-
-    // Start the loads of the current step into the operand's stage at LDS byte
-    // address `lds`, and move on.  They are done when the wave's vmcnt says so.
-    // Written as assembly because the builtin makes the compiler wait for every
-    // such load before the next LDS read, also of the other stage; there is no
-    // output register that could be reused too early.
-    __device__ __forceinline__ void issue(uint32_t lds, int wave)
-    {
-        const int64_t reach = 0x40000000;    // no offset inside a tile is larger
+        const int64_t reach = 0x7fffff00;    // no offset inside a tile is larger
         const uint32_t range = left <= 0 ? 0u : (uint32_t)(left < reach ? left : reach);
         const uint64_t b = (uint64_t)base;
         u4 rsrc;
@@ -137,129 +88,320 @@ struct Loader {
         rsrc[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xffffu);
         rsrc[2] = __builtin_amdgcn_readfirstlane(range);
         rsrc[3] = 0x00020000u;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t v = voff[q];
-            if constexpr (L == kInner)
-                if (chunk_k[q] >= k_left) v = kOutOfRange;
-            const uint32_t m = __builtin_amdgcn_readfirstlane(lds + (wave * 4 + q) * 1024);
-            asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                         :
-                         : "s"(m), "v"(v), "s"(rsrc));
-        }
+        return rsrc;
+    }
+    __device__ __forceinline__ void advance()
+    {
         base += step;
         left -= step;
-        if constexpr (L == kInner) k_left -= kDeep;
     }
 };
 
-// Fragments for one product of 16 x 16 x 32: lane l has row l % 16 and the 8 k from
-// (l / 16) * 8.  A wave's part begins at row `w0` of the tile; product t of it
-// takes rows w0 + 16 t + r, or with PERMUTED (t < 4) rows w0 + (r / 4) * 16 + 4 t + r % 4:
-// then the four products give each lane 16 results side by side.
-template <Layout L, bool PERMUTED>
-struct Reader {
-    uint32_t addr;       // kInner: of (t = 0, kk = 0); kOuter: before ^ (t << 5)
+// One load of 1 KiB into LDS at byte address `lds`: the lane's 16 bytes at offset v.
+// It is done when the wave's vmcnt says so.  Written as assembly because the
+// builtin makes the compiler wait for every such load before the next LDS read, also of
+// the other stage; there is no output register that could be reused too early.
+__device__ __forceinline__ void load_to_lds(uint32_t v, const u4& rsrc, uint32_t lds)
+{
+    const uint32_t m = __builtin_amdgcn_readfirstlane(lds);
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(m), "v"(v), "s"(rsrc));
+}
 
-    __device__ __forceinline__ void init(uint32_t operand, int w0, int lane)
+// kInner operand of 64 C rows: rows of 64 k (128 bytes) in LDS, 8 chunks each; a wave
+// loads C times 8 rows.  C is 1 (64 rows), 4 or 5.
+//
+// Fragments: lane l has row l % 16 and the 8 k from (l / 16) * 8.  Product t of a wave
+// takes rows w0 + 16 t + r; with RUNS products 0 to 3 take rows w0 + 16 (r / 4) + 4 t + r % 4
+// of the first 256 (then the four give each lane 16 results side by side), and with C = 5
+// product 4 takes 16 of the last 64.
+template <int C, bool RUNS>
+struct Inner {
+    static constexpr int kBytes = C * 64 * kDeep * 2;
+    Piece piece;
+    int64_t k_left;
+    uint32_t voff, voff_last, apart;
+    int chunk_k, chunk_k_last;
+    uint32_t addr, addr_last;
+
+    // Rows that one read takes together: r, r + 1, ... r + 7; with runs {0..3, 16..19} + 4 t.
+    static __device__ __forceinline__ int key(int row, bool runs)
+    {
+        return runs ? (row & 3) | ((row >> 4) & 1) << 2 : row & 7;
+    }
+    __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k0, int wave, int lane)
+    {
+        piece.base = static_cast<const char*>(o.base) + (row0 * o.ld + k0) * 2;
+        int64_t rows = o.rows - row0;
+        rows = rows < C * 64 ? rows : C * 64;
+        piece.left = ((rows - 1) * o.ld + o.depth - k0) * 2;
+        piece.step = kDeep * 2;
+        k_left = o.depth - k0;
+        // load q of wave w: rows 64 q + 8 w to + 7, with the key of row 8 w + ...
+        const int row = wave * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ key(row, RUNS);
+        chunk_k = chunk * 8;
+        voff = (uint32_t)((row * o.ld + chunk * 8) * 2);
+        if constexpr (C == 5 && RUNS) {
+            const int last = (lane & 7) ^ key(row, false);
+            chunk_k_last = last * 8;
+            voff_last = (uint32_t)(((256 + row) * o.ld + last * 8) * 2);
+        }
+        apart = (uint32_t)(64 * o.ld * 2);
+    }
+    __device__ __forceinline__ void issue(uint32_t lds, int wave)
+    {
+        const u4 rsrc = piece.descriptor();
+#pragma unroll
+        for (int q = 0; q < C; ++q) {
+            uint32_t v = chunk_k >= k_left ? kOutOfRange : voff + q * apart;
+            if constexpr (C == 5 && RUNS)
+                if (q == 4) v = chunk_k_last >= k_left ? kOutOfRange : voff_last;
+            load_to_lds(v, rsrc, lds + (q * 8 + wave) * 1024);
+        }
+        piece.advance();
+        k_left -= kDeep;
+    }
+    // w: which of the waves along this side
+    __device__ __forceinline__ void reader(uint32_t lds, int w, int products, int lane)
     {
         const int r = lane & 15, g = lane >> 4;
-        if constexpr (L == kInner) {
-            const int row = w0 + (PERMUTED ? (r >> 2) * 16 + (r & 3) : r);
-            addr = operand + row * 128 + ((g ^ Loader<L, PERMUTED>::key_inner(row)) << 4);
-        } else {
-            const int k = g * 8 + (r >> 2);
-            const int chunk = (w0 >> 3) | ((r & 3) >> 1);
-            addr = operand + k * 512 + ((chunk ^ Loader<L, PERMUTED>::key_outer(k)) << 4) + (r & 1) * 8;
+        const int row = RUNS ? w * 64 + (r >> 2) * 16 + (r & 3) : w * 16 * products + r;
+        addr = lds + row * 128 + ((g ^ key(row, RUNS)) << 4);
+        if constexpr (C == 5 && RUNS) {
+            const int last = 256 + w * 16 + r;
+            addr_last = lds + last * 128 + ((g ^ key(last, false)) << 4);
         }
     }
-
     __device__ __forceinline__ s8 get(uint32_t stage, int t, int kk) const
     {
-        if constexpr (L == kInner) {
-            // product t is 16 (PERMUTED: 4) rows further on; the other half of the
-            // step's k is chunk ^ 4
-            const uint32_t a = ((addr ^ (kk << 6)) + stage) + t * (PERMUTED ? 512 : 2048);
-            return *(ZO_LDS const s8*)(uintptr_t)a;
-        } else {
-            const uint32_t a = ((addr ^ (t << 5)) + stage) + kk * 16384;
-            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)a);
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)(a + 2048));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
+        // (the other half of the step's k is chunk ^ 4)
+        uint32_t a = ((addr ^ (kk << 6)) + stage) + t * (RUNS ? 512 : 2048);
+        if constexpr (C == 5 && RUNS)
+            if (t == 4) a = (addr_last ^ (kk << 6)) + stage;
+        return *(ZO_LDS const s8*)(uintptr_t)a;
     }
 };
 
-// acc[ti][tj][e]: result i = wave's i0 + 16 ti + lane % 16, and j = wave's j0 +
-// 16 tj + 4 (lane / 16) + e, or with the permuted kInner Q j0 + 16 (lane / 16) + 4 tj + e.
-// `steps` of kDeep from k0 on.  smem: 2 * kStageBytes.
-template <typename T, Layout LP, Layout LQ>
-__device__ __forceinline__ void gemm_tile(const Operand& P, const Operand& Q, int64_t i0, int64_t j0,
-                                          int64_t k0, int steps, uint32_t smem, f4 (&acc)[8][4])
-{
-    constexpr bool PERM = LQ == kInner;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Loader<LP, false> lp;
-    Loader<LQ, PERM> lq;
-    lp.init(P, i0, k0, wave, lane);
-    lq.init(Q, j0, k0, wave, lane);
-    Reader<LP, false> rp;
-    Reader<LQ, PERM> rq;
-    rp.init(smem, (wave >> 2) * kWaveI, lane);
-    rq.init(smem + kOperandBytes, (wave & 3) * kWaveJ, lane);
-#pragma unroll
-    for (int ti = 0; ti < 8; ++ti)
-#pragma unroll
-        for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
-    if (steps <= 0) return;
-    // Fragments of half a step (32 of k) are read while the half before is
-    // multiplied; the barrier of a step stands between its two halves, where the
-    // other half's fragments are on hand to go on with.
-    s8 a0[4], b0[8], a1[4], b1[8];
-    lp.issue(smem, wave);
-    lq.issue(smem + kOperandBytes, wave);
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (steps > 1) {
-        lp.issue(smem + kStageBytes, wave);
-        lq.issue(smem + kStageBytes + kOperandBytes, wave);
+// 64 columns of a kOuter operand: 64 rows of k with 128 bytes each.
+struct Outer64 {
+    static constexpr int kBytes = 64 * kDeep * 2;
+    uint32_t voff, addr;
+
+    // 16 lanes read 4 rows of k, 32 lanes 8, 32 bytes of each: all in different banks
+    static __device__ __forceinline__ int key(int k) { return 2 * ((k & 3) ^ ((k >> 3) & 1)); }
+    __device__ __forceinline__ void init(int64_t ld, int64_t col0, int wave, int lane)
+    {
+        const int k = wave * 8 + (lane >> 3);
+        const int chunk = (lane & 7) ^ key(k);
+        voff = (uint32_t)((k * ld + col0 + chunk * 8) * 2);
     }
+    __device__ __forceinline__ void issue(const u4& rsrc, uint32_t lds, int wave)
+    {
+        load_to_lds(voff, rsrc, lds + wave * 1024);
+    }
+    __device__ __forceinline__ void reader(uint32_t lds, int w0, int lane)
+    {
+        const int r = lane & 15, g = lane >> 4, k = g * 8 + (r >> 2);
+        const int chunk = (w0 >> 3) | ((r & 3) >> 1);
+        addr = lds + k * 128 + ((chunk ^ key(k)) << 4) + (r & 1) * 8;
+    }
+    __device__ __forceinline__ s8 get(uint32_t stage, int t, int kk) const
+    {
+        const uint32_t a = ((addr ^ (t << 5)) + stage) + kk * 4096;
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)a);
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)(a + 512));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// 256 columns: 64 rows of k with 512 bytes each.
+struct Outer256 {
+    static constexpr int kBytes = 256 * kDeep * 2;
+    uint32_t voff[2], apart, addr;
+
+    static __device__ __forceinline__ int key(int k) { return 2 * ((k & 3) | ((k >> 3) & 1) << 2); }
+    __device__ __forceinline__ void init(int64_t ld, int wave, int lane)
+    {
+        // load q of wave w: rows 8 w + 2 q and + 1 of k; q and q + 2 have the same key
 #pragma unroll
-    for (int tj = 0; tj < 4; ++tj) a0[tj] = rq.get(0, tj, 0);
+        for (int q = 0; q < 2; ++q) {
+            const int k = wave * 8 + q * 2 + (lane >> 5);
+            const int chunk = (lane & 31) ^ key(k);
+            voff[q] = (uint32_t)((k * ld + chunk * 8) * 2);
+        }
+        apart = (uint32_t)(4 * ld * 2);
+    }
+    __device__ __forceinline__ void issue(const u4& rsrc, uint32_t lds, int wave)
+    {
 #pragma unroll
-    for (int ti = 0; ti < 8; ++ti) b0[ti] = rp.get(0, ti, 0);
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t stage = (s & 1) ? kStageBytes : 0, other = kStageBytes - stage;
+        for (int q = 0; q < 4; ++q)
+            load_to_lds(voff[q & 1] + (q >> 1) * apart, rsrc, lds + (wave * 4 + q) * 1024);
+    }
+    __device__ __forceinline__ void reader(uint32_t lds, int w0, int lane)
+    {
+        const int r = lane & 15, g = lane >> 4, k = g * 8 + (r >> 2);
+        const int chunk = (w0 >> 3) | ((r & 3) >> 1);
+        addr = lds + k * 512 + ((chunk ^ key(k)) << 4) + (r & 1) * 8;
+    }
+    __device__ __forceinline__ s8 get(uint32_t stage, int t, int kk) const
+    {
+        const uint32_t a = ((addr ^ (t << 5)) + stage) + kk * 16384;
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)a);
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)(a + 2048));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// kOuter operand of 64 C columns: 64, 256, or 256 and 64 beside them (C = 5).
+// Product t of a wave with W products: columns 16 (w W + t); with C = 5 products 0 to 3
+// lie in the 256 and product 4 in the 64, at 256 + 16 w.
+template <int C>
+struct Outer {
+    static_assert(C == 1 || C == 4 || C == 5, "");
+    static constexpr int kWide = C == 1 ? 0 : Outer256::kBytes;
+    static constexpr int kBytes = C * 64 * kDeep * 2;
+    Piece piece;
+    Outer256 wide;
+    Outer64 narrow;
+
+    __device__ __forceinline__ void init(const Operand& o, int64_t col0, int64_t k0, int wave, int lane)
+    {
+        piece.base = static_cast<const char*>(o.base) + (k0 * o.ld + col0) * 2;
+        piece.left = ((o.depth - k0 - 1) * o.ld + o.rows - col0) * 2;
+        piece.step = kDeep * o.ld * 2;
+        if constexpr (C >= 4) wide.init(o.ld, wave, lane);
+        if constexpr (C != 4) narrow.init(o.ld, C == 5 ? 256 : 0, wave, lane);
+    }
+    __device__ __forceinline__ void issue(uint32_t lds, int wave)
+    {
+        const u4 rsrc = piece.descriptor();
+        if constexpr (C >= 4) wide.issue(rsrc, lds, wave);
+        if constexpr (C != 4) narrow.issue(rsrc, lds + kWide, wave);
+        piece.advance();
+    }
+    __device__ __forceinline__ void reader(uint32_t lds, int w, int products, int lane)
+    {
+        if constexpr (C >= 4) wide.reader(lds, C == 5 ? w * 64 : w * 16 * products, lane);
+        if constexpr (C != 4) narrow.reader(lds + kWide, C == 5 ? w * 16 : w * 16 * products, lane);
+    }
+    __device__ __forceinline__ s8 get(uint32_t stage, int t, int kk) const
+    {
+        if constexpr (C == 1) return narrow.get(stage, t, kk);
+        else if constexpr (C == 5) return t == 4 ? narrow.get(stage, 0, kk) : wide.get(stage, t, kk);
+        else return wide.get(stage, t, kk);
+    }
+};
+
+template <Layout L, int C, bool RUNS> struct Side;
+template <int C, bool RUNS> struct Side<kInner, C, RUNS> { using type = Inner<C, RUNS>; };
+template <int C, bool RUNS> struct Side<kOuter, C, RUNS> { using type = Outer<C>; };
+
+// acc[ti][tj][e]: i = tile's i0 + 16 NI (wave / 4) + 16 ti + lane % 16; j by
+// column_of() below.  `steps` of kDeep from k0 on.
+template <typename T, Layout LP, Layout LQ, int NI, int NJ>
+struct Gemm {
+    static constexpr int kTileI = 32 * NI, kTileJ = 64 * NJ;
+    using PSide = typename Side<LP, NI / 2, false>::type;
+    using QSide = typename Side<LQ, NJ, LQ == kInner>::type;
+    static constexpr int kStageBytes = PSide::kBytes + QSide::kBytes;
+    static constexpr int kLds = 2 * kStageBytes;
+    // Both halves' fragments beside the results, where 256 registers hold them.  (8 x 4:
+    // 3% faster with P kInner; with both kOuter 1% slower.)
+    static constexpr bool kAhead = LP == kInner && NI * NJ * 4 + 8 * (NI + NJ) <= 224;
+
+    // First j of results acc[.][tj][0..3] of a lane, within the tile.
+    static __device__ __forceinline__ int column_of(int tj, int wave, int lane)
+    {
+        const int w = wave & 3, g = lane >> 4;
+        if (tj == 4) return 256 + w * 16 + g * 4;
+        return LQ == kInner ? w * 64 + g * 16 + tj * 4 : w * 64 + tj * 16 + g * 4;
+    }
+    static __device__ __forceinline__ int row_of(int ti, int wave, int lane)
+    {
+        return (wave >> 2) * 16 * NI + ti * 16 + (lane & 15);
+    }
+
+    struct Half {
+        s8 a[NJ], b[NI];
+    };
+    static __device__ __forceinline__ void read(Half& f, const PSide& p, const QSide& q, uint32_t stage, int kk)
+    {
 #pragma unroll
-        for (int tj = 0; tj < 4; ++tj) a1[tj] = rq.get(stage, tj, 1);
+        for (int tj = 0; tj < NJ; ++tj) f.a[tj] = q.get(stage, tj, kk);
 #pragma unroll
-        for (int ti = 0; ti < 8; ++ti) b1[ti] = rp.get(stage, ti, 1);
+        for (int ti = 0; ti < NI; ++ti) f.b[ti] = p.get(stage, ti, kk);
+    }
+    static __device__ __forceinline__ void multiply(const Half& f, f4 (&acc)[NI][NJ])
+    {
 #pragma unroll
-        for (int ti = 0; ti < 8; ++ti)
+        for (int ti = 0; ti < NI; ++ti)
 #pragma unroll
-            for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = Mfma<T>::run(a0[tj], b0[ti], acc[ti][tj]);
-        // the next step's loads have arrived, for every wave; and every wave has all
-        // that it reads of this stage (the products above stay above: they are what
-        // the reads hide behind)
+            for (int tj = 0; tj < NJ; ++tj) acc[ti][tj] = Mfma<T>::run(f.a[tj], f.b[ti], acc[ti][tj]);
+    }
+    // The next step's loads have arrived, for every wave; and every wave has all that it
+    // reads of this stage.  (What stands above stays above.)
+    static __device__ __forceinline__ void turn()
+    {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(kLgkmDone);    // (the builtin: the compiler counts on it)
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        if (s + 2 < steps) {
-            lp.issue(smem + stage, wave);
-            lq.issue(smem + stage + kOperandBytes, wave);
-        }
-        if (s + 1 < steps) {
-#pragma unroll
-            for (int tj = 0; tj < 4; ++tj) a0[tj] = rq.get(other, tj, 0);
-#pragma unroll
-            for (int ti = 0; ti < 8; ++ti) b0[ti] = rp.get(other, ti, 0);
-        }
-#pragma unroll
-        for (int ti = 0; ti < 8; ++ti)
-#pragma unroll
-            for (int tj = 0; tj < 4; ++tj) acc[ti][tj] = Mfma<T>::run(a1[tj], b1[ti], acc[ti][tj]);
     }
-}
+
+    // smem: LDS address, a multiple of 1024.
+    static __device__ __forceinline__ void run(const Operand& P, const Operand& Q, int64_t i0, int64_t j0,
+                                               int64_t k0, int steps, uint32_t smem, f4 (&acc)[NI][NJ])
+    {
+        const int lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        PSide p;
+        QSide q;
+        p.init(P, i0, k0, wave, lane);
+        q.init(Q, j0, k0, wave, lane);
+        p.reader(smem, wave >> 2, NI, lane);
+        q.reader(smem + PSide::kBytes, wave & 3, NJ, lane);
+#pragma unroll
+        for (int ti = 0; ti < NI; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < NJ; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
+        if (steps <= 0) return;
+        auto issue = [&](uint32_t stage) {
+            p.issue(smem + stage, wave);
+            q.issue(smem + stage + PSide::kBytes, wave);
+        };
+        Half even;
+        issue(0);
+        turn();
+        if (steps > 1) issue(kStageBytes);
+        if constexpr (kAhead) {
+            // Fragments of half a step are read while the half before is multiplied; the
+            // step's barrier stands between its halves, where the other half's
+            // fragments are on hand to go on with.
+            Half odd;
+            read(even, p, q, 0, 0);
+            for (int s = 0; s < steps; ++s) {
+                const uint32_t stage = (s & 1) ? kStageBytes : 0, other = kStageBytes - stage;
+                read(odd, p, q, stage, 1);
+                multiply(even, acc);
+                turn();
+                if (s + 2 < steps) issue(stage);
+                if (s + 1 < steps) read(even, p, q, other, 0);
+                multiply(odd, acc);
+            }
+        } else {
+            for (int s = 0; s < steps; ++s) {
+                const uint32_t stage = (s & 1) ? kStageBytes : 0;
+                read(even, p, q, stage, 0);
+                multiply(even, acc);
+                read(even, p, q, stage, 1);
+                turn();
+                if (s + 2 < steps) issue(stage);
+                multiply(even, acc);
+            }
+        }
+    }
+};
 
 }  // namespace zo

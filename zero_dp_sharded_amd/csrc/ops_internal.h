@@ -41,12 +41,17 @@ hipError_t norm_backward(const NormBackward& a, int type, int affine, hipStream_
 
 // ------------------------------------------------------------------ vocabulary loss
 
+struct TileChoice {            // of the products: 32 ni x 64 nj results a workgroup
+    int ni, nj;
+};
+
 struct LossPlan {              // what a call's sizes settle
     int64_t tokens, vocab, width;
     int64_t chunk;             // tokens whose exponentials are held at once
     int64_t vocab_ld;          // their row stride
-    int64_t pieces;            // statistics of 64 ids each
-    int64_t width_ld;          // row stride of repacked operands
+    int64_t pieces;            // of a token's ids, with statistics each
+    int64_t width_ld;          // the width in whole chunks of 8
+    TileChoice logits_tile, hidden_tile, weight_tile;
     int splits;                // parts of the vocabulary of the hidden states' gradient
     // byte offsets into the workspace
     int64_t off_alpha, off_target, off_lse, off_stats, off_exp, off_split, off_sum, off_hidden, off_weight;

@@ -6,21 +6,22 @@
 // for the tokens that count (target != ignore_index); the others have loss 0 and a
 // row of zeros in G.
 //
-// The logits never reach memory.  The first product's epilogue takes each 64 ids
-// of a token (a piece) to their maximum m and the sum of exp(z - m), both in fp32,
-// and, where gradients are wanted, leaves exp(z - m) in the 2-byte type.  When every
-// piece is done, a token's pieces join to its lse, and one pass multiplies each
-// piece by exp(m - lse): those are the probabilities.  So the gradients cost
-// three matrix products in all (6 tokens vocab width operations); computing the
-// logits again would make it four.  The exponentials of a chunk of tokens, 2 bytes
-// each, are what is held: 0.8 GB at 8192 tokens and 50257 ids, of 288.
+// The logits never reach memory.  The first product's epilogue takes each piece of a
+// token (64 or 80 ids) to its maximum m and the sum of exp(z - m), both fp32, and, where
+// gradients are wanted, leaves exp(z - m) in the 2-byte type.  A second kernel joins
+// a token's pieces to lse and multiplies them by exp(m - lse), in place.  So the
+// gradients cost three matrix products in all (6 tokens vocab width operations);
+// computing the logits again would make it four.  What is held are the exponentials of a
+// chunk of tokens, 2 bytes each: 0.8 GB at 8192 tokens and 50257 ids, of 288; the
+// pass over them takes 300 us of 4100.  (bf16 could do without the pass, by
+// exponentials without a maximum and the factors exp(-lse) in the second product's
+// epilogue and in a copy of H; that took 7% less, and the copy's rounding made the
+// weight's gradient 1.7 times less exact.)
 //
-// Rounding to 2 bytes twice (the exponential, then its product with exp(m - lse))
-// costs G a relative error of at most two half steps an entry, random in sign over
-// the sums that follow.  The target's entry, where p - 1 would cancel, is computed
-// from the fp32 logit as expm1(z - lse).  What is held is G times 2^15 (fp16) or 2^32
-// (bf16), taken back in the products' epilogues: entries down to 2^-29 and 2^-158
-// stay normal numbers.
+// An entry of G is rounded to 2 bytes twice (as exp, and by its factor).  The target's
+// entry, where p - 1 would cancel, is computed from the fp32 logit as expm1(z - lse).
+// What is held is G times 2^15 (fp16) or 2^32 (bf16), taken back in the products'
+// epilogues: entries far below the type's normal range stay.
 
 #include "ops_common.h"
 #include "ops_gemm.h"
@@ -29,29 +30,26 @@
 namespace zo {
 namespace {
 
-constexpr int kPiece = 64;
-constexpr int64_t kVocabPad = 64;
-
 constexpr float kLog2e = 1.44269504088896340736f;
-
 template <typename T> constexpr float kHoldLog2 = 32.0f;        // factor of what is held
 template <> constexpr float kHoldLog2<_Float16> = 15.0f;
 template <typename T> constexpr float kHold = (float)(1ull << (int)kHoldLog2<T>);
 
 // Workgroup -> tile.  Workgroups go round the 8 dies; each die gets a run of tiles
-// that lie together (kGroup tiles of i by all of j, column by column), so that its
-// L2 serves the operands' pieces to the tiles that share them.
-__device__ __forceinline__ void tile_of(int64_t id, int64_t ti, int64_t tj, int64_t& i, int64_t& j)
+// that lie together (8 tiles of i by all of j, column by column), so that its L2
+// serves the operands' pieces to the tiles that share them.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t ti, uint32_t tj, int64_t& i, int64_t& j)
 {
-    constexpr int64_t kDies = 8, kGroup = 8;
-    const int64_t all = ti * tj, die = id % kDies, at = id / kDies;
-    const int64_t q = all / kDies, r = all % kDies;
-    const int64_t n = die * q + (die < r ? die : r) + at;
-    const int64_t per = kGroup * tj, g = n / per;
-    const int64_t first = g * kGroup;
-    const int64_t high = ti - first < kGroup ? ti - first : kGroup;
-    i = first + (n - g * per) % high;
-    j = (n - g * per) / high;
+    constexpr uint32_t kDies = 8, kGroup = 8;
+    const uint32_t all = ti * tj, die = id % kDies, at = id / kDies;
+    const uint32_t q = all / kDies, r = all % kDies;
+    const uint32_t n = die * q + (die < r ? die : r) + at;
+    const uint32_t per = kGroup * tj, g = n / per;
+    const uint32_t first = g * kGroup;
+    const uint32_t high = ti - first < kGroup ? ti - first : kGroup;
+    // (the same for all lanes: kept where that costs no vector register)
+    i = __builtin_amdgcn_readfirstlane(first + (n - g * per) % high);
+    j = __builtin_amdgcn_readfirstlane((n - g * per) / high);
 }
 
 template <typename T>
@@ -60,72 +58,97 @@ __device__ __forceinline__ T to_type(float x)
     return static_cast<T>(x);
 }
 
+__device__ __forceinline__ uint32_t lds_address(char* smem) { return (uint32_t)(uintptr_t)(ZO_LDS char*)smem; }
+
 // ------------------------------------------------------------------ the logits
 
 struct LogitsArgs {
     Operand h, w;
     const int64_t* targets;     // of the chunk's tokens
     float* target_logit;
-    float2* stats;              // [tokens][pieces]
+    float2* stats;              // [tokens][pieces]: maximum and sum
     void* exps;                 // [tokens][vocab_ld], or NULL: the loss alone
     int64_t tokens, vocab, vocab_ld, pieces;
-    int64_t ti, tj;
+    uint32_t ti, tj;          // tiles
 };
 
-template <typename T>
+template <typename T, int NI, int NJ>
 __global__ __launch_bounds__(kGemmThreads, 2) void logits_kernel(LogitsArgs a)
 {
+    using G = Gemm<T, kInner, kInner, NI, NJ>;
+    constexpr int R = 4 * NJ;                                  // a lane's ids, side by side
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     int64_t bi, bj;
     tile_of(blockIdx.x, a.ti, a.tj, bi, bj);
-    f4 acc[8][4];
-    const int steps = (int)ceil_div(a.h.depth, kDeep);
-    gemm_tile<T, kInner, kInner>(a.h, a.w, bi * kTile, bj * kTile, 0, steps,
-                                 (uint32_t)(uintptr_t)(ZO_LDS char*)smem, acc);
+    f4 acc[NI][NJ];
+    G::run(a.h, a.w, bi * G::kTileI, bj * G::kTileJ, 0, (int)ceil_div(a.h.depth, kDeep), lds_address(smem), acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t v0 = bj * kTile + (wave & 3) * kWaveJ;       // the wave's piece of 64 ids
-    if (v0 >= a.vocab_ld) return;
-    const int64_t v = v0 + (lane >> 4) * 16;                   // the lane's 16 ids
+    // the lane's ids: 16 from v on, and with NJ = 5 another 4 from `far` on
+    const int64_t v = bj * G::kTileJ + G::column_of(0, wave, lane);
+    const int64_t far = bj * G::kTileJ + G::column_of(4, wave, lane) - 16;       // (id of k >= 16: far + k)
+    if (bj * G::kTileJ + (wave & 3) * 64 >= a.vocab_ld) return;                  // (NJ = 4: past the last piece)
+    if ((bj + 1) * G::kTileJ > a.vocab) {                      // the tile that the vocabulary ends in
 #pragma unroll
-    for (int ti = 0; ti < 8; ++ti) {
-        const int64_t n = bi * kTile + (wave >> 2) * kWaveI + ti * 16 + (lane & 15);
-        float m = -INFINITY;
+        for (int ti = 0; ti < NI; ++ti)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            if (v + k >= a.vocab) acc[ti][k >> 2][k & 3] = -INFINITY;
-            m = fmaxf(m, acc[ti][k >> 2][k & 3]);
-        }
+            for (int k = 0; k < R; ++k)
+                if ((k < 16 ? v : far) + k >= a.vocab) acc[ti][k >> 2][k & 3] = -INFINITY;
+    }
+#pragma unroll
+    for (int ti = 0; ti < NI; ++ti) {
+        const int64_t n = bi * G::kTileI + G::row_of(ti, wave, lane);
+        float m = acc[ti][0][0];
+#pragma unroll
+        for (int k = 1; k < R; ++k) m = fmaxf(m, acc[ti][k >> 2][k & 3]);
         m = fmaxf(m, __shfl_xor(m, 16, kWave));
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
-        const int64_t target = n < a.tokens ? a.targets[n] - v : -1;
+        const int64_t target = n < a.tokens ? a.targets[n] : -1;
+        const bool near = target >= v && target < v + 16;
+        if (near || (NJ == 5 && target >= far + 16 && target < far + 20)) {
+            // (a chain of selections: an index into the registers would put them in memory)
+            const int at = (int)(target - (near ? v : far));
+            float z = 0.0f;
+#pragma unroll
+            for (int k = 0; k < R; ++k) z = at == k ? acc[ti][k >> 2][k & 3] : z;
+            a.target_logit[n] = z;
+        }
         // a piece of -infinities has no exponentials: 0, not exp(-inf + inf)
         const float base = m == -INFINITY ? 0.0f : m;
         float sum = 0.0f;
-        vec_t<T, 8> held[2];
+        vec_t<T, 4> held[NJ];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float z = acc[ti][k >> 2][k & 3];
-            if (target == k && v + k < a.vocab) a.target_logit[n] = z;
+        for (int k = 0; k < R; ++k) {
             // (the factor in the exponent: nothing is lost below fp32's normal range)
-            const float e = __builtin_amdgcn_exp2f(fmaf(z - base, kLog2e, kHoldLog2<T>));
+            const float e = __builtin_amdgcn_exp2f(fmaf(acc[ti][k >> 2][k & 3] - base, kLog2e, kHoldLog2<T>));
             sum += e;
-            held[k >> 3][k & 7] = to_type<T>(e);
+            held[k >> 2][k & 3] = to_type<T>(e);
         }
-        sum *= 1.0f / kHold<T>;
         sum += __shfl_xor(sum, 16, kWave);
         sum += __shfl_xor(sum, 32, kWave);
         if (n < a.tokens) {
-            if (lane < 16) a.stats[n * a.pieces + v0 / kPiece] = make_float2(m, sum);
+            if (lane < 16) a.stats[n * a.pieces + bj * 4 + (wave & 3)] = make_float2(m, sum * (1.0f / kHold<T>));
             if (a.exps != nullptr) {
-                auto* to = reinterpret_cast<vec_t<T, 8>*>(static_cast<T*>(a.exps) + n * a.vocab_ld + v);
-                to[0] = held[0];
-                to[1] = held[1];
+                T* to = static_cast<T*>(a.exps) + n * a.vocab_ld;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    reinterpret_cast<vec_t<T, 8>*>(to + v)[q] =
+                        __builtin_shufflevector(held[2 * q], held[2 * q + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+                if constexpr (NJ == 5) *reinterpret_cast<vec_t<T, 4>*>(to + far + 16) = held[4];
             }
         }
     }
 }
 
-// ------------------------------------------------------------------ statistics
+// The piece that id v belongs to: waves take 64 ids of each 256, or 64 + 16 of each 320.
+template <int NJ>
+__device__ __forceinline__ int64_t piece_of(int64_t v)
+{
+    if constexpr (NJ == 4) return v / 64;
+    const int64_t tile = v / 320, at = v % 320;
+    return tile * 4 + (at < 256 ? at / 64 : (at - 256) / 16);
+}
+
+// ------------------------------------------------------------------ joining the pieces
 
 __device__ __forceinline__ float block_max(float x, float* sh)
 {
@@ -148,103 +171,96 @@ __device__ __forceinline__ double block_sum(double x, double* sh)
     return x;
 }
 
-// One workgroup a token: its pieces join to lse, its loss, and (in place) each
-// piece's factor exp(m - lse).  A target outside the vocabulary that is not
-// ignore_index has loss NaN and factors NaN: the gradients then carry NaN, and a
-// checked step is skipped.
-__global__ __launch_bounds__(256) void join_kernel(float2* stats, const float* target_logit,
-                                                   const int64_t* targets, float* losses, float* lse_out,
-                                                   int64_t pieces, int64_t vocab, int64_t ignore)
+struct JoinArgs {
+    const float2* stats;
+    const float* target_logit;
+    const int64_t* targets;
+    float* losses;
+    float* lse;
+    void* exps;               // NULL: the loss alone
+    int64_t pieces, vocab, vocab_ld, ignore;
+};
+
+// A token: lse, its loss, and from its exponentials its row of G.  Where there are few
+// tokens, several workgroups a token (blockIdx.y) share its row, and each finds lse.  A
+// target outside the vocabulary that is not ignore_index has loss NaN and a row of NaN:
+// the gradients then carry NaN, and a checked step is skipped.
+template <typename T, int NJ>
+__global__ __launch_bounds__(256) void join_kernel(JoinArgs a)
 {
     __shared__ float shm[4];
     __shared__ double shs[4];
     const int64_t n = blockIdx.x;
-    float2* row = stats + n * pieces;
+    const float2* row = a.stats + n * a.pieces;
     float m = -INFINITY;
-    for (int64_t p = threadIdx.x; p < pieces; p += 256) m = fmaxf(m, row[p].x);
+    for (int64_t p = threadIdx.x; p < a.pieces; p += 256) m = fmaxf(m, row[p].x);
     m = block_max(m, shm);
     const float base = m == -INFINITY ? 0.0f : m;
     double sum = 0.0;
-    for (int64_t p = threadIdx.x; p < pieces; p += 256) {
+    for (int64_t p = threadIdx.x; p < a.pieces; p += 256) {
         const float2 s = row[p];
         sum += (double)(s.y * expf(s.x - base));
     }
     sum = block_sum(sum, shs);
     const float lse = base + (float)log(sum);
-    const int64_t t = targets[n];
-    const bool counts = t != ignore, known = t >= 0 && t < vocab;
-    if (threadIdx.x == 0) {
-        lse_out[n] = lse;
-        losses[n] = !counts ? 0.0f : known ? lse - target_logit[n] : __builtin_nanf("");
+    const int64_t t = a.targets[n];
+    const bool counts = t != a.ignore, known = t >= 0 && t < a.vocab;
+    const float z = counts && known ? a.target_logit[n] : 0.0f;
+    // what a token without a known target has instead
+    const float nothing = counts ? __builtin_nanf("") : 0.0f;
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        a.lse[n] = lse;
+        a.losses[n] = counts && known ? lse - z : nothing;
     }
-    for (int64_t p = threadIdx.x; p < pieces; p += 256) {
-        const float f = expf(row[p].x - lse);
-        row[p].y = !counts ? 0.0f : known ? f : __builtin_nanf("");
+    if (a.exps == nullptr) return;
+    T* exps = static_cast<T*>(a.exps) + n * a.vocab_ld;
+    const T own = to_type<T>(expm1f(z - lse) * kHold<T>);
+#pragma unroll 4
+    for (int64_t v = (blockIdx.y * 256 + threadIdx.x) * 8; v < a.vocab_ld; v += gridDim.y * 2048) {
+        auto* at = reinterpret_cast<vec_t<T, 8>*>(exps + v);
+        const float f = expf(row[piece_of<NJ>(v)].x - lse);
+        vec_t<T, 8> x = *at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            x[k] = counts && known ? to_type<T>((float)x[k] * f) : to_type<T>(nothing);
+            if (counts && known && v + k == t) x[k] = own;
+        }
+        *at = x;
     }
 }
 
-// How many tokens count, and the factor of the products' results.
-__global__ __launch_bounds__(1024) void count_kernel(const int64_t* targets, int64_t tokens, int64_t ignore,
-                                                     double grad_scale, float hold, float* alpha)
+// Sums over all tokens, in a fixed order: how many count, which settles the factor of
+// the products' results, and (the last time) the mean loss.
+__global__ __launch_bounds__(1024) void total_kernel(const int64_t* targets, const float* losses, int64_t tokens,
+                                                     int64_t ignore, double grad_scale, float hold, float* alpha,
+                                                     float* loss)
 {
-    __shared__ int sh[16];
+    __shared__ int shn[16];
+    __shared__ double shs[16];
     int n = 0;
-    for (int64_t i = threadIdx.x; i < tokens; i += 1024) n += targets[i] != ignore;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < tokens; i += 1024) {
+        n += targets[i] != ignore;
+        if (loss != nullptr) s += losses[i];
+    }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, kWave);
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = n;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int all = 0;
-        for (int k = 0; k < 16; ++k) all += sh[k];
-        alpha[0] = (float)(grad_scale / (all > 0 ? all : 1) / hold);
-        alpha[1] = (float)(all > 0 ? all : 1);
-    }
-}
-
-// The mean loss: fp64, in a fixed order.
-__global__ __launch_bounds__(1024) void mean_kernel(const float* losses, int64_t tokens, const float* alpha,
-                                                    float* loss)
-{
-    __shared__ double sh[16];
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < tokens; i += 1024) s += losses[i];
     s = wave_sum(s);
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
+    if ((threadIdx.x & 63) == 0) {
+        shn[threadIdx.x >> 6] = n;
+        shs[threadIdx.x >> 6] = s;
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-        for (int k = 0; k < 16; ++k) all += sh[k];
-        *loss = (float)(all / (double)alpha[1]);
+    if (threadIdx.x != 0) return;
+    int all = 0;
+    s = 0.0;
+    for (int k = 0; k < 16; ++k) {
+        all += shn[k];
+        s += shs[k];
     }
-}
-
-// ------------------------------------------------------------------ G
-
-// In place: what a piece holds times its factor, the target's entry by itself.
-// A lane has 8 ids; a workgroup 2048 of one token.
-template <typename T>
-__global__ __launch_bounds__(256) void scale_kernel(T* exps, const float2* stats, const float* target_logit,
-                                                    const float* lse, const int64_t* targets,
-                                                    int64_t vocab, int64_t vocab_ld, int64_t pieces,
-                                                    int64_t ignore)
-{
-    const int64_t n = blockIdx.y;
-    const int64_t v = (int64_t)blockIdx.x * 2048 + threadIdx.x * 8;
-    if (v >= vocab_ld) return;
-    auto* at = reinterpret_cast<vec_t<T, 8>*>(exps + n * vocab_ld + v);
-    const int64_t t = targets[n];
-    const float f = stats[n * pieces + v / kPiece].y;
-    vec_t<T, 8> x = *at;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = t == ignore ? to_type<T>(0.0f) : to_type<T>((float)x[k] * f);
-    if (t != ignore && t >= v && t < v + 8 && t < vocab) {
-        const T own = to_type<T>(expm1f(target_logit[n] - lse[n]) * kHold<T>);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (t - v == k) x[k] = own;
-    }
-    *at = x;
+    if (all < 1) all = 1;
+    *alpha = (float)(grad_scale / all / hold);
+    if (loss != nullptr) *loss = (float)(s / all);
 }
 
 // ------------------------------------------------------------------ the gradients
@@ -256,80 +272,95 @@ struct GradArgs {
     float* part;              // splits: fp32 parts [split][rows][cols], else NULL
     float* sum;               // running fp32 sum over chunks of tokens [rows][cols], or NULL
     int64_t rows, cols, out_ld;
-    int64_t ti, tj;
+    uint32_t ti, tj;          // tiles
     int64_t steps;            // of the whole depth
     int splits;
     int vector_out;           // 4 results can be stored at once
     int sum_in, sum_out;      // the sum is added / is where the result goes
 };
 
-template <typename T, Layout LP>
+template <typename T, Layout LP, int NI, int NJ>
 __global__ __launch_bounds__(kGemmThreads, 2) void grad_kernel(GradArgs a)
 {
+    using G = Gemm<T, LP, kOuter, NI, NJ>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    const int64_t tiles = a.ti * a.tj;
-    const int64_t split = blockIdx.x / tiles;
+    const uint32_t tiles = a.ti * a.tj;
+    const int64_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
     int64_t bi, bj;
     tile_of(blockIdx.x % tiles, a.ti, a.tj, bi, bj);
     const int64_t s0 = a.steps * split / a.splits, s1 = a.steps * (split + 1) / a.splits;
-    f4 acc[8][4];
-    gemm_tile<T, LP, kOuter>(a.p, a.q, bi * kTile, bj * kTile, s0 * kDeep, (int)(s1 - s0),
-                             (uint32_t)(uintptr_t)(ZO_LDS char*)smem, acc);
+    f4 acc[NI][NJ];
+    G::run(a.p, a.q, bi * G::kTileI, bj * G::kTileJ, s0 * kDeep, (int)(s1 - s0), lds_address(smem), acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float alpha = a.alpha[0];
+    if (a.part == nullptr && !a.sum_in && !a.sum_out && a.vector_out) {       // as good as always
 #pragma unroll
-    for (int ti = 0; ti < 8; ++ti) {
-        const int64_t i = bi * kTile + (wave >> 2) * kWaveI + ti * 16 + (lane & 15);
-        if (i >= a.rows) continue;
+        for (int ti = 0; ti < NI; ++ti) {
+            const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
+            if (i >= a.rows) continue;
+            T* to = static_cast<T*>(a.out) + i * a.out_ld;
 #pragma unroll
-        for (int tj = 0; tj < 4; ++tj) {
-            const int64_t j = bj * kTile + (wave & 3) * kWaveJ + tj * 16 + (lane >> 4) * 4;
-            const f4 c = acc[ti][tj];
-            if (a.part != nullptr) {
-                float* to = a.part + (split * a.rows + i) * a.cols + j;
+            for (int tj = 0; tj < NJ; ++tj) {
+                const int64_t j = bj * G::kTileJ + G::column_of(tj, wave, lane);
+                vec_t<T, 4> y;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < a.cols) to[e] = c[e];
-                continue;
-            }
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = c[e] * alpha;
-                if (a.sum_in && j + e < a.cols) x[e] += a.sum[i * a.cols + j + e];
-            }
-            if (a.sum_out) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < a.cols) a.sum[i * a.cols + j + e] = x[e];
-            } else {
-                T* to = static_cast<T*>(a.out) + i * a.out_ld + j;
-                if (a.vector_out && j + 4 <= a.cols) {
-                    vec_t<T, 4> y;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = to_type<T>(x[e]);
-                    *reinterpret_cast<vec_t<T, 4>*>(to) = y;
+                for (int e = 0; e < 4; ++e) y[e] = to_type<T>(acc[ti][tj][e] * alpha);
+                if (j + 4 <= a.cols) {
+                    *reinterpret_cast<vec_t<T, 4>*>(to + j) = y;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (j + e < a.cols) to[e] = to_type<T>(x[e]);
+                        if (j + e < a.cols) to[j + e] = y[e];
                 }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int ti = 0; ti < NI; ++ti) {
+        const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
+        if (i >= a.rows) continue;
+#pragma unroll
+        for (int tj = 0; tj < NJ; ++tj) {
+            const int64_t j = bj * G::kTileJ + G::column_of(tj, wave, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (j + e >= a.cols) continue;
+                const float c = acc[ti][tj][e];
+                if (a.part != nullptr) {
+                    a.part[(split * a.rows + i) * a.cols + j + e] = c;
+                    continue;
+                }
+                float* sum = a.sum + i * a.cols + j + e;
+                const float x = a.sum_in ? *sum + c * alpha : c * alpha;
+                if (a.sum_out) *sum = x;
+                else static_cast<T*>(a.out)[i * a.out_ld + j + e] = to_type<T>(x);
             }
         }
     }
 }
 
-// The parts of a split product, added in the order of the splits.
-template <typename T>
+// The parts of a split product, added in the order of the splits: W results a lane.
+template <typename T, int W>
 __global__ __launch_bounds__(256) void join_splits_kernel(const float* part, int splits, int64_t rows,
                                                           int64_t cols, const float* alpha, T* out,
                                                           int64_t out_ld)
 {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (at >= rows * cols) return;
-    float s = 0.0f;
-    for (int k = 0; k < splits; ++k) s += part[k * rows * cols + at];
-    out[at / cols * out_ld + at % cols] = to_type<T>(s * alpha[0]);
+    const int64_t all = rows * cols, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W;
+    if (at >= all) return;
+    float s[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) s[e] = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < splits; ++k) {
+        const vec_t<float, W> x = *reinterpret_cast<const vec_t<float, W>*>(part + k * all + at);
+#pragma unroll
+        for (int e = 0; e < W; ++e) s[e] += x[e];
+    }
+    vec_t<T, W> y;
+#pragma unroll
+    for (int e = 0; e < W; ++e) y[e] = to_type<T>(s[e] * alpha[0]);
+    store_vec<T, W>(out + at / cols * out_ld + at % cols, y);
 }
 
 // Rows of any stride and alignment to rows of ld, a multiple of 8, zeros behind the width.
@@ -346,28 +377,55 @@ __global__ __launch_bounds__(256) void repack_kernel(const T* x, int64_t stride,
     *reinterpret_cast<vec_t<T, 8>*>(out + at) = y;
 }
 
+// ------------------------------------------------------------------ launches
+
 bool loads_as_it_is(const void* p, int64_t stride, int64_t width)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && width % 8 == 0 && stride <= (1 << 21);
 }
 
+// A kernel's LDS beyond 64 KiB is asked for once.
 template <typename K>
-hipError_t allow_lds(K kernel)
+hipError_t allow(K kernel, int lds)
 {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               2 * kStageBytes);
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+}
+
+template <typename T, int NI, int NJ>
+hipError_t logits(LogitsArgs l, hipStream_t s)
+{
+    using G = Gemm<T, kInner, kInner, NI, NJ>;
+    static const hipError_t allowed = allow(logits_kernel<T, NI, NJ>, G::kLds);
+    if (allowed != hipSuccess) return allowed;
+    l.ti = (uint32_t)ceil_div(l.tokens, G::kTileI);
+    l.tj = (uint32_t)ceil_div(l.vocab, G::kTileJ);
+    logits_kernel<T, NI, NJ><<<dim3(l.ti * l.tj), kGemmThreads, G::kLds, s>>>(l);
+    return hipSuccess;
+}
+
+template <typename T, Layout LP, int NI, int NJ>
+hipError_t grad(GradArgs g, hipStream_t s)
+{
+    using G = Gemm<T, LP, kOuter, NI, NJ>;
+    static const hipError_t allowed = allow(grad_kernel<T, LP, NI, NJ>, G::kLds);
+    if (allowed != hipSuccess) return allowed;
+    g.ti = (uint32_t)ceil_div(g.rows, G::kTileI);
+    g.tj = (uint32_t)ceil_div(g.cols, G::kTileJ);
+    g.vector_out = ((uintptr_t)g.out & 7) == 0 && g.out_ld % 4 == 0;
+    grad_kernel<T, LP, NI, NJ><<<dim3(g.ti * g.tj * g.splits), kGemmThreads, G::kLds, s>>>(g);
+    return hipSuccess;
+}
+
+template <typename T, Layout LP>
+hipError_t grad(const GradArgs& g, const TileChoice& c, hipStream_t s)
+{
+    if (c.ni == 2) return grad<T, LP, 2, 4>(g, s);
+    return c.nj == 4 ? grad<T, LP, 8, 4>(g, s) : grad<T, LP, 8, 5>(g, s);
 }
 
 template <typename T>
 hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
 {
-    static const hipError_t allowed = [] {
-        hipError_t e = allow_lds(logits_kernel<T>);
-        if (e == hipSuccess) e = allow_lds(grad_kernel<T, kInner>);
-        if (e == hipSuccess) e = allow_lds(grad_kernel<T, kOuter>);
-        return e;
-    }();
-    if (allowed != hipSuccess) return allowed;
     float* alpha = reinterpret_cast<float*>(a.space + p.off_alpha);
     float* target_logit = reinterpret_cast<float*>(a.space + p.off_target);
     float* lse = a.lse != nullptr ? a.lse : reinterpret_cast<float*>(a.space + p.off_lse);
@@ -376,7 +434,7 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
     T* exps = gradient ? reinterpret_cast<T*>(a.space + p.off_exp) : nullptr;
     const T* h = static_cast<const T*>(a.hidden);
     const T* w = static_cast<const T*>(a.weight);
-    int64_t h_ld = a.hidden_stride, w_ld = a.weight_stride, depth = p.width;
+    int64_t h_ld = a.hidden_stride, w_ld = a.weight_stride;
     if (!loads_as_it_is(h, h_ld, p.width) || !loads_as_it_is(w, w_ld, p.width)) {
         T* hp = reinterpret_cast<T*>(a.space + p.off_hidden);
         T* wp = reinterpret_cast<T*>(a.space + p.off_weight);
@@ -388,74 +446,92 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         repack(w, w_ld, p.vocab, wp);
         h = hp;
         w = wp;
-        h_ld = w_ld = depth = p.width_ld;
+        h_ld = w_ld = p.width_ld;
     }
-    count_kernel<<<1, 1024, 0, s>>>(a.targets, p.tokens, a.ignore_index, a.grad_scale, kHold<T>, alpha);
-    const Operand ow{w, w_ld, p.vocab, depth};
-    if (p.tokens == 0 && gradient) {       // a sum over no tokens
-        GradArgs g{};
-        g.p = Operand{w, p.vocab_ld, p.vocab_ld, 0};
-        g.q = Operand{w, w_ld, depth, 0};
-        g.alpha = alpha;
-        g.rows = p.vocab;
-        g.cols = p.width;
-        g.ti = ceil_div(p.vocab, kTile);
-        g.tj = ceil_div(p.width, kTile);
-        g.splits = 1;
-        g.out = a.dweight;
-        g.out_ld = a.dweight_stride;
-        grad_kernel<T, kOuter><<<dim3((unsigned)(g.ti * g.tj)), kGemmThreads, 2 * kStageBytes, s>>>(g);
+    auto total = [&](float* loss) {
+        total_kernel<<<1, 1024, 0, s>>>(a.targets, a.losses, p.tokens, a.ignore_index, a.grad_scale, kHold<T>, alpha, loss);
+    };
+    hipError_t e = hipSuccess;
+    if (p.tokens == 0) {
+        total(a.loss);
+        if (gradient) {                    // a sum over no tokens
+            GradArgs g{};
+            g.p = Operand{w, p.vocab_ld, p.vocab_ld, 0};
+            g.q = Operand{w, w_ld, p.width_ld, 0};
+            g.alpha = alpha;
+            g.rows = p.vocab;
+            g.cols = p.width;
+            g.splits = 1;
+            g.out = a.dweight;
+            g.out_ld = a.dweight_stride;
+            e = grad<T, kOuter>(g, p.weight_tile, s);
+        }
+        return e != hipSuccess ? e : hipGetLastError();
     }
-    for (int64_t n0 = 0; n0 < p.tokens; n0 += p.chunk) {
+    const Operand ow{w, w_ld, p.vocab, p.width_ld};
+    for (int64_t n0 = 0; n0 < p.tokens && e == hipSuccess; n0 += p.chunk) {
         const int64_t n = p.tokens - n0 < p.chunk ? p.tokens - n0 : p.chunk;
-        const Operand oh{h + n0 * h_ld, h_ld, n, depth};
-        LogitsArgs l{oh, ow, a.targets + n0, target_logit, stats, exps, n, p.vocab, p.vocab_ld, p.pieces,
-                     ceil_div(n, kTile), ceil_div(p.vocab, kTile)};
-        logits_kernel<T><<<dim3((unsigned)(l.ti * l.tj)), kGemmThreads, 2 * kStageBytes, s>>>(l);
-        join_kernel<<<dim3((unsigned)n), 256, 0, s>>>(stats, target_logit, a.targets + n0, a.losses + n0,
-                                                      lse + n0, p.pieces, p.vocab, a.ignore_index);
+        const bool last = n0 + n == p.tokens;
+        const Operand oh{h + n0 * h_ld, h_ld, n, p.width_ld};
+        const LogitsArgs l{oh, ow, a.targets + n0, target_logit, stats, exps, n, p.vocab, p.vocab_ld, p.pieces, 0, 0};
+        if (p.logits_tile.ni == 2) e = logits<T, 2, 4>(l, s);
+        else if (p.logits_tile.nj == 4) e = logits<T, 8, 4>(l, s);
+        else e = logits<T, 8, 5>(l, s);
+        if (e != hipSuccess) return e;
+        const JoinArgs j{stats, target_logit, a.targets + n0, a.losses + n0, lse + n0, exps,
+                         p.pieces, p.vocab, p.vocab_ld, a.ignore_index};
+        // (a workgroup has 2048 ids at a time; 1024 workgroups fill the card)
+        int64_t share = gradient && n < 1024 ? ceil_div(1024, n) : 1;
+        if (share > ceil_div(p.vocab_ld, 2048)) share = ceil_div(p.vocab_ld, 2048);
+        const dim3 joins((unsigned)n, (unsigned)share);
+        if (p.logits_tile.nj == 4) join_kernel<T, 4><<<joins, 256, 0, s>>>(j);
+        else join_kernel<T, 5><<<joins, 256, 0, s>>>(j);
+        if (n0 == 0 || last) total(last ? a.loss : nullptr);
         if (!gradient) continue;
-        scale_kernel<T><<<dim3((unsigned)ceil_div(p.vocab_ld, 2048), (unsigned)n), 256, 0, s>>>(
-            exps, stats, target_logit, lse + n0, a.targets + n0, p.vocab, p.vocab_ld, p.pieces, a.ignore_index);
         GradArgs g{};
         g.alpha = alpha;
         g.cols = p.width;
-        g.tj = ceil_div(p.width, kTile);
-        // dH = G W: k runs over the vocabulary, in parts where there are few tiles
+        // dH = G W: k runs over the vocabulary, in parts where that fills the card
         g.p = Operand{exps, p.vocab_ld, n, p.vocab_ld};
-        g.q = Operand{w, w_ld, depth, p.vocab};
+        g.q = Operand{w, w_ld, p.width_ld, p.vocab};
         g.rows = n;
-        g.ti = ceil_div(n, kTile);
         g.steps = p.vocab_ld / kDeep;
         g.splits = p.splits;
         g.out = static_cast<T*>(a.dhidden) + n0 * a.dhidden_stride;
         g.out_ld = a.dhidden_stride;
-        g.vector_out = ((uintptr_t)g.out & 7) == 0 && g.out_ld % 4 == 0;
         g.part = p.splits > 1 ? reinterpret_cast<float*>(a.space + p.off_split) : nullptr;
-        grad_kernel<T, kInner><<<dim3((unsigned)(g.ti * g.tj * g.splits)), kGemmThreads, 2 * kStageBytes, s>>>(g);
-        if (p.splits > 1)
-            join_splits_kernel<T><<<dim3((unsigned)ceil_div(n * p.width, 256)), 256, 0, s>>>(
-                g.part, p.splits, n, p.width, alpha, static_cast<T*>(g.out), g.out_ld);
+        e = grad<T, kInner>(g, p.hidden_tile, s);
+        if (e != hipSuccess) return e;
+        if (p.splits > 1) {
+            T* out = static_cast<T*>(g.out);
+            if (p.width % 4 == 0)
+                join_splits_kernel<T, 4><<<dim3((unsigned)ceil_div(n * p.width, 1024)), 256, 0, s>>>(
+                    g.part, p.splits, n, p.width, alpha, out, g.out_ld);
+            else
+                join_splits_kernel<T, 1><<<dim3((unsigned)ceil_div(n * p.width, 256)), 256, 0, s>>>(
+                    g.part, p.splits, n, p.width, alpha, out, g.out_ld);
+        }
         // dW = G^T H: k runs over the chunk's tokens; with several chunks the sum
         // stays in fp32 until the last
         g.p = Operand{exps, p.vocab_ld, p.vocab_ld, n};
-        g.q = Operand{oh.base, h_ld, depth, n};
+        g.q = Operand{oh.base, h_ld, p.width_ld, n};
         g.rows = p.vocab;
-        g.ti = ceil_div(p.vocab, kTile);
         g.steps = ceil_div(n, kDeep);
         g.splits = 1;
         g.out = a.dweight;
         g.out_ld = a.dweight_stride;
-        g.vector_out = ((uintptr_t)g.out & 7) == 0 && g.out_ld % 4 == 0;
         g.part = nullptr;
         g.sum = reinterpret_cast<float*>(a.space + p.off_sum);
         g.sum_in = n0 > 0;
-        g.sum_out = n0 + n < p.tokens;
-        grad_kernel<T, kOuter><<<dim3((unsigned)(g.ti * g.tj)), kGemmThreads, 2 * kStageBytes, s>>>(g);
+        g.sum_out = !last;
+        e = grad<T, kOuter>(g, p.weight_tile, s);
     }
-    mean_kernel<<<1, 1024, 0, s>>>(a.losses, p.tokens, alpha, a.loss);
-    return hipGetLastError();
+    return e != hipSuccess ? e : hipGetLastError();
 }
+
+// Rows up to which tiles of 64 are taken instead of 256.  At 16 tokens x 50257 x 1600
+// they take 29, 30 and 64 us for the three products, against 38, 41 and 65.
+constexpr int64_t kFewRows = 128;
 
 }  // namespace
 
@@ -465,18 +541,47 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chu
     p.tokens = tokens;
     p.vocab = vocab;
     p.width = width;
-    p.vocab_ld = round_up(vocab, kVocabPad);
-    p.pieces = p.vocab_ld / kPiece;
     p.width_ld = round_up(width, 8);
     p.chunk = tokens < max_chunk ? tokens : max_chunk;
     if (p.chunk < 1) p.chunk = 1;
-    // parts of the vocabulary: enough workgroups for every CU, none with less than
-    // 8 steps
-    const int64_t tiles = ceil_div(p.chunk, kTile) * ceil_div(width, kTile);
+    // A tile of 256 x 320 takes 1.2 times as long as one of 256 x 256 (at 8192 x 1600 x
+    // 50257 the weight's gradient takes 1124 us instead of 1350, in 4 rounds of tiles
+    // instead of 6): the fewer rounds over the card, so weighed, win.
+    auto rounds = [](int64_t rows, int64_t cols, int nj, int64_t splits) {
+        return ceil_div(ceil_div(rows, 256) * ceil_div(cols, 64 * nj) * splits, kCUs);
+    };
+    auto wide = [&](int64_t rows, int64_t cols) {
+        return rounds(rows, cols, 5, 1) * 6 < rounds(rows, cols, 4, 1) * 5 ? 5 : 4;
+    };
+    const bool few = p.chunk <= kFewRows;
+    p.logits_tile = few ? TileChoice{2, 4} : TileChoice{8, wide(p.chunk, vocab)};
+    p.weight_tile = few ? TileChoice{2, 4} : TileChoice{8, wide(vocab, width)};
+    p.vocab_ld = round_up(vocab, p.logits_tile.nj == 5 ? 320 : 64);      // whole pieces, whole steps
+    p.pieces = p.vocab_ld / (16 * p.logits_tile.nj);
     const int64_t steps = p.vocab_ld / kDeep;
-    int64_t splits = tiles < kCUs ? kCUs / tiles : 1;
-    if (splits > steps / 8) splits = steps / 8;
-    p.splits = splits < 1 ? 1 : (int)splits;
+    p.splits = 1;
+    if (few) {
+        // parts of the vocabulary until every CU has a tile, none with less than 8 steps
+        p.hidden_tile = TileChoice{2, 4};
+        int64_t splits = kCUs / (ceil_div(p.chunk, 64) * ceil_div(width, 256));
+        if (splits > steps / 8) splits = steps / 8;
+        p.splits = splits < 1 ? 1 : (int)splits;
+    } else {
+        // the hidden states' gradient has few tiles and a long depth: of the tiles and
+        // parts, those that take the least, a step of 256 x 256 x 64 being 1.6 us, and the
+        // parts' way through memory 4 TB/s
+        double best = 0.0;
+        for (int nj = 4; nj <= 5; ++nj)
+            for (int64_t k = 1; k <= 16 && k <= (steps + 7) / 8; ++k) {
+                const double t = rounds(p.chunk, width, nj, k) * ceil_div(steps, k) * 1.6 * (nj == 5 ? 1.2 : 1.0) +
+                                 (k > 1 ? 2.0 * k * p.chunk * width * 4 / 4e6 + 5.0 : 0.0);
+                if (best == 0.0 || t < best) {
+                    best = t;
+                    p.hidden_tile = TileChoice{8, nj};
+                    p.splits = (int)k;
+                }
+            }
+    }
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t off = at;
