@@ -1,11 +1,14 @@
 // AdamW over the tensors of a model at once, with moments in 32 or in 8 bits.
 //
 // One launch updates every tensor: a table in device memory, made when the handle
-// is, cuts the tensors into chunks of 4096 elements, a workgroup each.  A lane has 4
-// elements side by side, so that every load and store of a wave is whole lines (512
-// bytes of 2-byte gradients, 1 KiB of fp32), and a wave's 256 elements are a block
-// of the 8-bit states.  Bound by memory: per element and step 28 bytes with fp32
-// moments and 2-byte storage, 14 with 8-bit moments.
+// is, cuts the tensors into chunks, a workgroup each.  A lane has 4 elements side by
+// side, so that every load and store of a wave is whole lines (512 bytes of 2-byte
+// gradients, 1 KiB of fp32), and a wave's 256 elements are a block of the 8-bit
+// states.  Bound by memory: per element and step 28 bytes with fp32 moments and 2-byte
+// storage, 16 with 8-bit moments; with the latter only because the arithmetic is
+// spare (a division by a step's constant in 3 operations, one hash for both moments'
+// noise, powers of two by ldexp): at 5 TB/s a wave has about 400 cycles for 256
+// elements of 16 bytes.
 //
 // The arithmetic is that of the shard's Adam (each operation rounded to fp32 in
 // the order written, no fused multiply-adds), so that a tensor's update has the same bits
@@ -36,14 +39,11 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 constexpr int kExpLeast = -100;       // the smallest power of two a block has
 constexpr int kExpNaN = 127;          // a block that holds nothing finite
 constexpr int kThreads = 256;
-constexpr int kBlocksPerWave = (int)(kAdamwChunk / kThreads / 4);    // 4 elements a lane
 
 template <int TYPE> struct Stored;
 template <> struct Stored<1> { using T = _Float16; };
 template <> struct Stored<2> { using T = __bf16; };
 template <> struct Stored<3> { using T = float; };
-
-__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
 
 // 32 bits of noise from 32 bits: shifts against multiplications by the fractions
 // of the golden ratio and of the root of two.
@@ -66,11 +66,23 @@ __device__ __forceinline__ uint32_t noise_key(uint64_t seed, int64_t t, int32_t 
 }
 
 // The largest of the wave's values, as bits of non-negative floats (so a NaN is
-// the largest of all).
+// the largest of all): inside rows of 16 lanes by DPP (a rotation by 8 or 4 reaches the
+// partner once those before agree), across rows by shuffles.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x)
+{
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, false);
+    return x > y ? x : y;
+}
+
 __device__ __forceinline__ uint32_t wave_max(uint32_t x)
 {
+    x = dpp_max<0x128>(x);      // row_ror:8
+    x = dpp_max<0x124>(x);      // row_ror:4
+    x = dpp_max<0x4E>(x);       // quad_perm [2,3,0,1]
+    x = dpp_max<0xB1>(x);       // quad_perm [1,0,3,2]
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
+    for (int off = 16; off <= 32; off *= 2) {
         const uint32_t y = __shfl_xor(x, off, kWave);
         x = x > y ? x : y;
     }
@@ -85,25 +97,52 @@ __device__ __forceinline__ int block_exp(uint32_t bits)
     return e < kExpLeast ? kExpLeast : e > kExpNaN ? kExpNaN : e;
 }
 
-// Magnitude x >= 0 to a code: scaled so that the code's least normal exponent is
-// fp32's, the code is the top bits of the float, and noise below them, added, rounds.
+// A value to a code: scaled so that the code's least normal exponent is fp32's, the
+// code is the top bits of the float's magnitude, and noise below them, added, rounds.
 // LEAST: 14 (m) or 30 (v).
 template <int LEAST>
-__device__ __forceinline__ uint32_t encode(float x, float inv_block, uint32_t r16)
+__device__ __forceinline__ uint32_t encode(float x, int block, uint32_t r16)
 {
-    const float z = (x * inv_block) * pow2(LEAST - 126);
+    const float z = __builtin_amdgcn_ldexpf(fabsf(x), LEAST - 126 - block);
     return (__builtin_bit_cast(uint32_t, z) + (r16 << 4) + 8) >> 20;
 }
 
-template <int LEAST>
-__device__ __forceinline__ float decode(uint32_t code, float block)
+__device__ __forceinline__ uint32_t encode_m(float x, int block, uint32_t r16)
 {
-    return (__builtin_bit_cast(float, code << 20) * pow2(126 - LEAST)) * block;
+    return (encode<14>(x, block, r16) & 127) | (__builtin_bit_cast(uint32_t, x) >> 24 & 128);
 }
 
-__device__ __forceinline__ float block_scale(int e)
+__device__ __forceinline__ uint32_t encode_v(float x, int block, uint32_t r16)
 {
-    return e >= kExpNaN ? __builtin_nanf("") : pow2(e < kExpLeast ? kExpLeast : e);
+    return encode<30>(x, block, r16) & 255;
+}
+
+// The code in bits 8 k to 8 k + 7, and what it stands for.
+__device__ __forceinline__ float decode_m(uint32_t codes, int k, int block)
+{
+    const uint32_t c = codes << (24 - 8 * k);                       // at the top
+    const uint32_t bits = (c & 0x7f000000u) >> 4 | (c & 0x80000000u);
+    return __builtin_amdgcn_ldexpf(__builtin_bit_cast(float, bits), 126 - 14 + block);
+}
+
+__device__ __forceinline__ float decode_v(uint32_t codes, int k, int block)
+{
+    return __builtin_amdgcn_ldexpf(__builtin_bit_cast(float, (codes >> (8 * k) & 255) << 20), 126 - 30 + block);
+}
+
+// A stored exponent for the decoders; a block of nothing finite is multiplied by NaN.
+__device__ __forceinline__ int block_of(int e) { return e < kExpLeast ? kExpLeast : e; }
+
+// x / c for a constant c in (0, 1], r its reciprocal, rounded: the quotient's
+// remainder is exact, and one step with it rounds as the division does (Markstein).
+// Where the remainder could fall below fp32's range the division itself is taken.
+__device__ __forceinline__ float divide_by(float x, float c, float r)
+{
+    const float q = x * r;
+    const float exact = fmaf(fmaf(-q, c, x), r, q);
+    const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+    if (__builtin_expect(b - 1 < 0x0d000000u - 1 || b >= 0x7e800000u, 0)) return x / c;    // below 2^-101, above 2^126
+    return exact;
 }
 
 // 4 elements from e on of an array of n, zeros past the end.
@@ -164,66 +203,42 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t e, int64_t n, ui
 // ------------------------------------------------------------------ the check
 
 template <int TYPE>
-__device__ __forceinline__ void norm_chunk(const TensorEntry& t, int64_t begin, float inv_scale, double& ss,
-                                           int& flag)
+__device__ __forceinline__ void norm_part(const TensorEntry& t, int64_t begin, int64_t end, float inv_scale,
+                                          double& ss)
 {
     using T = typename Stored<TYPE>::T;
+    constexpr int W = Vec<T>::W;
     const T* g = static_cast<const T*>(t.grad);
-    f4 x[kBlocksPerWave];
+    auto add = [&](float x) {
+        const double y = (double)(x * inv_scale);
+        ss = __builtin_fma(y, y, ss);      // (the product is exact in 64 bits)
+    };
+    int64_t e = begin + threadIdx.x * W;
+    constexpr int64_t step = kThreads * W;
+    for (; e + 3 * step + W <= end; e += 4 * step) {
+        vec_t<T, W> x[4];
 #pragma unroll
-    for (int u = 0; u < kBlocksPerWave; ++u)
-        x[u] = load4(g, begin + (u * kThreads + threadIdx.x) * 4, t.numel);
+        for (int u = 0; u < 4; ++u) x[u] = load_vec<T, W>(g + e + u * step);
 #pragma unroll
-    for (int u = 0; u < kBlocksPerWave; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float y = x[u][k] * inv_scale;
-            flag |= (__builtin_bit_cast(uint32_t, y) & 0x7f800000u) == 0x7f800000u;
-            ss += (double)y * (double)y;
+            for (int k = 0; k < W; ++k) add((float)x[u][k]);
+    }
+    for (; e < end; e += step) {
+        if (e + W <= end) {
+            const vec_t<T, W> x = load_vec<T, W>(g + e);
+#pragma unroll
+            for (int k = 0; k < W; ++k) add((float)x[k]);
+        } else {
+            for (int64_t k = e; k < end; ++k) add((float)g[k]);
         }
+    }
 }
 
-// One fp64 partial sum of squares a chunk, NaN where an unscaled value is not finite.
-__global__ __launch_bounds__(kThreads) void norm_kernel(AdamwLaunch a)
+// The step's decision, as the shard's device-resident flow takes it, from the sum of
+// squares (0 without a check: every step is taken).
+__device__ void decide(const AdamwLaunch& a, double s)
 {
-    __shared__ double sh[4];
-    __shared__ int shf[4];
-    const ChunkEntry c = a.chunks[blockIdx.x];
-    const TensorEntry t = a.tensors[c.tensor];
-    const float inv_scale = a.state->inv_scale;
-    double ss = 0.0;
-    int flag = 0;
-    if (t.type == 1) norm_chunk<1>(t, c.begin, inv_scale, ss, flag);
-    else if (t.type == 2) norm_chunk<2>(t, c.begin, inv_scale, ss, flag);
-    else norm_chunk<3>(t, c.begin, inv_scale, ss, flag);
-    ss = wave_sum(ss);
-    flag = __any(flag);
-    if ((threadIdx.x & 63) == 0) {
-        sh[threadIdx.x >> 6] = ss;
-        shf[threadIdx.x >> 6] = flag;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0)
-        a.partial[blockIdx.x] = (shf[0] | shf[1] | shf[2] | shf[3]) ? __builtin_nan("")
-                                                                    : (sh[0] + sh[1]) + (sh[2] + sh[3]);
-}
-
-// The partials in a fixed order, then the step's decision, as the shard's device-
-// resident flow takes it; without a check every step is taken.
-__global__ __launch_bounds__(1024) void decide_kernel(AdamwLaunch a, int checked)
-{
-    __shared__ double sh[16];
-    double s = 0.0;
-    if (checked) {
-        for (int64_t i = threadIdx.x; i < a.nchunks; i += 1024) s += a.partial[i];
-        s = wave_sum(s);
-        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
-        __syncthreads();
-        s = 0.0;
-        if (threadIdx.x == 0)
-            for (int k = 0; k < 16; ++k) s += sh[k];
-    }
-    if (threadIdx.x != 0) return;
     AdamwState d = *a.state;
     const bool overflow = !__builtin_isfinite(s);
     d.sumsq = s;
@@ -256,35 +271,83 @@ __global__ __launch_bounds__(1024) void decide_kernel(AdamwLaunch a, int checked
     *a.state = d;
 }
 
+__device__ __forceinline__ double block_sum(double x, double* sh)
+{
+    x = wave_sum(x);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
+// Workgroup b sums the squares of chunks [b n / grid, (b + 1) n / grid), tensor by tensor,
+// into an fp64 partial.  A value that is not finite makes its sum so, and no finite
+// ones can: fp32 squares stay far below fp64's range.
+__global__ __launch_bounds__(kThreads) void norm_kernel(AdamwLaunch a)
+{
+    __shared__ double sh[4];
+    const float inv_scale = a.state->inv_scale;
+    const int64_t last = a.nchunks * (blockIdx.x + 1) / gridDim.x;
+    double ss = 0.0;
+    for (int64_t c = a.nchunks * blockIdx.x / gridDim.x; c < last;) {
+        const ChunkEntry first = a.chunks[c];
+        const TensorEntry t = a.tensors[first.tensor];
+        // as many chunks as are left of this tensor
+        int64_t count = ceil_div(t.numel - first.begin, a.chunk);
+        if (count > last - c) count = last - c;
+        int64_t end = first.begin + count * a.chunk;
+        if (end > t.numel) end = t.numel;
+        if (t.type == 1) norm_part<1>(t, first.begin, end, inv_scale, ss);
+        else if (t.type == 2) norm_part<2>(t, first.begin, end, inv_scale, ss);
+        else norm_part<3>(t, first.begin, end, inv_scale, ss);
+        c += count;
+    }
+    ss = block_sum(ss, sh);
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = ss;
+}
+
+// The partials in a fixed order, and the decision.  (A launch of its own: left to the
+// workgroup of the check that ends last, the fences that takes cost 100 us at 2048
+// workgroups, against 5 for the launch.)
+__global__ __launch_bounds__(kThreads) void decide_kernel(AdamwLaunch a, int64_t partials)
+{
+    __shared__ double sh[4];
+    double s = 0.0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < partials; i += kThreads) s += a.partial[i];
+    s = block_sum(s, sh);
+    if (threadIdx.x == 0) decide(a, s);
+}
+
 // ------------------------------------------------------------------ the update
 
 // Textbook Adam on one element, in the order of the public header.
 __device__ __forceinline__ void adam(float g, float& p, float& m, float& v, const AdamwScalars& s,
-                                     const AdamwState& d, float wd, float lr)
+                                     const AdamwState& d, float r1, float r2, float wd, float lr)
 {
     g = g * d.upd_inv_scale;
     g = g * d.clip;
     if (s.l2) g = g + wd * p;
     m = s.b1 * m + s.omb1 * g;
     v = s.b2 * v + s.omb2 * (g * g);
-    float u = (m / d.bc1) / (sqrtf(v / d.bc2) + s.eps);
+    float u = divide_by(m, d.bc1, r1) / (sqrtf(divide_by(v, d.bc2, r2)) + s.eps);
     if (!s.l2) u = u + wd * p;
     p = p - lr * u;
 }
 
-template <int TYPE, int BITS>
+// U: blocks of 256 elements a wave.
+template <int TYPE, int BITS, int U>
 __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const AdamwState& d, const TensorEntry& t,
                                              const ChunkEntry& c)
 {
     using T = typename Stored<TYPE>::T;
     const int64_t n = t.numel;
     const int lane = threadIdx.x & 63;
-    f4 g[kBlocksPerWave], p[kBlocksPerWave], m[kBlocksPerWave], v[kBlocksPerWave];
-    uint32_t cm[kBlocksPerWave], cv[kBlocksPerWave];
-    float bm[kBlocksPerWave], bv[kBlocksPerWave];
+    f4 g[U], p[U], m[U], v[U];
+    uint32_t cm[U], cv[U];
+    int bm[U], bv[U];
     const int64_t e0 = c.begin + threadIdx.x * 4;
 #pragma unroll
-    for (int u = 0; u < kBlocksPerWave; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + u * kThreads * 4;
         g[u] = load4(static_cast<const T*>(t.grad), e, n);
         p[u] = load4(t.master, e, n);
@@ -295,29 +358,36 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const AdamwSt
             cm[u] = load_codes(static_cast<const uint8_t*>(t.m), e, n);
             cv[u] = load_codes(static_cast<const uint8_t*>(t.v), e, n);
             const int64_t b = e / kStateBlock, last = (n - 1) / kStateBlock;
-            bm[u] = block_scale(t.m_exp[b < last ? b : last]);
-            bv[u] = block_scale(t.v_exp[b < last ? b : last]);
+            bm[u] = t.m_exp[b < last ? b : last];
+            bv[u] = t.v_exp[b < last ? b : last];
         }
     }
     const float wd = t.weight_decay < 0.0f ? a.s.wd : t.weight_decay, lr = a.s.lr * t.lr_scale;
+    const float r1 = 1.0f / d.bc1, r2 = 1.0f / d.bc2;
     uint32_t key = 0;
     if constexpr (BITS == 8) key = noise_key(a.s.seed, d.t, c.tensor, c.begin);
 #pragma unroll
-    for (int u = 0; u < kBlocksPerWave; ++u) {
+    for (int u = 0; u < U; ++u) {
         const int64_t e = e0 + u * kThreads * 4;
         if constexpr (BITS == 8) {
+            const int em = block_of(bm[u]), ev = block_of(bv[u]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t x = cm[u] >> (8 * k) & 255, y = cv[u] >> (8 * k) & 255;
-                const float mag = decode<14>(x & 127, bm[u]);
-                m[u][k] = x & 128 ? -mag : mag;
-                v[u][k] = decode<30>(y, bv[u]);
+                m[u][k] = decode_m(cm[u], k, em);
+                v[u][k] = decode_v(cv[u], k, ev);
+            }
+            if (em == kExpNaN || ev == kExpNaN) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    m[u][k] = em == kExpNaN ? __builtin_nanf("") : m[u][k];
+                    v[u][k] = ev == kExpNaN ? __builtin_nanf("") : v[u][k];
+                }
             }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float pk = p[u][k], mk = m[u][k], vk = v[u][k];
-            adam(g[u][k], pk, mk, vk, a.s, d, wd, lr);
+            adam(g[u][k], pk, mk, vk, a.s, d, r1, r2, wd, lr);
             p[u][k] = pk;
             m[u][k] = mk;
             v[u][k] = vk;
@@ -338,15 +408,13 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const AdamwSt
                     top_v = y > top_v ? y : top_v;
                 }
             const int em = block_exp(wave_max(top_m)), ev = block_exp(wave_max(top_v));
-            const float im = pow2(em == kExpNaN ? 0 : -em), iv = pow2(ev == kExpNaN ? 0 : -ev);
             uint32_t xm = 0, xv = 0;
+            const uint32_t at = key + (uint32_t)e * 0xDDB3D743u;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t r = mix(key + (uint32_t)(e + k) * 0xDDB3D743u);
-                const uint32_t x = encode<14>(fabsf(m[u][k]), im, r & 0xffffu);
-                const uint32_t y = encode<30>(v[u][k], iv, r >> 16);
-                xm |= ((x & 127) | (m[u][k] < 0.0f ? 128u : 0u)) << (8 * k);
-                xv |= (y & 255) << (8 * k);
+                const uint32_t r = mix(at + k * 0xDDB3D743u);
+                xm |= encode_m(m[u][k], em, r & 0xffffu) << (8 * k);
+                xv |= encode_v(v[u][k], ev, r >> 16) << (8 * k);
             }
             store_codes(static_cast<uint8_t*>(t.m), e, n, xm);
             store_codes(static_cast<uint8_t*>(t.v), e, n, xv);
@@ -359,16 +427,16 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const AdamwSt
     }
 }
 
-template <int BITS>
+template <int BITS, int U>
 __global__ __launch_bounds__(kThreads) void update_kernel(AdamwLaunch a)
 {
     const ChunkEntry c = a.chunks[blockIdx.x];
     const TensorEntry t = a.tensors[c.tensor];
     const AdamwState d = *a.state;
     if (d.skip) return;
-    if (t.type == 1) update_chunk<1, BITS>(a, d, t, c);
-    else if (t.type == 2) update_chunk<2, BITS>(a, d, t, c);
-    else update_chunk<3, BITS>(a, d, t, c);
+    if (t.type == 1) update_chunk<1, BITS, U>(a, d, t, c);
+    else if (t.type == 2) update_chunk<2, BITS, U>(a, d, t, c);
+    else update_chunk<3, BITS, U>(a, d, t, c);
 }
 
 // ------------------------------------------------------------------ tables and states
@@ -398,54 +466,59 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const float* x, uint8_t*
         top = b > top ? b : top;
     }
     const int be = block_exp(wave_max(top));
-    const float inv = pow2(be == kExpNaN ? 0 : -be);
     uint32_t c = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         // to the nearest: half a code, less half of the noise's last place
-        if constexpr (SIGNED)
-            c |= ((encode<14>(fabsf(v[k]), inv, 32767) & 127) | (v[k] < 0.0f ? 128u : 0u)) << (8 * k);
-        else
-            c |= (encode<30>(v[k] > 0.0f ? v[k] : 0.0f, inv, 32767) & 255) << (8 * k);
+        if constexpr (SIGNED) c |= encode_m(v[k], be, 32767) << (8 * k);
+        else c |= encode_v(v[k] > 0.0f ? v[k] : 0.0f, be, 32767) << (8 * k);
     }
     store_codes(codes, e, n, c);
     if (lane == 0 && e < n) exps[e / kStateBlock] = (int8_t)be;
 }
 
+// 8 elements a lane: 512 bytes of codes a wave, and 1 or 2 KiB of values.
 template <typename T, bool SIGNED>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* codes, const int8_t* exps, T* out, int64_t n)
 {
-    const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
     if (e >= n) return;
-    const float b = block_scale(exps[e / kStateBlock]);
-    const uint32_t c = load_codes(codes, e, n);
-    f4 x;
+    const int b = block_of(exps[e / kStateBlock]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t y = c >> (8 * k) & 255;
-        if constexpr (SIGNED) {
-            const float mag = decode<14>(y & 127, b);
-            x[k] = y & 128 ? -mag : mag;
-        } else {
-            x[k] = decode<30>(y, b);
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = load_codes(codes, e + 4 * h, n);
+        f4 x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[k] = SIGNED ? decode_m(c, k, b) : decode_v(c, k, b);
+            if (b == kExpNaN) x[k] = __builtin_nanf("");
         }
+        store4(out, e + 4 * h, n, x);
     }
-    store4(out, e, n, x);
 }
 
 }  // namespace
 
 hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.nchunks);
-    if (checked && a.nchunks > 0) norm_kernel<<<grid, kThreads, 0, s>>>(a);
-    decide_kernel<<<1, 1024, 0, s>>>(a, checked);
+    // the check: a workgroup for 4096 elements, and 8 a CU at most, whose loads fill the
+    // memory's pipe
+    int64_t sums = checked ? ceil_div(a.nchunks * a.chunk, kAdamwChunk) : 0;
+    if (sums > kAdamwPartials) sums = kAdamwPartials;
+    if (sums > 0) norm_kernel<<<dim3((unsigned)sums), kThreads, 0, s>>>(a);
+    decide_kernel<<<1, kThreads, 0, s>>>(a, sums);
     if (a.nchunks > 0) {
-        if (bits == 32) update_kernel<32><<<grid, kThreads, 0, s>>>(a);
-        else update_kernel<8><<<grid, kThreads, 0, s>>>(a);
+        const dim3 grid((unsigned)a.nchunks);
+        const bool small = a.chunk == kAdamwSmallChunk;
+        if (bits == 32 && small) update_kernel<32, 1><<<grid, kThreads, 0, s>>>(a);
+        else if (bits == 32) update_kernel<32, 4><<<grid, kThreads, 0, s>>>(a);
+        else if (small) update_kernel<8, 1><<<grid, kThreads, 0, s>>>(a);
+        else update_kernel<8, 4><<<grid, kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
+
+int64_t adamw_chunk(int64_t elements) { return elements < kAdamwLarge ? kAdamwSmallChunk : kAdamwChunk; }
 
 hipError_t adamw_set_state(AdamwState* state, const AdamwState& to, hipStream_t s)
 {
@@ -473,7 +546,7 @@ hipError_t moments_pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n,
 template <typename T>
 static void unpack(const uint8_t* codes, const int8_t* exps, void* out, int64_t n, bool is_signed, hipStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(n, kThreads * 4));
+    const dim3 grid((unsigned)ceil_div(n, kThreads * 8));
     if (is_signed) unpack_kernel<T, true><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
     else unpack_kernel<T, false><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
 }

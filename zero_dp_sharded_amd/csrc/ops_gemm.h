@@ -216,7 +216,10 @@ struct Outer64 {
     }
 };
 
-// 256 columns: 64 rows of k with 512 bytes each.
+// 256 columns: 64 rows of k with 512 bytes each.  With RUNS the four products of a wave
+// take columns w0 + 16 (r / 4) + 4 t + r % 4, so that a lane's results lie side by
+// side, at the price of bank conflicts: where storing is what takes the time.
+template <bool RUNS>
 struct Outer256 {
     static constexpr int kBytes = 256 * kDeep * 2;
     uint32_t voff[2], apart, addr;
@@ -243,11 +246,14 @@ struct Outer256 {
     {
         const int r = lane & 15, g = lane >> 4, k = g * 8 + (r >> 2);
         const int chunk = (w0 >> 3) | ((r & 3) >> 1);
-        addr = lds + k * 512 + ((chunk ^ key(k)) << 4) + (r & 1) * 8;
+        const int piece = RUNS ? (w0 >> 3) | (r & 3) * 2 : chunk;
+        addr = lds + k * 512 + ((piece ^ key(k)) << 4) + (RUNS ? 0 : (r & 1) * 8);
     }
     __device__ __forceinline__ s8 get(uint32_t stage, int t, int kk) const
     {
-        const uint32_t a = ((addr ^ (t << 5)) + stage) + kk * 16384;
+        // (keys are even: bit 4 of the address is the chunk's own low bit)
+        const uint32_t turn = RUNS ? (t >> 1) << 4 | (t & 1) << 3 : t << 5;
+        const uint32_t a = ((addr ^ turn) + stage) + kk * 16384;
         const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)a);
         const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZO_LDS s4*)(uintptr_t)(a + 2048));
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -257,13 +263,13 @@ struct Outer256 {
 // kOuter operand of 64 C columns: 64, 256, or 256 and 64 beside them (C = 5).
 // Product t of a wave with W products: columns 16 (w W + t); with C = 5 products 0 to 3
 // lie in the 256 and product 4 in the 64, at 256 + 16 w.
-template <int C>
+template <int C, bool RUNS>
 struct Outer {
-    static_assert(C == 1 || C == 4 || C == 5, "");
-    static constexpr int kWide = C == 1 ? 0 : Outer256::kBytes;
+    static_assert(C == 1 || C == 4 || (C == 5 && !RUNS), "");
+    static constexpr int kWide = C == 1 ? 0 : Outer256<RUNS>::kBytes;
     static constexpr int kBytes = C * 64 * kDeep * 2;
     Piece piece;
-    Outer256 wide;
+    Outer256<RUNS> wide;
     Outer64 narrow;
 
     __device__ __forceinline__ void init(const Operand& o, int64_t col0, int64_t k0, int wave, int lane)
@@ -296,7 +302,7 @@ struct Outer {
 
 template <Layout L, int C, bool RUNS> struct Side;
 template <int C, bool RUNS> struct Side<kInner, C, RUNS> { using type = Inner<C, RUNS>; };
-template <int C, bool RUNS> struct Side<kOuter, C, RUNS> { using type = Outer<C>; };
+template <int C, bool RUNS> struct Side<kOuter, C, RUNS> { using type = Outer<C, RUNS>; };
 
 // acc[ti][tj][e]: i = tile's i0 + 16 NI (wave / 4) + 16 ti + lane % 16; j by
 // column_of() below.  `steps` of kDeep from k0 on.
@@ -304,7 +310,9 @@ template <typename T, Layout LP, Layout LQ, int NI, int NJ>
 struct Gemm {
     static constexpr int kTileI = 32 * NI, kTileJ = 64 * NJ;
     using PSide = typename Side<LP, NI / 2, false>::type;
-    using QSide = typename Side<LQ, NJ, LQ == kInner>::type;
+    // a lane's results of products 0 to 3 lie side by side
+    static constexpr bool kRuns = LQ == kInner || NI == 2;
+    using QSide = typename Side<LQ, NJ, kRuns>::type;
     static constexpr int kStageBytes = PSide::kBytes + QSide::kBytes;
     static constexpr int kLds = 2 * kStageBytes;
     // Both halves' fragments beside the results, where 256 registers hold them.  (8 x 4:
@@ -316,7 +324,7 @@ struct Gemm {
     {
         const int w = wave & 3, g = lane >> 4;
         if (tj == 4) return 256 + w * 16 + g * 4;
-        return LQ == kInner ? w * 64 + g * 16 + tj * 4 : w * 64 + tj * 16 + g * 4;
+        return kRuns ? w * 64 + g * 16 + tj * 4 : w * 64 + tj * 16 + g * 4;
     }
     static __device__ __forceinline__ int row_of(int ti, int wave, int lane)
     {

@@ -119,18 +119,23 @@ struct AdamwScalars {
     uint64_t seed;
 };
 
-constexpr int64_t kAdamwChunk = 4096;     // elements of a workgroup
+// Elements of a workgroup of the update: 4 blocks of 256 a wave; or one, where the
+// elements are few and more workgroups finish sooner.
+constexpr int64_t kAdamwChunk = 4096, kAdamwSmallChunk = 1024;
+constexpr int64_t kAdamwLarge = 8 << 20;  // elements from which on chunks are large
+constexpr int64_t kAdamwPartials = 2048;  // of the check, at most
 
 struct AdamwLaunch {
     const TensorEntry* tensors;
     const ChunkEntry* chunks;
-    int64_t nchunks;
+    int64_t nchunks, chunk;
     AdamwState* state;
-    double* partial;           // one a chunk
+    double* partial;           // kAdamwPartials
     AdamwScalars s;
 };
 
 hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t s);
+int64_t adamw_chunk(int64_t elements);
 hipError_t adamw_set_state(AdamwState* state, const AdamwState& to, hipStream_t s);
 constexpr int kGradsPerLaunch = 256;
 hipError_t adamw_set_grads(TensorEntry* tensors, const void* const* grads, int64_t first, int count, hipStream_t s);

@@ -275,7 +275,7 @@ struct GradArgs {
     uint32_t ti, tj;          // tiles
     int64_t steps;            // of the whole depth
     int splits;
-    int vector_out;           // 4 results can be stored at once
+    int vector_out;           // results that can be stored at once: 8, 4, or 0
     int sum_in, sum_out;      // the sum is added / is where the result goes
 };
 
@@ -299,6 +299,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void grad_kernel(GradArgs a)
             const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
             if (i >= a.rows) continue;
             T* to = static_cast<T*>(a.out) + i * a.out_ld;
+            if constexpr (G::kRuns && NJ == 4) {
+                const int64_t j = bj * G::kTileJ + G::column_of(0, wave, lane);
+                if (a.vector_out == 8 && j + 16 <= a.cols) {
+                    vec_t<T, 8> y[2];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = to_type<T>(acc[ti][k >> 2][k & 3] * alpha);
+                    reinterpret_cast<vec_t<T, 8>*>(to + j)[0] = y[0];
+                    reinterpret_cast<vec_t<T, 8>*>(to + j)[1] = y[1];
+                    continue;
+                }
+            }
 #pragma unroll
             for (int tj = 0; tj < NJ; ++tj) {
                 const int64_t j = bj * G::kTileJ + G::column_of(tj, wave, lane);
@@ -411,8 +422,10 @@ hipError_t grad(GradArgs g, hipStream_t s)
     if (allowed != hipSuccess) return allowed;
     g.ti = (uint32_t)ceil_div(g.rows, G::kTileI);
     g.tj = (uint32_t)ceil_div(g.cols, G::kTileJ);
-    g.vector_out = ((uintptr_t)g.out & 7) == 0 && g.out_ld % 4 == 0;
-    grad_kernel<T, LP, NI, NJ><<<dim3(g.ti * g.tj * g.splits), kGemmThreads, G::kLds, s>>>(g);
+    g.vector_out = ((uintptr_t)g.out & 15) == 0 && g.out_ld % 8 == 0 ? 8 : ((uintptr_t)g.out & 7) == 0 && g.out_ld % 4 == 0 ? 4 : 0;
+    // a single step has no second stage: more workgroups fit in a CU
+    const int lds = g.steps <= 1 ? G::kStageBytes : G::kLds;
+    grad_kernel<T, LP, NI, NJ><<<dim3(g.ti * g.tj * g.splits), kGemmThreads, lds, s>>>(g);
     return hipSuccess;
 }
 

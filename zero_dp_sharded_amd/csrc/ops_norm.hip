@@ -8,8 +8,9 @@
 // Both directions are bound by memory: 2 (forward) or 3 (backward) rows of D
 // elements, each moved once.  A row stays in registers between its sums and its
 // results; it belongs to one wave where it fits (no barrier at all), else to 4 or
-// 16 waves that join their sums through LDS; a row of more than 16384 elements (of
-// 2 bytes; 8192 of 4) is read again from cache instead.
+// 16 waves that join their sums through LDS; a row of more than 16384 elements is read
+// again from cache instead.  The backward pass reads a row while it works on the one
+// before.
 //
 // The weight's and bias's gradients are sums over all rows: each workgroup keeps
 // the sums of the rows it walks in registers, adds its waves' in LDS, and writes
@@ -42,18 +43,23 @@ __device__ __forceinline__ void row_sum(float& a, float& b, float2* sh)
     }
 }
 
-// The W elements from column c on, as fp32, zeros past the width.
+// The W elements from column c on, zeros past the width.
+template <typename T, int W>
+__device__ __forceinline__ vec_t<T, W> load_raw(const T* row, int64_t c, int64_t width)
+{
+    if (c + W <= width) return load_vec<T, W>(row + c);
+    vec_t<T, W> v;
+#pragma unroll
+    for (int k = 0; k < W; ++k) v[k] = c + k < width ? row[c + k] : static_cast<T>(0.0f);
+    return v;
+}
+
 template <typename T, int W>
 __device__ __forceinline__ void load_part(const T* row, int64_t c, int64_t width, float (&x)[W])
 {
-    if (c + W <= width) {
-        const vec_t<T, W> v = load_vec<T, W>(row + c);
+    const vec_t<T, W> v = load_raw<T, W>(row, c, width);
 #pragma unroll
-        for (int k = 0; k < W; ++k) x[k] = (float)v[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k) x[k] = c + k < width ? (float)row[c + k] : 0.0f;
-    }
+    for (int k = 0; k < W; ++k) x[k] = (float)v[k];
 }
 
 template <typename T, int W>
@@ -181,55 +187,111 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
 // ------------------------------------------------------------------ backward
 
 // A workgroup of WAVES waves, NW to a row, walks rows blockIdx, blockIdx + grid,
-// ... (in groups of WAVES / NW) and keeps its sums for dw and db.
+// ... (in groups of WAVES / NW) and keeps its sums for dw and db.  Up to 4 waves a row,
+// the next row is read meanwhile, and the weight is kept in LDS to have the registers
+// for that; with 16 the registers (128 a lane) do not reach.
 template <typename T, typename A, int NW, int WAVES, int K>
 __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
 {
     constexpr int W = Vec<T>::W;
     constexpr int ROWS = WAVES / NW;
     static_assert(ROWS == 1 || NW == 1, "several rows a workgroup: a wave each");
+    constexpr bool AHEAD = NW <= 4;
     __shared__ float2 sh[NW];
-    extern __shared__ float fold[];            // ROWS > 1: [2][K * 64 * W]
+    // the weight, 4 elements a lane side by side (AHEAD); at the end, with ROWS > 1, the
+    // sums of the waves, [2][K * W][64]
+    extern __shared__ __attribute__((aligned(16))) float fold[];
     const int lane = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int wave = threadIdx.x >> 6;
     const float inv = 1.0f / (float)a.width;
-    float w[K][W], dw[K][W], db[K][W];
+    float held[AHEAD ? 1 : K][W], dw[K][W], db[K][W];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+        float w[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-            w[k][e] = 1.0f;
+            w[e] = 1.0f;
             dw[k][e] = db[k][e] = 0.0f;
         }
         if (a.weight != nullptr)
-            load_part<A, W>(static_cast<const A*>(a.weight), (int64_t)(k * NW * 64 + lane) * W, a.width, w[k]);
+            load_part<A, W>(static_cast<const A*>(a.weight), (int64_t)(k * NW * 64 + lane) * W, a.width, w);
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            if constexpr (AHEAD) fold[((k * (W / 4) + e / 4) * NW * 64 + lane) * 4 + e % 4] = w[e];
+            else held[k][e] = w[e];
+        }
     }
-    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.rows; first += (int64_t)gridDim.x * ROWS) {
-        const int64_t row = NW == 1 ? first + wave : first;
-        if (row >= a.rows) break;              // (only with NW == 1: no barrier is missed)
-        const T* xr = static_cast<const T*>(a.x) + row * a.x_stride;
-        const T* dyr = static_cast<const T*>(a.dy) + row * a.dy_stride;
-        float x[K][W], g[K][W];
+    if constexpr (AHEAD) __syncthreads();
+    auto weight = [&](int k, float (&w)[W]) {
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int q = 0; q < W / 4; ++q) {
+                const vec_t<float, 4> v =
+                    *reinterpret_cast<const vec_t<float, 4>*>(fold + ((k * (W / 4) + q) * NW * 64 + lane) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[q * 4 + e] = v[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) w[e] = held[k][e];
+        }
+    };
+    const int64_t stride = (int64_t)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + (NW == 1 ? wave : 0);
+    vec_t<T, W> nx[K], ng[K];                  // the next row, as it lies in memory
+    auto fetch = [&](int64_t r) {
+        const T* xr = static_cast<const T*>(a.x) + r * a.x_stride;
+        const T* dyr = static_cast<const T*>(a.dy) + r * a.dy_stride;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
-            load_part<T, W>(xr, c, a.width, x[k]);
-            load_part<T, W>(dyr, c, a.width, g[k]);
+            nx[k] = load_raw<T, W>(xr, c, a.width);
+            ng[k] = load_raw<T, W>(dyr, c, a.width);
         }
-        const float mean = a.mean[row], rstd = a.rstd[row];
+    };
+    float nmean = 0.0f, nrstd = 0.0f;
+    if (AHEAD && row < a.rows) {
+        fetch(row);
+        nmean = a.mean[row];
+        nrstd = a.rstd[row];
+    }
+    // (rows of NW == 1 end wave by wave, the others' workgroups together: no barrier is
+    // missed)
+    for (; row < a.rows; row += stride) {
+        if constexpr (!AHEAD) {
+            fetch(row);
+            nmean = a.mean[row];
+            nrstd = a.rstd[row];
+        }
+        float x[K][W], g[K][W];
+        const float mean = nmean, rstd = nrstd;
         float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 // (past the width g is 0, and dw, db stay out of the result)
-                x[k][e] = (x[k][e] - mean) * rstd;
+                x[k][e] = ((float)nx[k][e] - mean) * rstd;
+                g[k][e] = (float)ng[k][e];
+            }
+        if (AHEAD && row + stride < a.rows) {
+            fetch(row + stride);
+            nmean = a.mean[row + stride];
+            nrstd = a.rstd[row + stride];
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float w[W];
+            weight(k, w);
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
                 dw[k][e] += g[k][e] * x[k][e];
                 db[k][e] += g[k][e];
-                g[k][e] *= w[k][e];
+                g[k][e] *= w[e];
                 sg += g[k][e];
                 sgx += g[k][e] * x[k][e];
             }
+        }
         row_sum<NW>(sg, sgx, sh);
         sg *= inv;
         sgx *= inv;
@@ -246,7 +308,8 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
     if (a.partial == nullptr) return;
     float* out = a.partial + (int64_t)blockIdx.x * 2 * a.width;
     if constexpr (ROWS > 1) {
-        // the waves' sums, one wave after the other
+        // the waves' sums, one wave after the other, once all are done with the weight
+        __syncthreads();
         for (int turn = 0; turn < ROWS; ++turn) {
             if (wave == turn) {
 #pragma unroll
@@ -355,8 +418,10 @@ __global__ __launch_bounds__(1024) void fold_kernel(const float* partial, int64_
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;       // of 2 * width columns
     const int64_t p0 = parts * wave / 16, p1 = parts * (wave + 1) / 16;
     float s = 0.0f;
-    if (c < 2 * width)
+    if (c < 2 * width) {
+#pragma unroll 16
         for (int64_t p = p0; p < p1; ++p) s += partial[p * 2 * width + c];
+    }
     sh[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= 2 * width) return;
@@ -371,7 +436,6 @@ __global__ __launch_bounds__(1024) void fold_kernel(const float* partial, int64_
 
 // ------------------------------------------------------------------ launches
 
-constexpr int kBackwardWaves = 8;      // rows of a workgroup where a row is a wave's
 constexpr int64_t kLongRows = 64;      // workgroups over the rows of very long ones
 
 template <typename T, typename A>
@@ -379,14 +443,19 @@ hipError_t forward(const NormForward& a, hipStream_t s)
 {
     constexpr int W = Vec<T>::W;
     if (a.rows == 0) return hipSuccess;
+    // lanes that a row keeps busy with one vector each; a wave keeps up to 64 elements
+    // of a lane in registers
     const int64_t lanes = ceil_div(a.width, W);
     const dim3 by4((unsigned)ceil_div(a.rows, 4)), by1((unsigned)a.rows);
-    if (lanes <= 64) forward_kernel<T, A, 1, 1><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 128) forward_kernel<T, A, 1, 2><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 256) forward_kernel<T, A, 1, 4><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 512) forward_kernel<T, A, 4, 2><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 1024) forward_kernel<T, A, 4, 4><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 2048) forward_kernel<T, A, 16, 2><<<by1, 1024, 0, s>>>(a);
+    constexpr int M = 8 / W;               // vectors of a lane in 8 elements
+    if (lanes <= 64 * M) forward_kernel<T, A, 1, M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 128 * M) forward_kernel<T, A, 1, 2 * M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 256 * M) forward_kernel<T, A, 1, 4 * M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 384 * M) forward_kernel<T, A, 1, 6 * M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 512 * M) forward_kernel<T, A, 4, 2 * M><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 768 * M) forward_kernel<T, A, 4, 3 * M><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 1024 * M) forward_kernel<T, A, 4, 4 * M><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 2048 * M) forward_kernel<T, A, 16, 2 * M><<<by1, 1024, 0, s>>>(a);
     else forward_long_kernel<T, A><<<by1, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -398,19 +467,24 @@ hipError_t backward(const NormBackward& a, hipStream_t s)
     const int64_t lanes = ceil_div(a.width, W);
     int64_t parts = 0;
     if (a.rows > 0) {
-        auto run = [&](auto kernel, int waves, int rows, int k) {
+        // `most` workgroups walk the rows: what their registers let stand in the CUs
+        auto run = [&](auto kernel, int waves, int rows, int k, int64_t most) {
             parts = ceil_div(a.rows, rows);
-            if (parts > kCUs) parts = kCUs;
-            const size_t lds = rows > 1 ? (size_t)2 * k * W * 64 * sizeof(float) : 0;
+            if (parts > most) parts = most;
+            const size_t lds = rows > 1 ? (size_t)2 * k * W * 64 * sizeof(float) : waves == 4 ? (size_t)k * W * 256 * sizeof(float) : 0;
             kernel<<<dim3((unsigned)parts), waves * 64, lds, s>>>(a);
         };
-        constexpr int B = kBackwardWaves;
-        if (lanes <= 64) run(backward_kernel<T, A, 1, B, 1>, B, B, 1);
-        else if (lanes <= 128) run(backward_kernel<T, A, 1, B, 2>, B, B, 2);
-        else if (lanes <= 256) run(backward_kernel<T, A, 1, B, 4>, B, B, 4);
-        else if (lanes <= 512) run(backward_kernel<T, A, 8, 8, 1>, 8, 1, 1);
-        else if (lanes <= 1024) run(backward_kernel<T, A, 16, 16, 1>, 16, 1, 1);
-        else if (lanes <= 2048) run(backward_kernel<T, A, 16, 16, 2>, 16, 1, 2);
+        constexpr int M = 8 / W;           // vectors of a lane in 8 elements
+        if (lanes <= 64 * M) run(backward_kernel<T, A, 1, 16, M>, 16, 16, M, kCUs);
+        else if (lanes <= 128 * M) run(backward_kernel<T, A, 1, 8, 2 * M>, 8, 8, 2 * M, kCUs);
+        else if (lanes <= 256 * M) {
+            // (4-byte rows of this size do not fit a wave's registers twice)
+            if constexpr (W == 8) run(backward_kernel<T, A, 1, 8, 4>, 8, 8, 4, kCUs);
+            else run(backward_kernel<T, A, 4, 4, 2>, 4, 1, 2, 2 * kCUs);
+        }
+        else if (lanes <= 512 * M) run(backward_kernel<T, A, 4, 4, 2 * M>, 4, 1, 2 * M, 2 * kCUs);
+        else if (lanes <= 1024 * M) run(backward_kernel<T, A, 4, 4, 4 * M>, 4, 1, 4 * M, 2 * kCUs);
+        else if (lanes <= 2048 * M) run(backward_kernel<T, A, 16, 16, 2 * M>, 16, 1, 2 * M, kCUs);
         else {
             backward_long_kernel<T, A><<<dim3((unsigned)a.rows), 1024, 0, s>>>(a);
             parts = a.rows < kLongRows ? a.rows : kLongRows;
@@ -428,7 +502,7 @@ hipError_t backward(const NormBackward& a, hipStream_t s)
 
 }  // namespace
 
-int64_t norm_partial_rows(int64_t rows, int64_t) { return rows < kCUs ? (rows < 1 ? 1 : rows) : kCUs; }
+int64_t norm_partial_rows(int64_t rows, int64_t) { return rows < 2 * kCUs ? (rows < 1 ? 1 : rows) : 2 * kCUs; }
 
 hipError_t norm_forward(const NormForward& a, int type, int affine, hipStream_t s)
 {

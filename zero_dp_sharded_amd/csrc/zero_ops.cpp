@@ -156,6 +156,7 @@ zero_status check_place(const Array* a, int n, void* stream, const char* who)
 }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxElements = (int64_t)1 << 40;     // of a handle: 12 TB of fp32 states
 
 // ------------------------------------------------------------------ layer norm
 
@@ -228,7 +229,7 @@ zero_status tensor_arrays(const zero_adamw_tensor& t, int32_t index, int bits, s
     const int32_t type = enum_value(t.type);
     if (!known_type(type)) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d has unknown type %d", who, index, (int)type);
     if (t.numel < 0) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d has numel < 0", who, index);
-    if (t.numel > ((int64_t)1 << 43)) return fail(ZERO_ERR_UNSUPPORTED, "%s: tensor %d has more than 2^43 elements", who, index);
+    if (t.numel > kMaxElements) return fail(ZERO_ERR_UNSUPPORTED, "%s: tensor %d has more than 2^40 elements", who, index);
     if (!(std::isfinite(t.weight_decay))) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d: weight_decay must be finite", who, index);
     if (!(std::isfinite(t.lr_scale) && t.lr_scale >= 0.0)) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d: lr_scale must be finite and >= 0", who, index);
     const size_t n = (size_t)t.numel, e = type_bytes(type), blocks = (n + zo::kStateBlock - 1) / zo::kStateBlock;
@@ -265,7 +266,7 @@ struct zero_adamw_s {
     uint64_t seed = 0;
     zero_adam_hparams hp{};
     zero_loss_scale_cfg ls{};
-    int64_t nchunks = 0;
+    int64_t nchunks = 0, chunk = 0;
     void* ws = nullptr;
     zo::TensorEntry* tensors = nullptr;
     zo::ChunkEntry* chunks = nullptr;
@@ -496,14 +497,14 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
         std::vector<Array> all;
         std::vector<zo::TensorEntry> table((size_t)n);
         std::vector<zo::ChunkEntry> chunks;
+        int64_t elements = 0;
         for (int32_t i = 0; i < n; ++i) {
             const zero_adamw_tensor& t = tensors[i];
             if (const zero_status s = tensor_arrays(t, i, cfg->state_bits, all, who)) return s;
             table[i] = zo::TensorEntry{t.grad, t.master, t.param, t.exp_avg, t.exp_avg_sq, t.exp_avg_exp, t.exp_avg_sq_exp,
                                        t.numel, (float)t.weight_decay, (float)t.lr_scale, enum_value(t.type), 0};
-            if ((int64_t)chunks.size() + t.numel / zo::kAdamwChunk + 1 > kMaxGrid)
-                return fail(ZERO_ERR_UNSUPPORTED, "%s: more than 2^43 elements", who);
-            for (int64_t b = 0; b < t.numel; b += zo::kAdamwChunk) chunks.push_back(zo::ChunkEntry{i, 0, b});
+            elements += t.numel;
+            if (elements > kMaxElements) return fail(ZERO_ERR_UNSUPPORTED, "%s: more than 2^40 elements", who);
         }
         // overlaps of so many arrays by their order in memory
         std::vector<const Array*> order;
@@ -522,6 +523,9 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
             if (a->written && (!written || a->end() > written->end())) written = a;
         }
         if (const zero_status s = check_place(all.data(), (int)all.size(), nullptr, who)) return s;
+        const int64_t chunk = zo::adamw_chunk(elements);
+        for (int32_t i = 0; i < n; ++i)
+            for (int64_t b = 0; b < tensors[i].numel; b += chunk) chunks.push_back(zo::ChunkEntry{i, 0, b});
         zero_adamw_s* h = new zero_adamw_s;
         h->n = n;
         h->bits = cfg->state_bits;
@@ -531,10 +535,11 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
         h->hp = *hp;
         h->ls = *ls;
         h->nchunks = (int64_t)chunks.size();
+        h->chunk = chunk;
         const size_t bt = table.size() * sizeof(table[0]), bc = chunks.size() * sizeof(zo::ChunkEntry);
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
         hipError_t e = hipGetDevice(&h->device);
-        if (e == hipSuccess) e = hipMalloc(&h->ws, up(bt) + up(bc) + up(sizeof(zo::AdamwState)) + up(chunks.size() * 8));
+        if (e == hipSuccess) e = hipMalloc(&h->ws, up(bt) + up(bc) + up(sizeof(zo::AdamwState)) + up(zo::kAdamwPartials * 8));
         if (e == hipSuccess) e = hipHostMalloc((void**)&h->host_state, sizeof(zo::AdamwState));
         if (e != hipSuccess) {
             release(h);
@@ -605,6 +610,7 @@ zero_status zero_adamw_step(zero_adamw_t h, const zero_adam_hparams* hp, void* s
     a.tensors = h->tensors;
     a.chunks = h->chunks;
     a.nchunks = h->nchunks;
+    a.chunk = h->chunk;
     a.state = h->state;
     a.partial = h->partial;
     a.s.b1 = (float)p.beta1;

@@ -105,20 +105,37 @@ def zero_ops_last_error() -> str:
 
 # ------------------------------------------------------------------ marshalling
 
+# torch and what of it every call needs, set by the first call (the library's
+# host-only entry points work without torch)
+torch = None
+_CODES: dict = {}
+
+
+def _load():
+    global torch
+    import torch as module
+    _CODES.update({module.float16: ZERO_FP16, module.bfloat16: ZERO_BF16, module.float32: ZERO_FP32})
+    torch = module
+    return module
+
+
+def _current(stream) -> int:
+    """hipStream_t of a stream, or of torch's current stream if None (by the raw
+    getter: the stream object alone would cost a small call a fifth of its time)."""
+    if stream is not None:
+        return _stream_ptr(stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _type_of(name: str, t) -> int:
-    import torch
-    code = {torch.float16: ZERO_FP16, torch.bfloat16: ZERO_BF16,
-            torch.float32: ZERO_FP32}.get(t.dtype)
+    code = _CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: expected float16, bfloat16 or float32, got {t.dtype}")
     return code
 
 
 def _tensor(name: str, t, dtype) -> None:
-    """A GPU tensor of the dtype (a torch dtype or its name; None: any)."""
-    import torch
-    if isinstance(dtype, str):
-        dtype = getattr(torch, dtype)
+    """A GPU tensor of the dtype (None: any)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     if dtype is not None and t.dtype != dtype:
@@ -127,15 +144,23 @@ def _tensor(name: str, t, dtype) -> None:
         raise ValueError(f"{name}: must live on the GPU, got {t.device}")
 
 
+def _matrix(name: str, t) -> tuple:
+    _tensor(name, t, None)
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions")
+    return t.shape
+
+
 def _rows(name: str, t, dtype, rows: int, width: int) -> tuple:
     """(address, row stride) of a [rows, width] tensor whose last dimension is
     contiguous; its row stride is free."""
     _tensor(name, t, dtype)
-    if t.dim() != 2 or tuple(t.shape) != (rows, width):
+    if t.shape != (rows, width):
         raise ValueError(f"{name}: expected shape ({rows}, {width}), got {tuple(t.shape)}")
-    if width > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if inner != 1 and width > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else max(width, 1))
+    return t.data_ptr(), (stride if rows > 1 else max(width, 1))
 
 
 def _flat(name: str, t, dtype, n: int) -> Optional[int]:
@@ -143,7 +168,7 @@ def _flat(name: str, t, dtype, n: int) -> Optional[int]:
     if t is None:
         return None
     _tensor(name, t, dtype)
-    if not t.is_contiguous() or t.numel() != n:
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous with {n} elements, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -151,7 +176,7 @@ def _flat(name: str, t, dtype, n: int) -> Optional[int]:
 def _space(t) -> tuple:
     if t is None:
         return None, 0
-    _tensor("workspace", t, "uint8")
+    _tensor("workspace", t, torch.uint8)
     if not t.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     return t.data_ptr(), t.numel()
@@ -164,10 +189,8 @@ def zero_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, *, eps: flo
     """y = (x - mean) * rstd * weight + bias over the last of x's two dimensions;
     mean and rstd (fp32, one a row) for the backward pass.  weight and bias (both
     of x's type or both fp32) may be None."""
-    _tensor("x", x, None)
-    if x.dim() != 2:
-        raise ValueError("x: expected two dimensions")
-    rows, width = x.shape
+    torch or _load()
+    rows, width = _matrix("x", x)
     t = _type_of("x", x)
     given = weight if weight is not None else bias
     at = t if given is None else _type_of("weight", given)
@@ -176,8 +199,8 @@ def zero_layernorm_forward(x, weight, bias, y, mean=None, rstd=None, *, eps: flo
     adt = None if given is None else given.dtype
     _check(lib().zero_layernorm_forward(
         xp, xs, _flat("weight", weight, adt, width), _flat("bias", bias, adt, width), rows, width,
-        t, at, eps, yp, ys, _flat("mean", mean, "float32", rows),
-        _flat("rstd", rstd, "float32", rows), _stream_ptr(stream)), "zero_layernorm_forward")
+        t, at, eps, yp, ys, _flat("mean", mean, torch.float32, rows),
+        _flat("rstd", rstd, torch.float32, rows), _current(stream)), "zero_layernorm_forward")
 
 
 def zero_layernorm_workspace(rows: int, width: int) -> int:
@@ -192,10 +215,8 @@ def zero_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=N
     """dx, and (where given) dweight and dbias, for dy and the forward pass's x, mean
     and rstd.  workspace: uint8, zero_layernorm_workspace(rows, width) bytes, needed
     with dweight or dbias."""
-    _tensor("x", x, None)
-    if x.dim() != 2:
-        raise ValueError("x: expected two dimensions")
-    rows, width = x.shape
+    torch or _load()
+    rows, width = _matrix("x", x)
     t = _type_of("x", x)
     given = next((g for g in (weight, dweight, dbias) if g is not None), None)
     at = t if given is None else _type_of("weight", given)
@@ -206,9 +227,9 @@ def zero_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=N
     wp, wn = _space(workspace)
     _check(lib().zero_layernorm_backward(
         dyp, dys, xp, xs, _flat("weight", weight, adt, width),
-        _flat("mean", mean, "float32", rows), _flat("rstd", rstd, "float32", rows), rows,
+        _flat("mean", mean, torch.float32, rows), _flat("rstd", rstd, torch.float32, rows), rows,
         width, t, at, dxp, dxs, _flat("dweight", dweight, adt, width),
-        _flat("dbias", dbias, adt, width), wp, wn, _stream_ptr(stream)), "zero_layernorm_backward")
+        _flat("dbias", dbias, adt, width), wp, wn, _current(stream)), "zero_layernorm_backward")
 
 
 # ------------------------------------------------------------------ vocabulary loss
@@ -229,11 +250,8 @@ def zero_vocab_loss(hidden, weight, targets, losses, lse, loss, dhidden=None, dw
     and targets [tokens] (int64): losses [tokens], lse [tokens] (or None) and the
     mean loss in fp32, and with dhidden and dweight both gradients of the mean
     times grad_scale.  workspace: uint8, zero_vocab_loss_workspace bytes."""
-    _tensor("hidden", hidden, None)
-    _tensor("weight", weight, hidden.dtype)
-    if hidden.dim() != 2 or weight.dim() != 2:
-        raise ValueError("hidden and weight: expected two dimensions")
-    (tokens, width), vocab = hidden.shape, weight.shape[0]
+    torch or _load()
+    (tokens, width), (vocab, _) = _matrix("hidden", hidden), _matrix("weight", weight)
     d = ZeroVocabLossDesc(tokens=tokens, vocab=vocab, width=width, type=_type_of("hidden", hidden),
                           max_tokens=max_tokens, ignore_index=ignore_index, grad_scale=grad_scale)
     hp, d.hidden_stride = _rows("hidden", hidden, hidden.dtype, tokens, width)
@@ -245,9 +263,9 @@ def zero_vocab_loss(hidden, weight, targets, losses, lse, loss, dhidden=None, dw
         dwp, d.dweight_stride = _rows("dweight", dweight, hidden.dtype, vocab, width)
     sp, sn = _space(workspace)
     _check(lib().zero_vocab_loss(
-        ctypes.byref(d), hp, wp, _flat("targets", targets, "int64", tokens),
-        _flat("losses", losses, "float32", tokens), _flat("lse", lse, "float32", tokens),
-        _flat("loss", loss, "float32", 1), dhp, dwp, sp, sn, _stream_ptr(stream)),
+        ctypes.byref(d), hp, wp, _flat("targets", targets, torch.int64, tokens),
+        _flat("losses", losses, torch.float32, tokens), _flat("lse", lse, torch.float32, tokens),
+        _flat("loss", loss, torch.float32, 1), dhp, dwp, sp, sn, _current(stream)),
         "zero_vocab_loss")
 
 
@@ -270,18 +288,19 @@ class AdamWTensor:
     lr_scale: float = 1.0
 
     def to_c(self, state_bits: int) -> ZeroAdamwTensor:
+        torch or _load()
         _tensor("grad", self.grad, None)
         n, t = self.grad.numel(), _type_of("grad", self.grad)
-        state = "float32" if state_bits == 32 else "uint8"
+        state = torch.float32 if state_bits == 32 else torch.uint8
         blocks = -(-n // BLOCK)
         if self.weight_decay is not None and self.weight_decay < 0:
             raise ValueError("weight_decay must be >= 0")
         return ZeroAdamwTensor(
-            n, t, _flat("grad", self.grad, None, n), _flat("master", self.master, "float32", n),
+            n, t, _flat("grad", self.grad, None, n), _flat("master", self.master, torch.float32, n),
             _flat("param", self.param, self.grad.dtype, n), _flat("exp_avg", self.exp_avg, state, n),
             _flat("exp_avg_sq", self.exp_avg_sq, state, n),
-            _flat("exp_avg_exp", self.exp_avg_exp, "int8", blocks),
-            _flat("exp_avg_sq_exp", self.exp_avg_sq_exp, "int8", blocks),
+            _flat("exp_avg_exp", self.exp_avg_exp, torch.int8, blocks),
+            _flat("exp_avg_sq_exp", self.exp_avg_sq_exp, torch.int8, blocks),
             -1.0 if self.weight_decay is None else self.weight_decay, self.lr_scale)
 
 
@@ -304,6 +323,7 @@ def zero_adamw_init(tensors: Sequence[AdamWTensor], *, hp: AdamHParams, ls: Loss
 
 def zero_adamw_set_grads(h: int, grads: Sequence, stream=None) -> None:
     """Other gradient tensors, of the same types and sizes, for the steps that follow."""
+    torch or _load()
     known = _adamw.get(h)
     if known is not None:
         if len(grads) != len(known):
@@ -311,32 +331,36 @@ def zero_adamw_set_grads(h: int, grads: Sequence, stream=None) -> None:
         ptrs = [_flat(f"gradient {i}", g, dt, n) for i, (g, (dt, n)) in enumerate(zip(grads, known))]
     else:
         ptrs = [g.data_ptr() for g in grads]
-    _check(lib().zero_adamw_set_grads(h, (_vp * len(ptrs))(*ptrs), len(ptrs), _stream_ptr(stream)),
+    _check(lib().zero_adamw_set_grads(h, (_vp * len(ptrs))(*ptrs), len(ptrs), _current(stream)),
            "zero_adamw_set_grads")
 
 
 def zero_adamw_step(h: int, hp: Optional[AdamHParams] = None, stream=None) -> None:
     """Enqueue one step of every tensor (capturable in a graph)."""
+    torch or _load()
     hpc = ctypes.byref(hp.to_c()) if hp is not None else None
-    _check(lib().zero_adamw_step(h, hpc, _stream_ptr(stream)), "zero_adamw_step")
+    _check(lib().zero_adamw_step(h, hpc, _current(stream)), "zero_adamw_step")
 
 
 def zero_adamw_result(h: int, stream=None) -> StepInfo:
     """The last step's result; waits for it."""
+    torch or _load()
     out = ZeroStepInfo()
-    _check(lib().zero_adamw_result(h, _stream_ptr(stream), ctypes.byref(out)), "zero_adamw_result")
+    _check(lib().zero_adamw_result(h, _current(stream), ctypes.byref(out)), "zero_adamw_result")
     return StepInfo.from_c(out)
 
 
 def zero_adamw_get_counters(h: int, stream=None):
+    torch or _load()
     t, s, g = _i64(), _f64(), _i64()
-    _check(lib().zero_adamw_get_counters(h, _stream_ptr(stream), ctypes.byref(t), ctypes.byref(s),
+    _check(lib().zero_adamw_get_counters(h, _current(stream), ctypes.byref(t), ctypes.byref(s),
                                          ctypes.byref(g)), "zero_adamw_get_counters")
     return t.value, s.value, g.value
 
 
 def zero_adamw_set_counters(h: int, step_t: int, scale: float, good_steps: int, stream=None) -> None:
-    _check(lib().zero_adamw_set_counters(h, _stream_ptr(stream), step_t, scale, good_steps),
+    torch or _load()
+    _check(lib().zero_adamw_set_counters(h, _current(stream), step_t, scale, good_steps),
            "zero_adamw_set_counters")
 
 
@@ -347,19 +371,21 @@ def zero_adamw_destroy(h: int) -> None:
 
 def zero_moments_pack(x, codes, exps, *, signed: bool, stream=None) -> None:
     """fp32 moments to 8 bits: codes (uint8) and exps (int8, one for every 256 elements)."""
-    _tensor("x", x, "float32")
+    torch or _load()
+    _tensor("x", x, torch.float32)
     n = x.numel()
-    _check(lib().zero_moments_pack(_flat("x", x, "float32", n), n, int(signed),
-                                   _flat("codes", codes, "uint8", n),
-                                   _flat("exps", exps, "int8", -(-n // BLOCK)),
-                                   _stream_ptr(stream)), "zero_moments_pack")
+    _check(lib().zero_moments_pack(_flat("x", x, torch.float32, n), n, int(signed),
+                                   _flat("codes", codes, torch.uint8, n),
+                                   _flat("exps", exps, torch.int8, -(-n // BLOCK)),
+                                   _current(stream)), "zero_moments_pack")
 
 
 def zero_moments_unpack(codes, exps, out, *, signed: bool, stream=None) -> None:
     """What 8-bit moments stand for, into out (fp32 or bf16; exact in both)."""
-    _tensor("codes", codes, "uint8")
+    torch or _load()
+    _tensor("codes", codes, torch.uint8)
     n = codes.numel()
-    _check(lib().zero_moments_unpack(_flat("codes", codes, "uint8", n),
-                                     _flat("exps", exps, "int8", -(-n // BLOCK)), n, int(signed),
+    _check(lib().zero_moments_unpack(_flat("codes", codes, torch.uint8, n),
+                                     _flat("exps", exps, torch.int8, -(-n // BLOCK)), n, int(signed),
                                      _type_of("out", out), _flat("out", out, None, n),
-                                     _stream_ptr(stream)), "zero_moments_unpack")
+                                     _current(stream)), "zero_moments_unpack")
