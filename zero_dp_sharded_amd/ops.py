@@ -304,20 +304,21 @@ class AdamWTensor:
             -1.0 if self.weight_decay is None else self.weight_decay, self.lr_scale)
 
 
-# sizes and types of the tensors of each live handle made through this binding
+# the tensors of each live handle made through this binding (kept from being freed
+# under it), and the gradients given since
 _adamw = {}
 
 
 def zero_adamw_init(tensors: Sequence[AdamWTensor], *, hp: AdamHParams, ls: LossScaleCfg,
                     state_bits: int = 32, checked: bool = True, max_grad_norm: float = 0.0,
                     seed: int = 0) -> int:
-    """A handle over the tensors; their arrays must outlive it."""
+    """A handle over the tensors, which are kept alive until it is destroyed."""
     arr = (ZeroAdamwTensor * len(tensors))(*[t.to_c(state_bits) for t in tensors])
     cfg = ZeroAdamwCfg(state_bits, int(checked), max_grad_norm, seed)
     h = _vp()
     _check(lib().zero_adamw_init(arr, len(tensors), ctypes.byref(hp.to_c()), ctypes.byref(ls.to_c()),
                                  ctypes.byref(cfg), ctypes.byref(h)), "zero_adamw_init")
-    _adamw[h.value] = [(t.grad.dtype, t.grad.numel()) for t in tensors]
+    _adamw[h.value] = [list(tensors), [t.grad for t in tensors]]
     return h.value
 
 
@@ -326,13 +327,15 @@ def zero_adamw_set_grads(h: int, grads: Sequence, stream=None) -> None:
     torch or _load()
     known = _adamw.get(h)
     if known is not None:
-        if len(grads) != len(known):
-            raise ValueError(f"expected {len(known)} gradients, got {len(grads)}")
-        ptrs = [_flat(f"gradient {i}", g, dt, n) for i, (g, (dt, n)) in enumerate(zip(grads, known))]
+        if len(grads) != len(known[1]):
+            raise ValueError(f"expected {len(known[1])} gradients, got {len(grads)}")
+        ptrs = [_flat(f"gradient {i}", g, old.dtype, old.numel()) for i, (g, old) in enumerate(zip(grads, known[1]))]
     else:
         ptrs = [g.data_ptr() for g in grads]
     _check(lib().zero_adamw_set_grads(h, (_vp * len(ptrs))(*ptrs), len(ptrs), _current(stream)),
            "zero_adamw_set_grads")
+    if known is not None:
+        known[1] = list(grads)
 
 
 def zero_adamw_step(h: int, hp: Optional[AdamHParams] = None, stream=None) -> None:
