@@ -7,8 +7,8 @@
 //
 // Both directions are bound by memory: 2 (forward) or 3 (backward) rows of D
 // elements, each moved once.  A row stays in registers between its sums and its
-// results; it belongs to one wave where it fits (no barrier at all), else to 4 or
-// 16 waves that join their sums through LDS; a row of more than 16384 elements is read
+// results; it belongs to one wave where it fits (no barrier at all), else to 4, 8
+// or 16 waves that join their sums through LDS; a row of more than 16384 elements is read
 // again from cache instead.  The backward pass reads a row while it works on the one
 // before.
 //
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void forward_kernel(NormFo
 #pragma unroll
         for (int e = 0; e < W; ++e) {
             v[k][e] = c + e < a.width ? v[k][e] - mean : 0.0f;
-            q += v[k][e] * v[k][e];
+            q = fmaf(v[k][e], v[k][e], q);
         }
     }
     row_sum<NW>(q, unused, sh);
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void forward_kernel(NormFo
         if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
         if (a.bias != nullptr) load_part<A, W>(static_cast<const A*>(a.bias), c, a.width, b);
 #pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = v[k][e] * rstd * w[e] + b[e];
+        for (int e = 0; e < W; ++e) w[e] = fmaf(v[k][e] * rstd, w[e], b[e]);
         store_part<T, W>(y, c, a.width, w);
     }
 }
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
         load_part<T, W>(x, c, a.width, v);
 #pragma unroll
         for (int e = 0; e < W; ++e)
-            if (c + e < a.width) q += (v[e] - mean) * (v[e] - mean);
+            if (c + e < a.width) q = fmaf(v[e] - mean, v[e] - mean, q);
     }
     unused = 0.0f;
     row_sum<16>(q, unused, sh);
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
         if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
         if (a.bias != nullptr) load_part<A, W>(static_cast<const A*>(a.bias), c, a.width, b);
 #pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = (v[e] - mean) * rstd * w[e] + b[e];
+        for (int e = 0; e < W; ++e) w[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
         store_part<T, W>(y, c, a.width, w);
     }
 }
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
 // A workgroup of WAVES waves, NW to a row, walks rows blockIdx, blockIdx + grid,
 // ... (in groups of WAVES / NW) and keeps its sums for dw and db.  Up to 4 waves a row,
 // the next row is read meanwhile, and the weight is kept in LDS to have the registers
-// for that; with 16 the registers (128 a lane) do not reach.
+// for that; with 8, LDS does not reach: the weight is read row by row from cache.
 template <typename T, typename A, int NW, int WAVES, int K>
 __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
 {
@@ -204,24 +204,28 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
     const int lane = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int wave = threadIdx.x >> 6;
     const float inv = 1.0f / (float)a.width;
-    float held[AHEAD ? 1 : K][W], dw[K][W], db[K][W];
+    float dw[K][W], db[K][W];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        float w[W];
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            w[e] = 1.0f;
-            dw[k][e] = db[k][e] = 0.0f;
-        }
+        for (int e = 0; e < W; ++e) dw[k][e] = db[k][e] = 0.0f;
+    }
+    auto load_weight = [&](int k, float (&w)[W]) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = 1.0f;
         if (a.weight != nullptr)
             load_part<A, W>(static_cast<const A*>(a.weight), (int64_t)(k * NW * 64 + lane) * W, a.width, w);
+    };
+    if constexpr (AHEAD) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            if constexpr (AHEAD) fold[((k * (W / 4) + e / 4) * NW * 64 + lane) * 4 + e % 4] = w[e];
-            else held[k][e] = w[e];
+        for (int k = 0; k < K; ++k) {
+            float w[W];
+            load_weight(k, w);
+#pragma unroll
+            for (int e = 0; e < W; ++e) fold[((k * (W / 4) + e / 4) * NW * 64 + lane) * 4 + e % 4] = w[e];
         }
+        __syncthreads();
     }
-    if constexpr (AHEAD) __syncthreads();
     auto weight = [&](int k, float (&w)[W]) {
         if constexpr (AHEAD) {
 #pragma unroll
@@ -232,8 +236,7 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
                 for (int e = 0; e < 4; ++e) w[q * 4 + e] = v[e];
             }
         } else {
-#pragma unroll
-            for (int e = 0; e < W; ++e) w[e] = held[k][e];
+            load_weight(k, w);
         }
     };
     const int64_t stride = (int64_t)gridDim.x * ROWS;
@@ -285,11 +288,11 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
             weight(k, w);
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                dw[k][e] += g[k][e] * x[k][e];
+                dw[k][e] = fmaf(g[k][e], x[k][e], dw[k][e]);
                 db[k][e] += g[k][e];
                 g[k][e] *= w[e];
                 sg += g[k][e];
-                sgx += g[k][e] * x[k][e];
+                sgx = fmaf(g[k][e], x[k][e], sgx);
             }
         }
         row_sum<NW>(sg, sgx, sh);
@@ -301,7 +304,7 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
             const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
             if (c >= a.width) continue;
 #pragma unroll
-            for (int e = 0; e < W; ++e) g[k][e] = rstd * (g[k][e] - sg - x[k][e] * sgx);
+            for (int e = 0; e < W; ++e) g[k][e] = rstd * fmaf(-x[k][e], sgx, g[k][e] - sg);
             store_part<T, W>(dxr, c, a.width, g[k]);
         }
     }
@@ -367,9 +370,9 @@ __global__ __launch_bounds__(1024) void backward_long_kernel(NormBackward a)
                 const float xhat = (x[e] - mean) * rstd;
                 if (turn == 0) {
                     sg += g[e];
-                    sgx += g[e] * xhat;
+                    sgx = fmaf(g[e], xhat, sgx);
                 } else {
-                    g[e] = rstd * (g[e] - sg - xhat * sgx);
+                    g[e] = rstd * fmaf(-xhat, sgx, g[e] - sg);
                 }
             }
             if (turn == 1) store_part<T, W>(dxr, c, a.width, g);
@@ -399,7 +402,7 @@ __global__ __launch_bounds__(256) void columns_long_kernel(NormBackward a, int64
         const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-            dw[e] += g[e] * ((x[e] - mean) * rstd);
+            dw[e] = fmaf(g[e], (x[e] - mean) * rstd, dw[e]);
             db[e] += g[e];
         }
     }
@@ -484,7 +487,7 @@ hipError_t backward(const NormBackward& a, hipStream_t s)
         }
         else if (lanes <= 512 * M) run(backward_kernel<T, A, 4, 4, 2 * M>, 4, 1, 2 * M, 2 * kCUs);
         else if (lanes <= 1024 * M) run(backward_kernel<T, A, 4, 4, 4 * M>, 4, 1, 4 * M, 2 * kCUs);
-        else if (lanes <= 2048 * M) run(backward_kernel<T, A, 16, 16, 2 * M>, 16, 1, 2 * M, kCUs);
+        else if (lanes <= 2048 * M) run(backward_kernel<T, A, 8, 8, 4 * M>, 8, 1, 4 * M, kCUs);
         else {
             backward_long_kernel<T, A><<<dim3((unsigned)a.rows), 1024, 0, s>>>(a);
             parts = a.rows < kLongRows ? a.rows : kLongRows;
