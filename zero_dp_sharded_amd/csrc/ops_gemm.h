@@ -130,7 +130,8 @@ struct Inner {
     {
         return runs ? (row & 3) | ((row >> 4) & 1) << 2 : row & 7;
     }
-    __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k0, int wave, int lane)
+    // The tile from row0 and k0 on.
+    __device__ __forceinline__ void begin(const Operand& o, int64_t row0, int64_t k0)
     {
         piece.base = static_cast<const char*>(o.base) + (row0 * o.ld + k0) * 2;
         int64_t rows = o.rows - row0;
@@ -138,6 +139,10 @@ struct Inner {
         piece.left = ((rows - 1) * o.ld + o.depth - k0) * 2;
         piece.step = kDeep * 2;
         k_left = o.depth - k0;
+    }
+    // What a lane loads of any tile.
+    __device__ __forceinline__ void lanes(const Operand& o, int wave, int lane)
+    {
         // load q of wave w: rows 64 q + 8 w to + 7, with the key of row 8 w + ...
         const int row = wave * 8 + (lane >> 3);
         const int chunk = (lane & 7) ^ key(row, RUNS);
@@ -153,9 +158,11 @@ struct Inner {
     __device__ __forceinline__ void issue(uint32_t lds, int wave)
     {
         const u4 rsrc = piece.descriptor();
+        uint32_t first = voff;
+        asm volatile("" : "+v"(first));      // (added to here, not kept C times in registers)
 #pragma unroll
         for (int q = 0; q < C; ++q) {
-            uint32_t v = chunk_k >= k_left ? kOutOfRange : voff + q * apart;
+            uint32_t v = chunk_k >= k_left ? kOutOfRange : first + q * apart;
             if constexpr (C == 5 && RUNS)
                 if (q == 4) v = chunk_k_last >= k_left ? kOutOfRange : voff_last;
             load_to_lds(v, rsrc, lds + (q * 8 + wave) * 1024);
@@ -238,9 +245,11 @@ struct Outer256 {
     }
     __device__ __forceinline__ void issue(const u4& rsrc, uint32_t lds, int wave)
     {
+        uint32_t first[2] = {voff[0], voff[1]};
+        asm volatile("" : "+v"(first[0]), "+v"(first[1]));
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            load_to_lds(voff[q & 1] + (q >> 1) * apart, rsrc, lds + (wave * 4 + q) * 1024);
+            load_to_lds(first[q & 1] + (q >> 1) * apart, rsrc, lds + (wave * 4 + q) * 1024);
     }
     __device__ __forceinline__ void reader(uint32_t lds, int w0, int lane)
     {
@@ -272,11 +281,14 @@ struct Outer {
     Outer256<RUNS> wide;
     Outer64 narrow;
 
-    __device__ __forceinline__ void init(const Operand& o, int64_t col0, int64_t k0, int wave, int lane)
+    __device__ __forceinline__ void begin(const Operand& o, int64_t col0, int64_t k0)
     {
         piece.base = static_cast<const char*>(o.base) + (k0 * o.ld + col0) * 2;
         piece.left = ((o.depth - k0 - 1) * o.ld + o.rows - col0) * 2;
         piece.step = kDeep * o.ld * 2;
+    }
+    __device__ __forceinline__ void lanes(const Operand& o, int wave, int lane)
+    {
         if constexpr (C >= 4) wide.init(o.ld, wave, lane);
         if constexpr (C != 4) narrow.init(o.ld, C == 5 ? 256 : 0, wave, lane);
     }
@@ -304,8 +316,10 @@ template <Layout L, int C, bool RUNS> struct Side;
 template <int C, bool RUNS> struct Side<kInner, C, RUNS> { using type = Inner<C, RUNS>; };
 template <int C, bool RUNS> struct Side<kOuter, C, RUNS> { using type = Outer<C, RUNS>; };
 
-// acc[ti][tj][e]: i = tile's i0 + 16 NI (wave / 4) + 16 ti + lane % 16; j by
-// column_of() below.  `steps` of kDeep from k0 on.
+// acc[ti][tj][e]: i by row_of(), j by column_of() below, within the tile.  One tile:
+// begin(), then run(); a workgroup that goes on to another tile begins it from run()'s
+// `free`, which is called when both stages have been read, so that its loads are under
+// way during the last products and whatever is done with the results.
 template <typename T, Layout LP, Layout LQ, int NI, int NJ>
 struct Gemm {
     static constexpr int kTileI = 32 * NI, kTileJ = 64 * NJ;
@@ -358,31 +372,46 @@ struct Gemm {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    // smem: LDS address, a multiple of 1024.
-    static __device__ __forceinline__ void run(const Operand& P, const Operand& Q, int64_t i0, int64_t j0,
-                                               int64_t k0, int steps, uint32_t smem, f4 (&acc)[NI][NJ])
+    PSide p;
+    QSide q;
+    int wave;
+    uint32_t smem;
+
+    // lds: address of kLds bytes (kStageBytes where every tile has one step), a multiple
+    // of 1024.
+    __device__ __forceinline__ Gemm(const Operand& P, const Operand& Q, uint32_t lds) : smem(lds)
     {
         const int lane = threadIdx.x & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        PSide p;
-        QSide q;
-        p.init(P, i0, k0, wave, lane);
-        q.init(Q, j0, k0, wave, lane);
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        p.lanes(P, wave, lane);
+        q.lanes(Q, wave, lane);
         p.reader(smem, wave >> 2, NI, lane);
         q.reader(smem + PSide::kBytes, wave & 3, NJ, lane);
+    }
+    __device__ __forceinline__ void issue(uint32_t stage)
+    {
+        p.issue(smem + stage, wave);
+        q.issue(smem + stage + PSide::kBytes, wave);
+    }
+    // Start on the tile at (i0, j0), `steps` of kDeep from k0 on.
+    __device__ __forceinline__ void begin(const Operand& P, const Operand& Q, int64_t i0, int64_t j0, int64_t k0,
+                                          int steps)
+    {
+        p.begin(P, i0, k0);
+        q.begin(Q, j0, k0);
+        if (steps > 0) issue(0);
+        if (steps > 1) issue(kStageBytes);
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(int steps, f4 (&acc)[NI][NJ], F free)
+    {
 #pragma unroll
         for (int ti = 0; ti < NI; ++ti)
 #pragma unroll
             for (int tj = 0; tj < NJ; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
-        if (steps <= 0) return;
-        auto issue = [&](uint32_t stage) {
-            p.issue(smem + stage, wave);
-            q.issue(smem + stage + PSide::kBytes, wave);
-        };
+        if (steps <= 0) return free();
         Half even;
-        issue(0);
         turn();
-        if (steps > 1) issue(kStageBytes);
         if constexpr (kAhead) {
             // Fragments of half a step are read while the half before is multiplied; the
             // step's barrier stands between its halves, where the other half's
@@ -396,6 +425,7 @@ struct Gemm {
                 turn();
                 if (s + 2 < steps) issue(stage);
                 if (s + 1 < steps) read(even, p, q, other, 0);
+                else free();
                 multiply(odd, acc);
             }
         } else {
@@ -406,6 +436,7 @@ struct Gemm {
                 read(even, p, q, stage, 1);
                 turn();
                 if (s + 2 < steps) issue(stage);
+                if (s + 1 == steps) free();
                 multiply(even, acc);
             }
         }

@@ -35,14 +35,20 @@ template <typename T> constexpr float kHoldLog2 = 32.0f;        // factor of wha
 template <> constexpr float kHoldLog2<_Float16> = 15.0f;
 template <typename T> constexpr float kHold = (float)(1ull << (int)kHoldLog2<T>);
 
-// Workgroup -> tile.  Workgroups go round the 8 dies; each die gets a run of tiles
-// that lie together (8 tiles of i by all of j, column by column), so that its L2
-// serves the operands' pieces to the tiles that share them.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t ti, uint32_t tj, int64_t& i, int64_t& j)
+// The n-th tile of those that die `die` of 8 takes.  Workgroups go round the dies;
+// each die gets a run of tiles that lie together (8 tiles of i by all of j, column by
+// column), so that its L2 serves the operands' pieces to the tiles that share them.
+constexpr uint32_t kDies = 8;
+
+__device__ __forceinline__ uint32_t tiles_of(uint32_t die, uint32_t all)
 {
-    constexpr uint32_t kDies = 8, kGroup = 8;
-    const uint32_t all = ti * tj, die = id % kDies, at = id / kDies;
-    const uint32_t q = all / kDies, r = all % kDies;
+    return all / kDies + (die < all % kDies ? 1 : 0);
+}
+
+__device__ __forceinline__ void tile_of(uint32_t die, uint32_t at, uint32_t ti, uint32_t tj, int64_t& i, int64_t& j)
+{
+    constexpr uint32_t kGroup = 8;
+    const uint32_t q = ti * tj / kDies, r = ti * tj % kDies;
     const uint32_t n = die * q + (die < r ? die : r) + at;
     const uint32_t per = kGroup * tj, g = n / per;
     const uint32_t first = g * kGroup;
@@ -72,18 +78,16 @@ struct LogitsArgs {
     uint32_t ti, tj;          // tiles
 };
 
+// From a tile's logits to the pieces' statistics and the exponentials.
 template <typename T, int NI, int NJ>
-__global__ __launch_bounds__(kGemmThreads, 2) void logits_kernel(LogitsArgs a)
+__device__ __forceinline__ void logits_out(const LogitsArgs& a, int64_t bi, int64_t bj, f4 (&acc)[NI][NJ])
 {
     using G = Gemm<T, kInner, kInner, NI, NJ>;
-    constexpr int R = 4 * NJ;                                  // a lane's ids, side by side
-    extern __shared__ __attribute__((aligned(1024))) char smem[];
-    int64_t bi, bj;
-    tile_of(blockIdx.x, a.ti, a.tj, bi, bj);
-    f4 acc[NI][NJ];
-    G::run(a.h, a.w, bi * G::kTileI, bj * G::kTileJ, 0, (int)ceil_div(a.h.depth, kDeep), lds_address(smem), acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // the lane's ids: 16 from v on, and with NJ = 5 another 4 from `far` on
+    constexpr int R = 4 * NJ;                                  // a lane's ids
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));      // (addresses are made here, and not kept in registers over the products)
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // 16 from v on, and with NJ = 5 another 4 from `far` on
     const int64_t v = bj * G::kTileJ + G::column_of(0, wave, lane);
     const int64_t far = bj * G::kTileJ + G::column_of(4, wave, lane) - 16;       // (id of k >= 16: far + k)
     if (bj * G::kTileJ + (wave & 3) * 64 >= a.vocab_ld) return;                  // (NJ = 4: past the last piece)
@@ -136,6 +140,37 @@ __global__ __launch_bounds__(kGemmThreads, 2) void logits_kernel(LogitsArgs a)
                 if constexpr (NJ == 5) *reinterpret_cast<vec_t<T, 4>*>(to + far + 16) = held[4];
             }
         }
+    }
+}
+
+// A die's workgroups walk its tiles, and load the next one while they are at a tile's
+// exponentials (a tile of width 1600 is 25 steps of 2 us, its exponentials 7 us and its
+// first loads 3).
+template <typename T, int NI, int NJ>
+__global__ __launch_bounds__(kGemmThreads, 2) void logits_kernel(LogitsArgs a)
+{
+    using G = Gemm<T, kInner, kInner, NI, NJ>;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const uint32_t die = blockIdx.x % kDies, mine = tiles_of(die, a.ti * a.tj);
+    const uint32_t stride = (gridDim.x + kDies - 1 - die) / kDies;       // workgroups of the die
+    const int steps = (int)ceil_div(a.h.depth, kDeep);
+    G g(a.h, a.w, lds_address(smem));
+    int64_t bi = 0, bj = 0;
+    uint32_t at = blockIdx.x / kDies;
+    if (at >= mine) return;
+    tile_of(die, at, a.ti, a.tj, bi, bj);
+    g.begin(a.h, a.w, bi * G::kTileI, bj * G::kTileJ, 0, steps);
+    for (;;) {
+        f4 acc[NI][NJ];
+        const int64_t i = bi, j = bj;
+        at += stride;
+        g.run(steps, acc, [&] {
+            if (at >= mine) return;
+            tile_of(die, at, a.ti, a.tj, bi, bj);
+            g.begin(a.h, a.w, bi * G::kTileI, bj * G::kTileJ, 0, steps);
+        });
+        logits_out<T, NI, NJ>(a, i, j, acc);
+        if (at >= mine) return;
     }
 }
 
@@ -284,13 +319,15 @@ __global__ __launch_bounds__(kGemmThreads, 2) void grad_kernel(GradArgs a)
 {
     using G = Gemm<T, LP, kOuter, NI, NJ>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    const uint32_t tiles = a.ti * a.tj;
+    const uint32_t tiles = a.ti * a.tj, id = blockIdx.x % tiles;
     const int64_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
     int64_t bi, bj;
-    tile_of(blockIdx.x % tiles, a.ti, a.tj, bi, bj);
+    tile_of(id % kDies, id / kDies, a.ti, a.tj, bi, bj);
     const int64_t s0 = a.steps * split / a.splits, s1 = a.steps * (split + 1) / a.splits;
     f4 acc[NI][NJ];
-    G::run(a.p, a.q, bi * G::kTileI, bj * G::kTileJ, s0 * kDeep, (int)(s1 - s0), lds_address(smem), acc);
+    G g(a.p, a.q, lds_address(smem));
+    g.begin(a.p, a.q, bi * G::kTileI, bj * G::kTileJ, s0 * kDeep, (int)(s1 - s0));
+    g.run((int)(s1 - s0), acc, [] {});
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float alpha = a.alpha[0];
     if (a.part == nullptr && !a.sum_in && !a.sum_out && a.vector_out) {       // as good as always
@@ -410,7 +447,9 @@ hipError_t logits(LogitsArgs l, hipStream_t s)
     if (allowed != hipSuccess) return allowed;
     l.ti = (uint32_t)ceil_div(l.tokens, G::kTileI);
     l.tj = (uint32_t)ceil_div(l.vocab, G::kTileJ);
-    logits_kernel<T, NI, NJ><<<dim3(l.ti * l.tj), kGemmThreads, G::kLds, s>>>(l);
+    // as many workgroups as stand in the CUs at once: one, or two of the small tile's
+    const uint32_t stand = kCUs * (NI == 2 ? 2 : 1), tiles = l.ti * l.tj;
+    logits_kernel<T, NI, NJ><<<dim3(tiles < stand ? tiles : stand), kGemmThreads, G::kLds, s>>>(l);
     return hipSuccess;
 }
 
