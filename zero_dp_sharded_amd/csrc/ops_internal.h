@@ -124,12 +124,13 @@ struct AdamwScalars {
 constexpr int64_t kAdamwChunk = 4096, kAdamwSmallChunk = 1024;
 constexpr int64_t kAdamwLarge = 8 << 20;  // elements from which on chunks are large
 constexpr int64_t kAdamwPartials = 2048;  // of the check, at most
+constexpr int64_t kAdamwInline = 512;     // that the update adds itself
 
 struct AdamwLaunch {
     const TensorEntry* tensors;
     const ChunkEntry* chunks;
     int64_t nchunks, chunk;
-    AdamwState* state;
+    AdamwState* state;         // and a copy beside it
     double* partial;           // kAdamwPartials
     AdamwScalars s;
 };

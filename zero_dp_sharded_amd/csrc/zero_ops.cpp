@@ -91,9 +91,29 @@ bool overlap(const Array& a, const Array& b)
     return true;
 }
 
-// The runtime's view of an array: see device_range_ok of the shard's ABI.
+zero_status past_end(const Array& a, hipDeviceptr_t base, size_t size, const char* who)
+{
+    if (a.end() <= (uintptr_t)base + size) return ZERO_OK;
+    return fail(ZERO_ERR_INVALID_ARG, "%s: %s runs %zu bytes past the end of its allocation", who, a.name,
+                (size_t)(a.end() - ((uintptr_t)base + size)));
+}
+
+// The runtime's view of an array: memory of this device, and its range inside its
+// allocation.  With one GPU in the system an allocation that the runtime knows can be
+// of no other, and one question is enough (two for each of six arrays are half of a
+// small call's time).
 zero_status on_device(const Array& a, int dev, const char* who)
 {
+    static const bool alone = [] {
+        int n = 0;
+        return hipGetDeviceCount(&n) == hipSuccess && n == 1;
+    }();
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    if (alone) {
+        if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)a.p) == hipSuccess) return past_end(a, base, size, who);
+        (void)hipGetLastError();
+    }
     hipPointerAttribute_t t;
     if (hipPointerGetAttributes(&t, a.p) != hipSuccess) {
         (void)hipGetLastError();
@@ -104,15 +124,8 @@ zero_status on_device(const Array& a, int dev, const char* who)
     if (t.type == hipMemoryTypeDevice) {
         if (t.device != dev)
             return fail(ZERO_ERR_INVALID_ARG, "%s: %s is memory of device %d, the current one is %d", who, a.name, t.device, dev);
-        hipDeviceptr_t base = nullptr;
-        size_t size = 0;
-        if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)a.p) == hipSuccess) {
-            if (a.end() > (uintptr_t)base + size)
-                return fail(ZERO_ERR_INVALID_ARG, "%s: %s runs %zu bytes past the end of its allocation", who, a.name,
-                            (size_t)(a.end() - ((uintptr_t)base + size)));
-        } else {
-            (void)hipGetLastError();
-        }
+        if (hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)a.p) == hipSuccess) return past_end(a, base, size, who);
+        (void)hipGetLastError();
     }
     return ZERO_OK;
 }
@@ -539,7 +552,7 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
         const size_t bt = table.size() * sizeof(table[0]), bc = chunks.size() * sizeof(zo::ChunkEntry);
         auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
         hipError_t e = hipGetDevice(&h->device);
-        if (e == hipSuccess) e = hipMalloc(&h->ws, up(bt) + up(bc) + up(sizeof(zo::AdamwState)) + up(zo::kAdamwPartials * 8));
+        if (e == hipSuccess) e = hipMalloc(&h->ws, up(bt) + up(bc) + up(2 * sizeof(zo::AdamwState)) + up(zo::kAdamwPartials * 8));
         if (e == hipSuccess) e = hipHostMalloc((void**)&h->host_state, sizeof(zo::AdamwState));
         if (e != hipSuccess) {
             release(h);
@@ -550,7 +563,7 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
         h->tensors = reinterpret_cast<zo::TensorEntry*>(at);
         h->chunks = reinterpret_cast<zo::ChunkEntry*>(at + up(bt));
         h->state = reinterpret_cast<zo::AdamwState*>(at + up(bt) + up(bc));
-        h->partial = reinterpret_cast<double*>(at + up(bt) + up(bc) + up(sizeof(zo::AdamwState)));
+        h->partial = reinterpret_cast<double*>(at + up(bt) + up(bc) + up(2 * sizeof(zo::AdamwState)));
         const zo::AdamwState first = state_of(h, hp->initial_step, ls->init_scale, 0);
         e = hipMemcpy(h->tensors, table.data(), bt, hipMemcpyHostToDevice);
         if (e == hipSuccess && bc) e = hipMemcpy(h->chunks, chunks.data(), bc, hipMemcpyHostToDevice);
