@@ -97,9 +97,9 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
  * tokens = 0: loss 0, dweight zeros.
  * Tokens are taken max_tokens at a time (0: 8192), with the workspace's size in
  * proportion; the gradient of the weight is then summed in fp32 in the workspace.
- * Performance: where an operand's address is not a multiple of 16 bytes, or its
- * stride or the width not a multiple of 8 elements, both operands are copied into
- * the workspace first.
+ * Performance: both operands are copied into the workspace first where the width is
+ * no multiple of 8, and either where its address is no multiple of 4 bytes or its
+ * stride is odd.
  */
 typedef struct {
     int64_t tokens, vocab, width;

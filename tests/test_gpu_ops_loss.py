@@ -145,6 +145,20 @@ def test_strides_and_addresses():
         assert not dhb[:, :3].any() and not dhb[:, 67:].any() and not dwb[:, 0].any()
 
 
+@pytest.mark.parametrize("n,v,d,pad", [(50, 333, 70, 0), (5, 700, 1380, 0), (130, 300, 67, 1), (9, 129, 1, 1), (200, 513, 66, 4),
+                                       (60, 270, 64, 2), (140, 700, 328, 6), (17, 99, 8, 10), (300, 90, 258, 0), (1000, 100, 40, 0),
+                                       (2115, 788, 256, 0)])
+def test_what_lies_between_rows_and_behind_them_is_not_used(n, v, d, pad):
+    """NaN between the rows and behind the last, at widths that are a multiple of 8 and
+    that are none; and products of few tiles and long depth, which go in parts."""
+    h, w, targets = make(n, v, d, torch.bfloat16, seed=n + d)
+    big = [torch.full((rows + 1, d + pad), float("nan"), dtype=torch.bfloat16, device=DEV)[:rows, :d] for rows in (n, v)]
+    big[0].copy_(h)
+    big[1].copy_(w)
+    targets[n // 2] = -100
+    check(big[0], big[1], targets, run(big[0], big[1], targets))
+
+
 def test_ignored_unknown_and_no_tokens():
     h, w, targets = make(30, 90, 64, torch.float16, seed=6)
     # none counts: loss 0, gradients 0, whatever the logits

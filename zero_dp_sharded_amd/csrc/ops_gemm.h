@@ -62,9 +62,10 @@ template <> struct Mfma<_Float16> {
 };
 
 // Where an operand lies: `rows` i (or j) by `depth` k, 2-byte elements.  kInner:
-// element (i, k) at i * ld + k, `depth` a multiple of 8.  kOuter: at k * ld + i,
-// `rows` a multiple of 8.  Base 16-byte aligned, ld a multiple of 8,
+// element (i, k) at i * ld + k; kOuter: at k * ld + i.  Base 4-byte aligned, ld even,
 // ld <= 2^21 (an offset inside a tile stays below 2^31 - 16 bytes).
+// Loads are of 8 elements: a kInner depth is a multiple of 8; what a kOuter tile reads
+// beyond `rows` goes into results that are none.
 struct Operand {
     const void* base;
     int64_t ld;
@@ -96,6 +97,10 @@ struct Piece {
         left -= step;
     }
 };
+
+// The range check goes by words of 4 bytes: the one that an odd count of elements
+// ends in is loaded.
+__device__ __forceinline__ int64_t whole_words(int64_t bytes) { return (bytes + 3) & ~(int64_t)3; }
 
 // One load of 1 KiB into LDS at byte address `lds`: the lane's 16 bytes at offset v.
 // It is done when the wave's vmcnt says so.  Written as assembly because the
@@ -136,7 +141,7 @@ struct Inner {
         piece.base = static_cast<const char*>(o.base) + (row0 * o.ld + k0) * 2;
         int64_t rows = o.rows - row0;
         rows = rows < C * 64 ? rows : C * 64;
-        piece.left = ((rows - 1) * o.ld + o.depth - k0) * 2;
+        piece.left = whole_words(((rows - 1) * o.ld + o.depth - k0) * 2);
         piece.step = kDeep * 2;
         k_left = o.depth - k0;
     }
@@ -284,7 +289,7 @@ struct Outer {
     __device__ __forceinline__ void begin(const Operand& o, int64_t col0, int64_t k0)
     {
         piece.base = static_cast<const char*>(o.base) + (k0 * o.ld + col0) * 2;
-        piece.left = ((o.depth - k0 - 1) * o.ld + o.rows - col0) * 2;
+        piece.left = whole_words(((o.depth - k0 - 1) * o.ld + o.rows - col0) * 2);
         piece.step = kDeep * o.ld * 2;
     }
     __device__ __forceinline__ void lanes(const Operand& o, int wave, int lane)

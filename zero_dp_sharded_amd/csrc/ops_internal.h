@@ -52,7 +52,7 @@ struct LossPlan {              // what a call's sizes settle
     int64_t pieces;            // of a token's ids, with statistics each
     int64_t width_ld;          // the width in whole chunks of 8
     TileChoice logits_tile, hidden_tile, weight_tile;
-    int splits;                // parts of the vocabulary of the hidden states' gradient
+    int hidden_splits, weight_splits;      // parts of the gradients' products
     // byte offsets into the workspace
     int64_t off_alpha, off_target, off_lse, off_stats, off_exp, off_split, off_sum, off_hidden, off_weight;
     int64_t bytes;

@@ -23,6 +23,8 @@
 // What is held is G times 2^15 (fp16) or 2^32 (bf16), taken back in the products'
 // epilogues: entries far below the type's normal range stay.
 
+#include <type_traits>
+
 #include "ops_common.h"
 #include "ops_gemm.h"
 #include "ops_internal.h"
@@ -411,25 +413,40 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const float* part, int
     store_vec<T, W>(out + at / cols * out_ld + at % cols, y);
 }
 
-// Rows of any stride and alignment to rows of ld, a multiple of 8, zeros behind the width.
+// Rows of any stride and alignment to rows of ld, a multiple of 8, zeros behind the
+// width: of one array or, from workgroup `first` on, of another.
 template <typename T>
-__global__ __launch_bounds__(256) void repack_kernel(const T* x, int64_t stride, int64_t rows, int64_t width,
-                                                     T* out, int64_t ld)
+struct Repack {
+    const T* x;
+    T* out;
+    int64_t stride, rows;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void repack_kernel(Repack<T> a, Repack<T> b, int64_t first, int64_t width, int64_t ld)
 {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (at >= rows * ld) return;
-    const int64_t r = at / ld, c = at % ld;
+    const bool second = blockIdx.x >= first;
+    const Repack<T> r = second ? b : a;
+    const int64_t at = ((blockIdx.x - (second ? first : 0)) * 256 + threadIdx.x) * 8;
+    if (at >= r.rows * ld) return;
+    const int64_t i = at / ld, c = at % ld;
+    const T* x = r.x + i * r.stride + c;
     vec_t<T, 8> y;
+    if (c + 8 <= width) {
+        y = load_vec<T, 8>(x);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = c + k < width ? x[r * stride + c + k] : to_type<T>(0.0f);
-    *reinterpret_cast<vec_t<T, 8>*>(out + at) = y;
+        for (int k = 0; k < 8; ++k) y[k] = c + k < width ? x[k] : to_type<T>(0.0f);
+    }
+    *reinterpret_cast<vec_t<T, 8>*>(r.out + at) = y;
 }
 
 // ------------------------------------------------------------------ launches
 
-bool loads_as_it_is(const void* p, int64_t stride, int64_t width)
+// What the products' loads need of an address and a stride.
+bool loads_as_it_is(const void* p, int64_t stride)
 {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && width % 8 == 0 && stride <= (1 << 21);
+    return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && stride % 2 == 0 && stride <= (1 << 21);
 }
 
 // A kernel's LDS beyond 64 KiB is asked for once.
@@ -487,18 +504,26 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
     const T* h = static_cast<const T*>(a.hidden);
     const T* w = static_cast<const T*>(a.weight);
     int64_t h_ld = a.hidden_stride, w_ld = a.weight_stride;
-    if (!loads_as_it_is(h, h_ld, p.width) || !loads_as_it_is(w, w_ld, p.width)) {
-        T* hp = reinterpret_cast<T*>(a.space + p.off_hidden);
-        T* wp = reinterpret_cast<T*>(a.space + p.off_weight);
-        auto repack = [&](const T* x, int64_t stride, int64_t rows, T* out) {
-            if (rows > 0)
-                repack_kernel<T><<<dim3((unsigned)ceil_div(rows * p.width_ld, 2048)), 256, 0, s>>>(x, stride, rows, p.width, out, p.width_ld);
-        };
-        repack(h, h_ld, p.tokens, hp);
-        repack(w, w_ld, p.vocab, wp);
-        h = hp;
-        w = wp;
-        h_ld = w_ld = p.width_ld;
+    // operands whose rows cannot be loaded as they lie, 8 elements at a time
+    Repack<T> copies[2];
+    int many = 0;
+    if (!loads_as_it_is(h, h_ld) || p.width % 8 != 0) {
+        T* to = reinterpret_cast<T*>(a.space + p.off_hidden);
+        copies[many++] = Repack<T>{h, to, h_ld, p.tokens};
+        h = to;
+        h_ld = p.width_ld;
+    }
+    if (!loads_as_it_is(w, w_ld) || p.width % 8 != 0) {
+        T* to = reinterpret_cast<T*>(a.space + p.off_weight);
+        copies[many++] = Repack<T>{w, to, w_ld, p.vocab};
+        w = to;
+        w_ld = p.width_ld;
+    }
+    if (many > 0) {
+        const int64_t first = ceil_div(copies[0].rows * p.width_ld, 2048);
+        const int64_t all = first + (many > 1 ? ceil_div(copies[1].rows * p.width_ld, 2048) : 0);
+        if (all > 0)
+            repack_kernel<T><<<dim3((unsigned)all), 256, 0, s>>>(copies[0], copies[many - 1], first, p.width, p.width_ld);
     }
     auto total = [&](float* loss) {
         total_kernel<<<1, 1024, 0, s>>>(a.targets, a.losses, p.tokens, a.ignore_index, a.grad_scale, kHold<T>, alpha, loss);
@@ -509,7 +534,7 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         if (gradient) {                    // a sum over no tokens
             GradArgs g{};
             g.p = Operand{w, p.vocab_ld, p.vocab_ld, 0};
-            g.q = Operand{w, w_ld, p.width_ld, 0};
+            g.q = Operand{w, w_ld, p.width, 0};
             g.alpha = alpha;
             g.rows = p.vocab;
             g.cols = p.width;
@@ -543,47 +568,85 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         GradArgs g{};
         g.alpha = alpha;
         g.cols = p.width;
-        // dH = G W: k runs over the vocabulary, in parts where that fills the card
+        // A product, in parts of its depth where that fills the card.
+        auto product = [&](auto layout, int splits, const TileChoice& tile) {
+            constexpr Layout LP = decltype(layout)::value;
+            g.splits = splits;
+            g.part = splits > 1 ? reinterpret_cast<float*>(a.space + p.off_split) : nullptr;
+            const hipError_t err = grad<T, LP>(g, tile, s);
+            if (err != hipSuccess || splits == 1) return err;
+            T* out = static_cast<T*>(g.out);
+            const int64_t all = g.rows * g.cols;
+            if (g.cols % 4 == 0)
+                join_splits_kernel<T, 4><<<dim3((unsigned)ceil_div(all, 1024)), 256, 0, s>>>(g.part, splits, g.rows, g.cols, alpha, out, g.out_ld);
+            else
+                join_splits_kernel<T, 1><<<dim3((unsigned)ceil_div(all, 256)), 256, 0, s>>>(g.part, splits, g.rows, g.cols, alpha, out, g.out_ld);
+            return hipSuccess;
+        };
+        // dH = G W: k runs over the vocabulary
         g.p = Operand{exps, p.vocab_ld, n, p.vocab_ld};
-        g.q = Operand{w, w_ld, p.width_ld, p.vocab};
+        g.q = Operand{w, w_ld, p.width, p.vocab};
         g.rows = n;
         g.steps = p.vocab_ld / kDeep;
-        g.splits = p.splits;
         g.out = static_cast<T*>(a.dhidden) + n0 * a.dhidden_stride;
         g.out_ld = a.dhidden_stride;
-        g.part = p.splits > 1 ? reinterpret_cast<float*>(a.space + p.off_split) : nullptr;
-        e = grad<T, kInner>(g, p.hidden_tile, s);
+        e = product(std::integral_constant<Layout, kInner>{}, p.hidden_splits, p.hidden_tile);
         if (e != hipSuccess) return e;
-        if (p.splits > 1) {
-            T* out = static_cast<T*>(g.out);
-            if (p.width % 4 == 0)
-                join_splits_kernel<T, 4><<<dim3((unsigned)ceil_div(n * p.width, 1024)), 256, 0, s>>>(
-                    g.part, p.splits, n, p.width, alpha, out, g.out_ld);
-            else
-                join_splits_kernel<T, 1><<<dim3((unsigned)ceil_div(n * p.width, 256)), 256, 0, s>>>(
-                    g.part, p.splits, n, p.width, alpha, out, g.out_ld);
-        }
         // dW = G^T H: k runs over the chunk's tokens; with several chunks the sum
         // stays in fp32 until the last
         g.p = Operand{exps, p.vocab_ld, p.vocab_ld, n};
         g.q = Operand{oh.base, h_ld, p.width_ld, n};
         g.rows = p.vocab;
         g.steps = ceil_div(n, kDeep);
-        g.splits = 1;
         g.out = a.dweight;
         g.out_ld = a.dweight_stride;
-        g.part = nullptr;
         g.sum = reinterpret_cast<float*>(a.space + p.off_sum);
         g.sum_in = n0 > 0;
         g.sum_out = !last;
-        e = grad<T, kOuter>(g, p.weight_tile, s);
+        e = product(std::integral_constant<Layout, kOuter>{}, p.weight_splits, p.weight_tile);
     }
     return e != hipSuccess ? e : hipGetLastError();
 }
 
 // Rows up to which tiles of 64 are taken instead of 256.  At 16 tokens x 50257 x 1600
-// they take 29, 30 and 64 us for the three products, against 38, 41 and 65.
+// they take 29, 30 and 44 us for the three products, against 38, 41 and 65.
 constexpr int64_t kFewRows = 128;
+
+// Rounds of tiles over the card.
+int64_t rounds_of(int64_t rows, int64_t cols, const TileChoice& c, int64_t splits)
+{
+    return ceil_div(ceil_div(rows, 32 * c.ni) * ceil_div(cols, 64 * c.nj) * splits, kCUs * (c.ni == 2 ? 2 : 1));
+}
+
+// The tile of a gradient's product of `steps` steps, and into how many parts its depth
+// goes, by what they should take: a step of 256 x 256 x 64 is 1.6 us, of 256 x 320
+// 1.2 times that (at 8192 x 1600 x 50257 the weight's gradient takes 1124 us with it, in 4
+// rounds, and 1350 without, in 6), of 64 x 256, two to a CU, 0.8; a round's beginning and
+// end 4; and the parts go through memory at 4 TB/s, and through a launch.
+TileChoice choose(int64_t rows, int64_t cols, int64_t steps, bool may_split, int* splits)
+{
+    const bool few = rows <= kFewRows;
+    TileChoice tile{few ? 2 : 8, 4};
+    double best = 0.0;
+    *splits = 1;
+    for (int nj = 4; nj <= (few ? 4 : 5); ++nj) {
+        const TileChoice c{few ? 2 : 8, nj};
+        // no part of less than 8 steps, and no more than four rounds of them
+        const int64_t tiles = ceil_div(rows, 32 * c.ni) * ceil_div(cols, 64 * c.nj);
+        const int64_t most = may_split ? (steps + 7) / 8 : 1;
+        for (int64_t k = 1; k <= most && (k == 1 || tiles * k <= 4 * kCUs); ++k) {
+            const double step = few ? 0.8 : nj == 5 ? 1.92 : 1.6;
+            const double t = rounds_of(rows, cols, c, k) * (ceil_div(steps, k) * step + 4.0) +
+                             (k > 1 ? 2.0 * k * rows * cols * 4 / 4e6 + 5.0 : 0.0);
+            if (best == 0.0 || t < best) {
+                best = t;
+                tile = c;
+                *splits = (int)k;
+            }
+        }
+    }
+    return tile;
+}
 
 }  // namespace
 
@@ -596,44 +659,17 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chu
     p.width_ld = round_up(width, 8);
     p.chunk = tokens < max_chunk ? tokens : max_chunk;
     if (p.chunk < 1) p.chunk = 1;
-    // A tile of 256 x 320 takes 1.2 times as long as one of 256 x 256 (at 8192 x 1600 x
-    // 50257 the weight's gradient takes 1124 us instead of 1350, in 4 rounds of tiles
-    // instead of 6): the fewer rounds over the card, so weighed, win.
-    auto rounds = [](int64_t rows, int64_t cols, int nj, int64_t splits) {
-        return ceil_div(ceil_div(rows, 256) * ceil_div(cols, 64 * nj) * splits, kCUs);
-    };
-    auto wide = [&](int64_t rows, int64_t cols) {
-        return rounds(rows, cols, 5, 1) * 6 < rounds(rows, cols, 4, 1) * 5 ? 5 : 4;
-    };
-    const bool few = p.chunk <= kFewRows;
-    p.logits_tile = few ? TileChoice{2, 4} : TileChoice{8, wide(p.chunk, vocab)};
-    p.weight_tile = few ? TileChoice{2, 4} : TileChoice{8, wide(vocab, width)};
+    // the logits: no parts; the larger tile where its rounds are fewer by enough
+    const TileChoice narrow{8, 4}, wide{8, 5};
+    p.logits_tile = p.chunk <= kFewRows ? TileChoice{2, 4}
+                    : rounds_of(p.chunk, vocab, wide, 1) * 6 < rounds_of(p.chunk, vocab, narrow, 1) * 5 ? wide : narrow;
     p.vocab_ld = round_up(vocab, p.logits_tile.nj == 5 ? 320 : 64);      // whole pieces, whole steps
     p.pieces = p.vocab_ld / (16 * p.logits_tile.nj);
-    const int64_t steps = p.vocab_ld / kDeep;
-    p.splits = 1;
-    if (few) {
-        // parts of the vocabulary until every CU has a tile, none with less than 8 steps
-        p.hidden_tile = TileChoice{2, 4};
-        int64_t splits = kCUs / (ceil_div(p.chunk, 64) * ceil_div(width, 256));
-        if (splits > steps / 8) splits = steps / 8;
-        p.splits = splits < 1 ? 1 : (int)splits;
-    } else {
-        // the hidden states' gradient has few tiles and a long depth: of the tiles and
-        // parts, those that take the least, a step of 256 x 256 x 64 being 1.6 us, and the
-        // parts' way through memory 4 TB/s
-        double best = 0.0;
-        for (int nj = 4; nj <= 5; ++nj)
-            for (int64_t k = 1; k <= 16 && k <= (steps + 7) / 8; ++k) {
-                const double t = rounds(p.chunk, width, nj, k) * ceil_div(steps, k) * 1.6 * (nj == 5 ? 1.2 : 1.0) +
-                                 (k > 1 ? 2.0 * k * p.chunk * width * 4 / 4e6 + 5.0 : 0.0);
-                if (best == 0.0 || t < best) {
-                    best = t;
-                    p.hidden_tile = TileChoice{8, nj};
-                    p.splits = (int)k;
-                }
-            }
-    }
+    p.hidden_tile = choose(p.chunk, width, p.vocab_ld / kDeep, true, &p.hidden_splits);
+    p.weight_tile = choose(vocab, width, ceil_div(p.chunk, kDeep), p.chunk >= tokens, &p.weight_splits);
+    if (p.chunk <= kFewRows) p.weight_tile = TileChoice{2, 4};           // one or two steps: storing is what takes the time
+    const int64_t parts_hidden = p.hidden_splits > 1 ? p.hidden_splits * p.chunk * width : 0;
+    const int64_t parts_weight = p.weight_splits > 1 ? p.weight_splits * vocab * width : 0;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t off = at;
@@ -645,7 +681,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chu
     p.off_lse = take(tokens * 4);
     p.off_stats = take(p.chunk * p.pieces * 8);
     p.off_exp = take(gradient ? p.chunk * p.vocab_ld * 2 : 0);
-    p.off_split = take(gradient && p.splits > 1 ? p.splits * p.chunk * width * 4 : 0);
+    p.off_split = take(gradient ? (parts_hidden > parts_weight ? parts_hidden : parts_weight) * 4 : 0);
     p.off_sum = take(gradient && p.chunk < tokens ? vocab * width * 4 : 0);
     p.off_hidden = take(tokens * p.width_ld * 2);
     p.off_weight = take(vocab * p.width_ld * 2);
