@@ -23,6 +23,11 @@
 namespace zo {
 namespace {
 
+// PAST: results of more bytes than the L2s hold (4 MiB for each of 8 dies) are written past
+// them, so that what is still to be read stays there: 16384 rows of 1600 bf16 forward
+// 36.8 -> 27.8 us, backward 46.4 -> 44.6.  Smaller ones stay for their reader.
+constexpr int64_t kCaches = 32 << 20;
+
 // Sum of a and b over the NW waves of a row, the same in each.
 template <int NW>
 __device__ __forceinline__ void row_sum(float& a, float& b, float2* sh)
@@ -62,14 +67,14 @@ __device__ __forceinline__ void load_part(const T* row, int64_t c, int64_t width
     for (int k = 0; k < W; ++k) x[k] = (float)v[k];
 }
 
-template <typename T, int W>
+template <bool PAST = false, typename T, int W>
 __device__ __forceinline__ void store_part(T* row, int64_t c, int64_t width, const float (&x)[W])
 {
     if (c + W <= width) {
         vec_t<T, W> v;
 #pragma unroll
         for (int k = 0; k < W; ++k) v[k] = static_cast<T>(x[k]);
-        store_vec<T, W>(row + c, v);
+        store_vec<T, W, PAST>(row + c, v);
     } else {
 #pragma unroll
         for (int k = 0; k < W; ++k)
@@ -80,7 +85,7 @@ __device__ __forceinline__ void store_part(T* row, int64_t c, int64_t width, con
 // ------------------------------------------------------------------ forward
 
 // NW waves a row, K vectors a lane; with NW == 1 a workgroup has 4 rows.
-template <typename T, typename A, int NW, int K>
+template <typename T, typename A, bool PAST, int NW, int K>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void forward_kernel(NormForward a)
 {
     constexpr int W = Vec<T>::W;
@@ -131,12 +136,12 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void forward_kernel(NormFo
         if (a.bias != nullptr) load_part<A, W>(static_cast<const A*>(a.bias), c, a.width, b);
 #pragma unroll
         for (int e = 0; e < W; ++e) w[e] = fmaf(v[k][e] * rstd, w[e], b[e]);
-        store_part<T, W>(y, c, a.width, w);
+        store_part<PAST>(y, c, a.width, w);
     }
 }
 
 // Rows too long for registers: 16 waves walk the row three times.
-template <typename T, typename A>
+template <typename T, typename A, bool PAST>
 __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
 {
     constexpr int W = Vec<T>::W;
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
         if (a.bias != nullptr) load_part<A, W>(static_cast<const A*>(a.bias), c, a.width, b);
 #pragma unroll
         for (int e = 0; e < W; ++e) w[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
-        store_part<T, W>(y, c, a.width, w);
+        store_part<PAST>(y, c, a.width, w);
     }
 }
 
@@ -190,7 +195,7 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(NormForward a)
 // ... (in groups of WAVES / NW) and keeps its sums for dw and db.  Up to 4 waves a row,
 // the next row is read meanwhile, and the weight is kept in LDS to have the registers
 // for that; with 8, LDS does not reach: the weight is read row by row from cache.
-template <typename T, typename A, int NW, int WAVES, int K>
+template <typename T, typename A, bool PAST, int NW, int WAVES, int K>
 __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
 {
     constexpr int W = Vec<T>::W;
@@ -305,7 +310,7 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
             if (c >= a.width) continue;
 #pragma unroll
             for (int e = 0; e < W; ++e) g[k][e] = rstd * fmaf(-x[k][e], sgx, g[k][e] - sg);
-            store_part<T, W>(dxr, c, a.width, g[k]);
+            store_part<PAST>(dxr, c, a.width, g[k]);
         }
     }
     if (a.partial == nullptr) return;
@@ -336,14 +341,14 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
     for (int k = 0; k < K; ++k) {
         const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
         if (c >= a.width) continue;
-        store_part<float, W>(out, c, a.width, dw[k]);
-        store_part<float, W>(out + a.width, c, a.width, db[k]);
+        store_part(out, c, a.width, dw[k]);
+        store_part(out + a.width, c, a.width, db[k]);
     }
 }
 
 // Rows too long for registers: dx row by row, and the sums for dw and db over
 // slabs of rows, a lane W columns.
-template <typename T, typename A>
+template <typename T, typename A, bool PAST>
 __global__ __launch_bounds__(1024) void backward_long_kernel(NormBackward a)
 {
     constexpr int W = Vec<T>::W;
@@ -375,7 +380,7 @@ __global__ __launch_bounds__(1024) void backward_long_kernel(NormBackward a)
                     g[e] = rstd * fmaf(-xhat, sgx, g[e] - sg);
                 }
             }
-            if (turn == 1) store_part<T, W>(dxr, c, a.width, g);
+            if (turn == 1) store_part<PAST>(dxr, c, a.width, g);
         }
         if (turn == 0) {
             row_sum<16>(sg, sgx, sh);
@@ -407,8 +412,8 @@ __global__ __launch_bounds__(256) void columns_long_kernel(NormBackward a, int64
         }
     }
     float* out = a.partial + (int64_t)blockIdx.y * 2 * a.width;
-    store_part<float, W>(out, c, a.width, dw);
-    store_part<float, W>(out + a.width, c, a.width, db);
+    store_part(out, c, a.width, dw);
+    store_part(out + a.width, c, a.width, db);
 }
 
 // dw and db: the partial rows, added in 16 runs by 16 waves, the runs in order.
@@ -441,8 +446,8 @@ __global__ __launch_bounds__(1024) void fold_kernel(const float* partial, int64_
 
 constexpr int64_t kLongRows = 64;      // workgroups over the rows of very long ones
 
-template <typename T, typename A>
-hipError_t forward(const NormForward& a, hipStream_t s)
+template <typename T, typename A, bool PAST>
+hipError_t forward_rows(const NormForward& a, hipStream_t s)
 {
     constexpr int W = Vec<T>::W;
     if (a.rows == 0) return hipSuccess;
@@ -451,20 +456,20 @@ hipError_t forward(const NormForward& a, hipStream_t s)
     const int64_t lanes = ceil_div(a.width, W);
     const dim3 by4((unsigned)ceil_div(a.rows, 4)), by1((unsigned)a.rows);
     constexpr int M = 8 / W;               // vectors of a lane in 8 elements
-    if (lanes <= 64 * M) forward_kernel<T, A, 1, M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 128 * M) forward_kernel<T, A, 1, 2 * M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 256 * M) forward_kernel<T, A, 1, 4 * M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 384 * M) forward_kernel<T, A, 1, 6 * M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 512 * M) forward_kernel<T, A, 4, 2 * M><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 768 * M) forward_kernel<T, A, 4, 3 * M><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 1024 * M) forward_kernel<T, A, 4, 4 * M><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 2048 * M) forward_kernel<T, A, 16, 2 * M><<<by1, 1024, 0, s>>>(a);
-    else forward_long_kernel<T, A><<<by1, 1024, 0, s>>>(a);
+    if (lanes <= 64 * M) forward_kernel<T, A, PAST, 1, M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 128 * M) forward_kernel<T, A, PAST, 1, 2 * M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 256 * M) forward_kernel<T, A, PAST, 1, 4 * M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 384 * M) forward_kernel<T, A, PAST, 1, 6 * M><<<by4, 256, 0, s>>>(a);
+    else if (lanes <= 512 * M) forward_kernel<T, A, PAST, 4, 2 * M><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 768 * M) forward_kernel<T, A, PAST, 4, 3 * M><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 1024 * M) forward_kernel<T, A, PAST, 4, 4 * M><<<by1, 256, 0, s>>>(a);
+    else if (lanes <= 2048 * M) forward_kernel<T, A, PAST, 16, 2 * M><<<by1, 1024, 0, s>>>(a);
+    else forward_long_kernel<T, A, PAST><<<by1, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <typename T, typename A>
-hipError_t backward(const NormBackward& a, hipStream_t s)
+template <typename T, typename A, bool PAST>
+hipError_t backward_rows(const NormBackward& a, hipStream_t s)
 {
     constexpr int W = Vec<T>::W;
     const int64_t lanes = ceil_div(a.width, W);
@@ -478,18 +483,18 @@ hipError_t backward(const NormBackward& a, hipStream_t s)
             kernel<<<dim3((unsigned)parts), waves * 64, lds, s>>>(a);
         };
         constexpr int M = 8 / W;           // vectors of a lane in 8 elements
-        if (lanes <= 64 * M) run(backward_kernel<T, A, 1, 16, M>, 16, 16, M, kCUs);
-        else if (lanes <= 128 * M) run(backward_kernel<T, A, 1, 8, 2 * M>, 8, 8, 2 * M, kCUs);
+        if (lanes <= 64 * M) run(backward_kernel<T, A, PAST, 1, 16, M>, 16, 16, M, kCUs);
+        else if (lanes <= 128 * M) run(backward_kernel<T, A, PAST, 1, 8, 2 * M>, 8, 8, 2 * M, kCUs);
         else if (lanes <= 256 * M) {
             // (4-byte rows of this size do not fit a wave's registers twice)
-            if constexpr (W == 8) run(backward_kernel<T, A, 1, 8, 4>, 8, 8, 4, kCUs);
-            else run(backward_kernel<T, A, 4, 4, 2>, 4, 1, 2, 2 * kCUs);
+            if constexpr (W == 8) run(backward_kernel<T, A, PAST, 1, 8, 4>, 8, 8, 4, kCUs);
+            else run(backward_kernel<T, A, PAST, 4, 4, 2>, 4, 1, 2, 2 * kCUs);
         }
-        else if (lanes <= 512 * M) run(backward_kernel<T, A, 4, 4, 2 * M>, 4, 1, 2 * M, 2 * kCUs);
-        else if (lanes <= 1024 * M) run(backward_kernel<T, A, 4, 4, 4 * M>, 4, 1, 4 * M, 2 * kCUs);
-        else if (lanes <= 2048 * M) run(backward_kernel<T, A, 8, 8, 4 * M>, 8, 1, 4 * M, kCUs);
+        else if (lanes <= 512 * M) run(backward_kernel<T, A, PAST, 4, 4, 2 * M>, 4, 1, 2 * M, 2 * kCUs);
+        else if (lanes <= 1024 * M) run(backward_kernel<T, A, PAST, 4, 4, 4 * M>, 4, 1, 4 * M, 2 * kCUs);
+        else if (lanes <= 2048 * M) run(backward_kernel<T, A, PAST, 8, 8, 4 * M>, 8, 1, 4 * M, kCUs);
         else {
-            backward_long_kernel<T, A><<<dim3((unsigned)a.rows), 1024, 0, s>>>(a);
+            backward_long_kernel<T, A, PAST><<<dim3((unsigned)a.rows), 1024, 0, s>>>(a);
             parts = a.rows < kLongRows ? a.rows : kLongRows;
             const int64_t slab = ceil_div(a.rows, parts);
             parts = ceil_div(a.rows, slab);
@@ -501,6 +506,18 @@ hipError_t backward(const NormBackward& a, hipStream_t s)
         fold_kernel<A><<<dim3((unsigned)ceil_div(2 * a.width, 64)), 1024, 0, s>>>(
             a.partial, parts, a.width, static_cast<A*>(a.dweight), static_cast<A*>(a.dbias));
     return hipGetLastError();
+}
+
+template <typename T, typename A>
+hipError_t forward(const NormForward& a, hipStream_t s)
+{
+    return a.rows * a.width * (int64_t)sizeof(T) > kCaches ? forward_rows<T, A, true>(a, s) : forward_rows<T, A, false>(a, s);
+}
+
+template <typename T, typename A>
+hipError_t backward(const NormBackward& a, hipStream_t s)
+{
+    return a.rows * a.width * (int64_t)sizeof(T) > kCaches ? backward_rows<T, A, true>(a, s) : backward_rows<T, A, false>(a, s);
 }
 
 }  // namespace
