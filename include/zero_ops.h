@@ -170,7 +170,7 @@ typedef struct zero_adamw_s* zero_adamw_t; /* opaque */
  * counter and the loss scale live in device memory.
  * Errors: INVALID_ARG (NULL, n < 1, numel < 0, a tensor's arrays NULL, misaligned
  * or not those of its state_bits and type, overlaps, values out of range,
- * max_grad_norm without checked), UNSUPPORTED (n > 2^20, more than 2^40 elements),
+ * max_grad_norm without checked), UNSUPPORTED (n > 2^20, more than 2^38 elements),
  * OOM, HIP.
  */
 zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const zero_adam_hparams* hp,

@@ -39,6 +39,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 constexpr int kExpLeast = -100;       // the smallest power of two a block has
 constexpr int kExpNaN = 127;          // a block that holds nothing finite
 constexpr int kThreads = 256;
+constexpr int kLds = 160 * 1024;      // of a CU
 
 template <int TYPE> struct Stored;
 template <> struct Stored<1> { using T = _Float16; };
@@ -146,12 +147,12 @@ __device__ __forceinline__ float divide_by(float x, float c, float r)
 }
 
 // 4 elements from e on of an array of n, zeros past the end.
-template <typename T>
+template <bool NT = false, typename T>
 __device__ __forceinline__ f4 load4(const T* p, int64_t e, int64_t n)
 {
     f4 x;
     if (e + 4 <= n) {
-        const vec_t<T, 4> v = load_vec<T, 4>(p + e);
+        const vec_t<T, 4> v = load_vec<T, 4, NT>(p + e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = (float)v[k];
     } else {
@@ -161,14 +162,14 @@ __device__ __forceinline__ f4 load4(const T* p, int64_t e, int64_t n)
     return x;
 }
 
-template <typename T>
+template <bool NT = false, typename T>
 __device__ __forceinline__ void store4(T* p, int64_t e, int64_t n, f4 x)
 {
     if (e + 4 <= n) {
         vec_t<T, 4> v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = static_cast<T>(x[k]);
-        store_vec<T, 4>(p + e, v);
+        store_vec<T, 4, NT>(p + e, v);
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -176,10 +177,11 @@ __device__ __forceinline__ void store4(T* p, int64_t e, int64_t n, f4 x)
     }
 }
 
+template <bool NT = false>
 __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t e, int64_t n)
 {
     if (e + 4 <= n) {
-        const vec_t<uint8_t, 4> v = load_vec<uint8_t, 4>(p + e);
+        const vec_t<uint8_t, 4> v = load_vec<uint8_t, 4, NT>(p + e);
         return __builtin_bit_cast(uint32_t, v);
     }
     uint32_t x = 0;
@@ -189,10 +191,11 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t e, int6
     return x;
 }
 
+template <bool NT = false>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t e, int64_t n, uint32_t x)
 {
     if (e + 4 <= n) {
-        store_vec<uint8_t, 4>(p + e, __builtin_bit_cast(vec_t<uint8_t, 4>, x));
+        store_vec<uint8_t, 4, NT>(p + e, __builtin_bit_cast(vec_t<uint8_t, 4>, x));
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -342,30 +345,31 @@ __device__ __forceinline__ void adam(float g, float& p, float& m, float& v, cons
     p = p - lr * u;
 }
 
-// U: blocks of 256 elements a wave.  `decided` gives the step's state, once the loads
-// are under way.
-template <int TYPE, int BITS, int U, typename F>
-__device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const TensorEntry& t, const ChunkEntry& c,
-                                             F decided)
+// U: blocks of 256 elements a wave, those of a workgroup's waves side by side.
+// `decided` gives the step's state, once the loads are under way.
+template <int TYPE, int BITS, int WAVES, int U, bool NT, typename F>
+__device__ __forceinline__ void update_part(const AdamwLaunch& a, const TensorEntry& t, int32_t tensor, int64_t begin,
+                                            F decided)
 {
+    constexpr int kStep = WAVES * kStateBlock;
     using T = typename Stored<TYPE>::T;
     const int64_t n = t.numel;
     const int lane = threadIdx.x & 63;
     f4 g[U], p[U], m[U], v[U];
     uint32_t cm[U], cv[U];
     int bm[U], bv[U];
-    const int64_t e0 = c.begin + threadIdx.x * 4;
+    const int64_t e0 = begin + threadIdx.x * 4;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t e = e0 + u * kThreads * 4;
-        g[u] = load4(static_cast<const T*>(t.grad), e, n);
-        p[u] = load4(t.master, e, n);
+        const int64_t e = e0 + u * kStep;
+        g[u] = load4<NT>(static_cast<const T*>(t.grad), e, n);
+        p[u] = load4<NT>(t.master, e, n);
         if constexpr (BITS == 32) {
-            m[u] = load4(static_cast<const float*>(t.m), e, n);
-            v[u] = load4(static_cast<const float*>(t.v), e, n);
+            m[u] = load4<NT>(static_cast<const float*>(t.m), e, n);
+            v[u] = load4<NT>(static_cast<const float*>(t.v), e, n);
         } else {
-            cm[u] = load_codes(static_cast<const uint8_t*>(t.m), e, n);
-            cv[u] = load_codes(static_cast<const uint8_t*>(t.v), e, n);
+            cm[u] = load_codes<NT>(static_cast<const uint8_t*>(t.m), e, n);
+            cv[u] = load_codes<NT>(static_cast<const uint8_t*>(t.v), e, n);
             const int64_t b = e / kStateBlock, last = (n - 1) / kStateBlock;
             bm[u] = t.m_exp[b < last ? b : last];
             bv[u] = t.v_exp[b < last ? b : last];
@@ -376,10 +380,10 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const TensorE
     const float wd = t.weight_decay < 0.0f ? a.s.wd : t.weight_decay, lr = a.s.lr * t.lr_scale;
     const float r1 = 1.0f / d.bc1, r2 = 1.0f / d.bc2;
     uint32_t key = 0;
-    if constexpr (BITS == 8) key = noise_key(a.s.seed, d.t, c.tensor, c.begin);
+    if constexpr (BITS == 8) key = noise_key(a.s.seed, d.t, tensor, begin);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t e = e0 + u * kThreads * 4;
+        const int64_t e = e0 + u * kStep;
         if constexpr (BITS == 8) {
             const int em = block_of(bm[u]), ev = block_of(bv[u]);
 #pragma unroll
@@ -403,11 +407,11 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const TensorE
             m[u][k] = mk;
             v[u][k] = vk;
         }
-        store4(t.master, e, n, p[u]);
-        if constexpr (TYPE != 3) store4(static_cast<T*>(t.param), e, n, p[u]);
+        store4<NT>(t.master, e, n, p[u]);
+        if constexpr (TYPE != 3) store4<NT>(static_cast<T*>(t.param), e, n, p[u]);
         if constexpr (BITS == 32) {
-            store4(static_cast<float*>(t.m), e, n, m[u]);
-            store4(static_cast<float*>(t.v), e, n, v[u]);
+            store4<NT>(static_cast<float*>(t.m), e, n, m[u]);
+            store4<NT>(static_cast<float*>(t.v), e, n, v[u]);
         } else {
             uint32_t top_m = 0, top_v = 0;
 #pragma unroll
@@ -427,8 +431,8 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const TensorE
                 xm |= encode_m(m[u][k], em, r & 0xffffu) << (8 * k);
                 xv |= encode_v(v[u][k], ev, r >> 16) << (8 * k);
             }
-            store_codes(static_cast<uint8_t*>(t.m), e, n, xm);
-            store_codes(static_cast<uint8_t*>(t.v), e, n, xv);
+            store_codes<NT>(static_cast<uint8_t*>(t.m), e, n, xm);
+            store_codes<NT>(static_cast<uint8_t*>(t.v), e, n, xv);
             const int64_t first = e - lane * 4;       // the wave's block
             if (lane == 0 && first < n) {
                 t.m_exp[first / kStateBlock] = (int8_t)em;
@@ -441,11 +445,15 @@ __device__ __forceinline__ void update_chunk(const AdamwLaunch& a, const TensorE
 // PARTIALS: every workgroup adds the check's partials itself and takes the same
 // decision from the state that the check left aside; the first writes it.  Up to 512
 // partials (2M elements: 17.2 -> 16.3 us a step) that is faster than a launch for it.
-template <int BITS, int U, bool PARTIALS>
-__global__ __launch_bounds__(kThreads) void update_kernel(AdamwLaunch a, int64_t partials)
+template <int BITS, int WAVES, int U, bool NT, bool PARTIALS>
+__global__ __launch_bounds__(WAVES * 64) void update_kernel(AdamwLaunch a, int64_t partials)
 {
-    const ChunkEntry c = a.chunks[blockIdx.x];
+    constexpr int kElements = WAVES * U * kStateBlock;
+    const uint32_t parts = (uint32_t)(a.chunk / kElements);
+    const ChunkEntry c = a.chunks[blockIdx.x / parts];
     const TensorEntry t = a.tensors[c.tensor];
+    const int64_t begin = c.begin + blockIdx.x % parts * kElements;
+    if (begin >= t.numel) return;              // (never the first workgroup)
     auto decided = [&]() -> AdamwState {
         if constexpr (!PARTIALS) {
             return *a.state;
@@ -460,9 +468,9 @@ __global__ __launch_bounds__(kThreads) void update_kernel(AdamwLaunch a, int64_t
             return sh;
         }
     };
-    if (t.type == 1) update_chunk<1, BITS, U>(a, t, c, decided);
-    else if (t.type == 2) update_chunk<2, BITS, U>(a, t, c, decided);
-    else update_chunk<3, BITS, U>(a, t, c, decided);
+    if (t.type == 1) update_part<1, BITS, WAVES, U, NT>(a, t, c.tensor, begin, decided);
+    else if (t.type == 2) update_part<2, BITS, WAVES, U, NT>(a, t, c.tensor, begin, decided);
+    else update_part<3, BITS, WAVES, U, NT>(a, t, c.tensor, begin, decided);
 }
 
 // ------------------------------------------------------------------ tables and states
@@ -479,12 +487,13 @@ __global__ __launch_bounds__(kGradsPerLaunch) void set_grads_kernel(TensorEntry*
 
 __global__ void set_state_kernel(AdamwState* state, AdamwState to) { *state = to; }
 
-template <bool SIGNED>
+// NT: past the caches, for arrays of kAdamwLarge elements and more.
+template <bool SIGNED, bool NT>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const float* x, uint8_t* codes, int8_t* exps, int64_t n)
 {
     const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
     const int lane = threadIdx.x & 63;
-    const f4 v = load4(x, e, n);
+    const f4 v = load4<NT>(x, e, n);
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -499,27 +508,50 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const float* x, uint8_t*
         if constexpr (SIGNED) c |= encode_m(v[k], be, 32767) << (8 * k);
         else c |= encode_v(v[k] > 0.0f ? v[k] : 0.0f, be, 32767) << (8 * k);
     }
-    store_codes(codes, e, n, c);
+    store_codes<NT>(codes, e, n, c);
     if (lane == 0 && e < n) exps[e / kStateBlock] = (int8_t)be;
 }
 
-// 8 elements a lane: 512 bytes of codes a wave, and 1 or 2 KiB of values.
-template <typename T, bool SIGNED>
+// 16 bytes of values a lane and store, kUnpack of them: a wave's loads and stores are whole
+// lines (326M values to bf16 161 us, 6.1 TB/s; 212 through the caches, and 430 past
+// them with half lines).
+constexpr int kUnpack = 4;
+
+template <typename T, bool SIGNED, bool NT>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* codes, const int8_t* exps, T* out, int64_t n)
 {
-    const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
-    if (e >= n) return;
-    const int b = block_of(exps[e / kStateBlock]);
+    constexpr int W = Vec<T>::W;
+    const int64_t e0 = ((int64_t)blockIdx.x * kUnpack * kThreads + threadIdx.x) * W, last = (n - 1) / kStateBlock;
+    uint32_t c[kUnpack][W / 4];
+    int b[kUnpack];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t c = load_codes(codes, e + 4 * h, n);
-        f4 x;
+    for (int u = 0; u < kUnpack; ++u) {
+        const int64_t e = e0 + u * kThreads * W, block = e / kStateBlock;
+        if (e + W <= n) {
+            const auto v = load_vec<uint8_t, W, NT>(codes + e);
+            __builtin_memcpy(c[u], &v, W);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[k] = SIGNED ? decode_m(c, k, b) : decode_v(c, k, b);
-            if (b == kExpNaN) x[k] = __builtin_nanf("");
+            for (int q = 0; q < W / 4; ++q) c[u][q] = load_codes<false>(codes, e + 4 * q, n);
         }
-        store4(out, e + 4 * h, n, x);
+        b[u] = block_of(exps[block < last ? block : last]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnpack; ++u) {
+        const int64_t e = e0 + u * kThreads * W;
+        vec_t<T, W> x;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float y = SIGNED ? decode_m(c[u][k / 4], k % 4, b[u]) : decode_v(c[u][k / 4], k % 4, b[u]);
+            x[k] = static_cast<T>(b[u] == kExpNaN ? __builtin_nanf("") : y);
+        }
+        if (e + W <= n) {
+            store_vec<T, W, NT>(out + e, x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (e + k < n) out[e + k] = x[k];
+        }
     }
 }
 
@@ -532,19 +564,33 @@ hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t 
     int64_t sums = checked ? ceil_div(a.nchunks * a.chunk, kAdamwChunk) : 0;
     if (sums > kAdamwPartials) sums = kAdamwPartials;
     if (sums > 0) norm_kernel<<<dim3((unsigned)sums), kThreads, 0, s>>>(a);
-    const dim3 grid((unsigned)a.nchunks);
     const bool small = a.chunk == kAdamwSmallChunk;
     if (small && sums > 0 && sums <= kAdamwInline) {
-        if (bits == 32) update_kernel<32, 1, true><<<grid, kThreads, 0, s>>>(a, sums);
-        else update_kernel<8, 1, true><<<grid, kThreads, 0, s>>>(a, sums);
+        const dim3 grid((unsigned)a.nchunks);
+        if (bits == 32) update_kernel<32, 4, 1, false, true><<<grid, kThreads, 0, s>>>(a, sums);
+        else update_kernel<8, 4, 1, false, true><<<grid, kThreads, 0, s>>>(a, sums);
         return hipGetLastError();
     }
     decide_kernel<<<1, kThreads, 0, s>>>(a, sums);
-    if (a.nchunks > 0) {
-        if (bits == 32 && small) update_kernel<32, 1, false><<<grid, kThreads, 0, s>>>(a, 0);
-        else if (bits == 32) update_kernel<32, 4, false><<<grid, kThreads, 0, s>>>(a, 0);
-        else if (small) update_kernel<8, 1, false><<<grid, kThreads, 0, s>>>(a, 0);
-        else update_kernel<8, 4, false><<<grid, kThreads, 0, s>>>(a, 0);
+    if (a.nchunks == 0) return hipGetLastError();
+    if (small) {
+        const dim3 grid((unsigned)a.nchunks);
+        if (bits == 32) update_kernel<32, 4, 1, false, false><<<grid, kThreads, 0, s>>>(a, 0);
+        else update_kernel<8, 4, 1, false, false><<<grid, kThreads, 0, s>>>(a, 0);
+        return hipGetLastError();
+    }
+    // Past the caches, all of it.  With fp32 moments 8 streams share the memory, and a wave
+    // of 256 elements a workgroup, 18 to a CU (held there by LDS that is asked for and
+    // not used), is what it serves best: 326M elements in 1471 us with the check, 6.2 TB/s
+    // (16 a CU: 1488, 14: 1542, 20: 1527; workgroups of 4 waves of 1024 elements: 1720,
+    // and 1883 through the caches).  With 8-bit moments the arithmetic wants all the waves
+    // there are: workgroups of 4 of 1024 elements and no limit 1010 us, 5.2 TB/s (through
+    // the caches 1050; 16 waves of 256 elements 1550).
+    if (bits == 32) {
+        const int lds = kLds / 18 - 1024;
+        update_kernel<32, 1, 1, true, false><<<dim3((unsigned)(a.nchunks * (a.chunk / kStateBlock))), 64, lds, s>>>(a, 0);
+    } else {
+        update_kernel<8, 4, 4, true, false><<<dim3((unsigned)a.nchunks), kThreads, 0, s>>>(a, 0);
     }
     return hipGetLastError();
 }
@@ -565,29 +611,39 @@ hipError_t adamw_set_grads(TensorEntry* tensors, const void* const* grads, int64
     return hipGetLastError();
 }
 
-hipError_t moments_pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n, bool is_signed, hipStream_t s)
+template <bool NT>
+static void pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n, bool is_signed, hipStream_t s)
 {
     const dim3 grid((unsigned)ceil_div(n, kThreads * 4));
+    if (is_signed) pack_kernel<true, NT><<<grid, kThreads, 0, s>>>(x, codes, exps, n);
+    else pack_kernel<false, NT><<<grid, kThreads, 0, s>>>(x, codes, exps, n);
+}
+
+hipError_t moments_pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n, bool is_signed, hipStream_t s)
+{
     if (n == 0) return hipSuccess;
-    if (is_signed) pack_kernel<true><<<grid, kThreads, 0, s>>>(x, codes, exps, n);
-    else pack_kernel<false><<<grid, kThreads, 0, s>>>(x, codes, exps, n);
+    if (n < kAdamwLarge) pack<false>(x, codes, exps, n, is_signed, s);
+    else pack<true>(x, codes, exps, n, is_signed, s);
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool NT>
 static void unpack(const uint8_t* codes, const int8_t* exps, void* out, int64_t n, bool is_signed, hipStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(n, kThreads * 8));
-    if (is_signed) unpack_kernel<T, true><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
-    else unpack_kernel<T, false><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
+    const dim3 grid((unsigned)ceil_div(n, kUnpack * kThreads * Vec<T>::W));
+    if (is_signed) unpack_kernel<T, true, NT><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
+    else unpack_kernel<T, false, NT><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
 }
 
 hipError_t moments_unpack(const uint8_t* codes, const int8_t* exps, void* out, int64_t n, int type, bool is_signed,
                           hipStream_t s)
 {
     if (n == 0) return hipSuccess;
-    if (type == 2) unpack<__bf16>(codes, exps, out, n, is_signed, s);
-    else unpack<float>(codes, exps, out, n, is_signed, s);
+    const bool large = n >= kAdamwLarge;
+    if (type == 2 && large) unpack<__bf16, true>(codes, exps, out, n, is_signed, s);
+    else if (type == 2) unpack<__bf16, false>(codes, exps, out, n, is_signed, s);
+    else if (large) unpack<float, true>(codes, exps, out, n, is_signed, s);
+    else unpack<float, false>(codes, exps, out, n, is_signed, s);
     return hipGetLastError();
 }
 

@@ -169,7 +169,7 @@ zero_status check_place(const Array* a, int n, void* stream, const char* who)
 }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
-constexpr int64_t kMaxElements = (int64_t)1 << 40;     // of a handle: 12 TB of fp32 states
+constexpr int64_t kMaxElements = (int64_t)1 << 38;     // of a handle: 4 TB with fp32 masters and moments
 
 // ------------------------------------------------------------------ layer norm
 
@@ -242,7 +242,7 @@ zero_status tensor_arrays(const zero_adamw_tensor& t, int32_t index, int bits, s
     const int32_t type = enum_value(t.type);
     if (!known_type(type)) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d has unknown type %d", who, index, (int)type);
     if (t.numel < 0) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d has numel < 0", who, index);
-    if (t.numel > kMaxElements) return fail(ZERO_ERR_UNSUPPORTED, "%s: tensor %d has more than 2^40 elements", who, index);
+    if (t.numel > kMaxElements) return fail(ZERO_ERR_UNSUPPORTED, "%s: tensor %d has more than 2^38 elements", who, index);
     if (!(std::isfinite(t.weight_decay))) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d: weight_decay must be finite", who, index);
     if (!(std::isfinite(t.lr_scale) && t.lr_scale >= 0.0)) return fail(ZERO_ERR_INVALID_ARG, "%s: tensor %d: lr_scale must be finite and >= 0", who, index);
     const size_t n = (size_t)t.numel, e = type_bytes(type), blocks = (n + zo::kStateBlock - 1) / zo::kStateBlock;
@@ -517,7 +517,7 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
             table[i] = zo::TensorEntry{t.grad, t.master, t.param, t.exp_avg, t.exp_avg_sq, t.exp_avg_exp, t.exp_avg_sq_exp,
                                        t.numel, (float)t.weight_decay, (float)t.lr_scale, enum_value(t.type), 0};
             elements += t.numel;
-            if (elements > kMaxElements) return fail(ZERO_ERR_UNSUPPORTED, "%s: more than 2^40 elements", who);
+            if (elements > kMaxElements) return fail(ZERO_ERR_UNSUPPORTED, "%s: more than 2^38 elements", who);
         }
         // overlaps of so many arrays by their order in memory
         std::vector<const Array*> order;
