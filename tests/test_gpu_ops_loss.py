@@ -253,3 +253,30 @@ def test_types_are_refused():
         zs.zero_vocab_loss(h, w, targets, out, None, out[:1].clone(), dweight=w.clone(), workspace=space)
     with pytest.raises(zs.ZeroError, match="workspace"):
         zs.zero_vocab_loss(h, w, targets, out, None, out[:1].clone(), workspace=space[:256])
+
+
+@pytest.mark.parametrize("n,v,d,t", [(1, 3644, 160, "bf16"), (1, 2271, 57, "fp16"), (4, 1003, 57, "fp16"), (5, 900, 64, "bf16"),
+                                     (9, 3001, 200, "fp16"), (31, 513, 96, "bf16"), (32, 777, 41, "fp16")])
+def test_few_tokens_lose_nothing_to_the_held_gradient(n, v, d, t):
+    """Up to 32 tokens an entry of G is held in two numbers, so a gradient is off by its
+    own rounding (u) and, relative to the sum of its terms' magnitudes, by: the two numbers'
+    u^2, twice; 2 dz of a logit and of lse; the exponent's argument, below 2^6, rounded to
+    fp32 and some roundings beside (2^-16 in all); the fp32 sums (as in check).  A step of
+    fp16's smallest numbers under 2^15 is 2^-39 of G, and there are two of them."""
+    t = TYPES[t]
+    h, w, targets = make(n, v, d, t, seed=n + v, lean=6.0)
+    _, _, _, dh, dw = run(h, w, targets, scale=64.0)
+    H, W = h.double().cpu(), w.double().cpu()
+    z = H @ W.t()
+    p = torch.softmax(z, 1)
+    one = torch.nn.functional.one_hot(targets.cpu(), v).double()
+    G = p * (1 - one)
+    G = G - one * G.sum(1, keepdim=True)
+    dz = (d * 2.0 ** -23 * (H.abs() @ W.abs().t())).max(1, keepdim=True).values
+    u = torch.finfo(t).eps / 2
+    dG = G.abs() * 2 * u * u * (1 + u) + p * (4 * dz + 2.0 ** -16) + one * 2.0 ** -22 + 2.0 ** -38
+    low = torch.finfo(t).tiny * torch.finfo(t).eps
+    for got, ref, off in ((dh, G @ W, dG @ W.abs() + G.abs() @ W.abs() * (v * 2.0 ** -23)),
+                          (dw, G.t() @ H, dG.t() @ H.abs() + G.abs().t() @ H.abs() * (2 * n * 2.0 ** -23 + 2.0 ** -20))):
+        ref, off = ref * (64.0 / n), off * (64.0 / n)
+        assert ((got.double().cpu() - ref).abs() <= u * ref.abs() + off * (1 + u) + low).all()

@@ -71,6 +71,8 @@ struct Operand {
     int64_t ld;
     int64_t rows;
     int64_t depth;
+    int64_t pairs = 0;       // kOuter, one step: of so many entries, in pairs (see pair_row)
+    bool twice = false;      // with pairs: they lie once, and both of a pair are the same row
 };
 
 // The piece of an operand that a tile reads, as it moves along k.
@@ -196,6 +198,23 @@ struct Inner {
     }
 };
 
+// Entries in pairs: rows 32 b to + 15 are the first halves of entries 16 b to + 15, rows
+// 32 b + 16 to + 31 the second halves, so that products of 16 rows have both in one lane.
+__host__ __device__ __forceinline__ int64_t pair_row(int64_t entry) { return (entry >> 4) * 32 + (entry & 15); }
+__host__ __device__ __forceinline__ int64_t pair_rows(int64_t entries) { return (entries + 15) / 16 * 32; }
+__device__ __forceinline__ int pair_entry(int row) { return (row >> 5) * 16 + (row & 15); }
+
+// Byte offset of row k of a step.  Rows that are no entry's are zeros.
+__device__ __forceinline__ uint32_t offset_of_k(const Operand& o, int k, int column)
+{
+    if (o.pairs > 0) {
+        if (pair_entry(k) >= o.pairs) return kOutOfRange;
+        if (o.twice) k = pair_entry(k);
+    }
+    return (uint32_t)((k * o.ld + column) * 2);
+}
+
+
 // 64 columns of a kOuter operand: 64 rows of k with 128 bytes each.
 struct Outer64 {
     static constexpr int kBytes = 64 * kDeep * 2;
@@ -203,11 +222,11 @@ struct Outer64 {
 
     // 16 lanes read 4 rows of k, 32 lanes 8, 32 bytes of each: all in different banks
     static __device__ __forceinline__ int key(int k) { return 2 * ((k & 3) ^ ((k >> 3) & 1)); }
-    __device__ __forceinline__ void init(int64_t ld, int64_t col0, int wave, int lane)
+    __device__ __forceinline__ void init(const Operand& o, int col0, int wave, int lane)
     {
         const int k = wave * 8 + (lane >> 3);
         const int chunk = (lane & 7) ^ key(k);
-        voff = (uint32_t)((k * ld + col0 + chunk * 8) * 2);
+        voff = offset_of_k(o, k, col0 + chunk * 8);
     }
     __device__ __forceinline__ void issue(const u4& rsrc, uint32_t lds, int wave)
     {
@@ -234,19 +253,24 @@ struct Outer64 {
 template <bool RUNS>
 struct Outer256 {
     static constexpr int kBytes = 256 * kDeep * 2;
-    uint32_t voff[2], apart, addr;
+    uint32_t voff[2], apart[RUNS ? 2 : 1], addr;     // (RUNS: there may be pairs)
 
     static __device__ __forceinline__ int key(int k) { return 2 * ((k & 3) | ((k >> 3) & 1) << 2); }
-    __device__ __forceinline__ void init(int64_t ld, int wave, int lane)
+    __device__ __forceinline__ void init(const Operand& o, int wave, int lane)
     {
         // load q of wave w: rows 8 w + 2 q and + 1 of k; q and q + 2 have the same key
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int k = wave * 8 + q * 2 + (lane >> 5);
             const int chunk = (lane & 31) ^ key(k);
-            voff[q] = (uint32_t)((k * ld + chunk * 8) * 2);
+            if constexpr (RUNS) {
+                voff[q] = offset_of_k(o, k, chunk * 8);
+                apart[q] = offset_of_k(o, k + 4, chunk * 8) - voff[q];
+            } else {
+                voff[q] = (uint32_t)((k * o.ld + chunk * 8) * 2);
+            }
         }
-        apart = (uint32_t)(4 * ld * 2);
+        if constexpr (!RUNS) apart[0] = (uint32_t)(4 * o.ld * 2);
     }
     __device__ __forceinline__ void issue(const u4& rsrc, uint32_t lds, int wave)
     {
@@ -254,7 +278,7 @@ struct Outer256 {
         asm volatile("" : "+v"(first[0]), "+v"(first[1]));
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            load_to_lds(first[q & 1] + (q >> 1) * apart, rsrc, lds + (wave * 4 + q) * 1024);
+            load_to_lds(first[q & 1] + (q >> 1) * apart[RUNS ? q & 1 : 0], rsrc, lds + (wave * 4 + q) * 1024);
     }
     __device__ __forceinline__ void reader(uint32_t lds, int w0, int lane)
     {
@@ -294,8 +318,8 @@ struct Outer {
     }
     __device__ __forceinline__ void lanes(const Operand& o, int wave, int lane)
     {
-        if constexpr (C >= 4) wide.init(o.ld, wave, lane);
-        if constexpr (C != 4) narrow.init(o.ld, C == 5 ? 256 : 0, wave, lane);
+        if constexpr (C >= 4) wide.init(o, wave, lane);
+        if constexpr (C != 4) narrow.init(o, C == 5 ? 256 : 0, wave, lane);
     }
     __device__ __forceinline__ void issue(uint32_t lds, int wave)
     {

@@ -53,6 +53,7 @@ struct LossPlan {              // what a call's sizes settle
     int64_t width_ld;          // the width in whole chunks of 8
     TileChoice logits_tile, hidden_tile, weight_tile;
     int hidden_splits, weight_splits;      // parts of the gradients' products
+    bool pairs;                // an entry of G is held as two numbers
     // byte offsets into the workspace
     int64_t off_alpha, off_target, off_lse, off_stats, off_exp, off_split, off_sum, off_hidden, off_weight;
     int64_t bytes;

@@ -18,8 +18,8 @@
 // epilogue and in a copy of H; that took 7% less, and the copy's rounding made the
 // weight's gradient 1.7 times less exact.)
 //
-// An entry of G is rounded to 2 bytes twice (as exp, and by its factor).  The target's
-// entry, where p - 1 would cancel, is computed from the fp32 logit as expm1(z - lse).
+// An entry of G is rounded to 2 bytes twice (as exp, and by its factor); up to 32 tokens it
+// is held in two 2-byte numbers, as good as exact (see kPairs).  The target's entry, where p - 1 would cancel, is computed from the fp32 logit as expm1(z - lse).
 // What is held is G times 2^15 (fp16) or 2^32 (bf16), taken back in the products'
 // epilogues: entries far below the type's normal range stay.
 
@@ -76,6 +76,7 @@ struct LogitsArgs {
     float* target_logit;
     float2* stats;              // [tokens][pieces]: maximum and sum
     void* exps;                 // [tokens][vocab_ld], or NULL: the loss alone
+    int pairs;                  // the exponentials are in pairs: beside each what its rounding takes away (NI = 2)
     int64_t tokens, vocab, vocab_ld, pieces;
     uint32_t ti, tj;          // tiles
 };
@@ -121,25 +122,34 @@ __device__ __forceinline__ void logits_out(const LogitsArgs& a, int64_t bi, int6
         // a piece of -infinities has no exponentials: 0, not exp(-inf + inf)
         const float base = m == -INFINITY ? 0.0f : m;
         float sum = 0.0f;
-        vec_t<T, 4> held[NJ];
+        vec_t<T, 4> held[NJ], low[NJ];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             // (the factor in the exponent: nothing is lost below fp32's normal range)
             const float e = __builtin_amdgcn_exp2f(fmaf(acc[ti][k >> 2][k & 3] - base, kLog2e, kHoldLog2<T>));
             sum += e;
             held[k >> 2][k & 3] = to_type<T>(e);
+            if constexpr (NI == 2) low[k >> 2][k & 3] = to_type<T>(e - (float)held[k >> 2][k & 3]);
         }
         sum += __shfl_xor(sum, 16, kWave);
         sum += __shfl_xor(sum, 32, kWave);
         if (n < a.tokens) {
             if (lane < 16) a.stats[n * a.pieces + bj * 4 + (wave & 3)] = make_float2(m, sum * (1.0f / kHold<T>));
             if (a.exps != nullptr) {
-                T* to = static_cast<T*>(a.exps) + n * a.vocab_ld;
+                T* to = static_cast<T*>(a.exps) + (NI == 2 && a.pairs ? pair_row(n) : n) * a.vocab_ld;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     reinterpret_cast<vec_t<T, 8>*>(to + v)[q] =
                         __builtin_shufflevector(held[2 * q], held[2 * q + 1], 0, 1, 2, 3, 4, 5, 6, 7);
                 if constexpr (NJ == 5) *reinterpret_cast<vec_t<T, 4>*>(to + far + 16) = held[4];
+                if constexpr (NI == 2) {
+                    if (a.pairs) {
+                        auto* under = reinterpret_cast<vec_t<T, 8>*>(to + 16 * a.vocab_ld + v);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            under[q] = __builtin_shufflevector(low[2 * q], low[2 * q + 1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    }
+                }
             }
         }
     }
@@ -215,6 +225,7 @@ struct JoinArgs {
     float* losses;
     float* lse;
     void* exps;               // NULL: the loss alone
+    int pairs;                // they are in pairs
     int64_t pieces, vocab, vocab_ld, ignore;
 };
 
@@ -250,8 +261,29 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a)
         a.losses[n] = counts && known ? lse - z : nothing;
     }
     if (a.exps == nullptr) return;
-    T* exps = static_cast<T*>(a.exps) + n * a.vocab_ld;
-    const T own = to_type<T>(expm1f(z - lse) * kHold<T>);
+    T* exps = static_cast<T*>(a.exps) + (a.pairs ? pair_row(n) : n) * a.vocab_ld;
+    const float target = expm1f(z - lse) * kHold<T>;
+    const T own = to_type<T>(target);
+    if (a.pairs) {
+        T* low = exps + 16 * a.vocab_ld;
+        for (int64_t v = (blockIdx.y * 256 + threadIdx.x) * 8; v < a.vocab_ld; v += gridDim.y * 2048) {
+            auto* at = reinterpret_cast<vec_t<T, 8>*>(exps + v);
+            auto* under = reinterpret_cast<vec_t<T, 8>*>(low + v);
+            const float f = expf(row[piece_of<NJ>(v)].x - lse);
+            vec_t<T, 8> x = *at, y = *under;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float g = ((float)x[k] + (float)y[k]) * f;
+                if (v + k == t) g = target;
+                if (!(counts && known)) g = nothing;
+                x[k] = to_type<T>(g);
+                y[k] = to_type<T>(g - (float)x[k]);
+            }
+            *at = x;
+            *under = y;
+        }
+        return;
+    }
 #pragma unroll 4
     for (int64_t v = (blockIdx.y * 256 + threadIdx.x) * 8; v < a.vocab_ld; v += gridDim.y * 2048) {
         auto* at = reinterpret_cast<vec_t<T, 8>*>(exps + v);
@@ -314,6 +346,7 @@ struct GradArgs {
     int splits;
     int vector_out;           // results that can be stored at once: 8, 4, or 0
     int sum_in, sum_out;      // the sum is added / is where the result goes
+    int pairs;                // p's rows are in pairs, and a result is the sum of a pair's (NI = 2)
 };
 
 template <typename T, Layout LP, int NI, int NJ>
@@ -332,10 +365,22 @@ __global__ __launch_bounds__(kGemmThreads, 2) void grad_kernel(GradArgs a)
     g.run((int)(s1 - s0), acc, [] {});
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float alpha = a.alpha[0];
+    if constexpr (NI == 2 && LP == kInner) {
+        if (a.pairs) {
+#pragma unroll
+            for (int tj = 0; tj < NJ; ++tj) acc[0][tj] += acc[1][tj];
+        }
+    }
+    auto row_at = [&](int ti) -> int64_t {
+        const int row = G::row_of(ti, wave, lane);
+        if constexpr (NI == 2 && LP == kInner)
+            if (a.pairs) return ti == 0 ? pair_entry(row) : a.rows;        // (one tile)
+        return bi * G::kTileI + row;
+    };
     if (a.part == nullptr && !a.sum_in && !a.sum_out && a.vector_out) {       // as good as always
 #pragma unroll
         for (int ti = 0; ti < NI; ++ti) {
-            const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
+            const int64_t i = row_at(ti);
             if (i >= a.rows) continue;
             T* to = static_cast<T*>(a.out) + i * a.out_ld;
             if constexpr (G::kRuns && NJ == 4) {
@@ -368,7 +413,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void grad_kernel(GradArgs a)
     }
 #pragma unroll
     for (int ti = 0; ti < NI; ++ti) {
-        const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
+        const int64_t i = row_at(ti);
         if (i >= a.rows) continue;
 #pragma unroll
         for (int tj = 0; tj < NJ; ++tj) {
@@ -550,12 +595,13 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         const int64_t n = p.tokens - n0 < p.chunk ? p.tokens - n0 : p.chunk;
         const bool last = n0 + n == p.tokens;
         const Operand oh{h + n0 * h_ld, h_ld, n, p.width_ld};
-        const LogitsArgs l{oh, ow, a.targets + n0, target_logit, stats, exps, n, p.vocab, p.vocab_ld, p.pieces, 0, 0};
+        const int64_t held = p.pairs ? pair_rows(n) : n;        // rows of G
+        const LogitsArgs l{oh, ow, a.targets + n0, target_logit, stats, exps, p.pairs, n, p.vocab, p.vocab_ld, p.pieces, 0, 0};
         if (p.logits_tile.ni == 2) e = logits<T, 2, 4>(l, s);
         else if (p.logits_tile.nj == 4) e = logits<T, 8, 4>(l, s);
         else e = logits<T, 8, 5>(l, s);
         if (e != hipSuccess) return e;
-        const JoinArgs j{stats, target_logit, a.targets + n0, a.losses + n0, lse + n0, exps,
+        const JoinArgs j{stats, target_logit, a.targets + n0, a.losses + n0, lse + n0, exps, p.pairs,
                          p.pieces, p.vocab, p.vocab_ld, a.ignore_index};
         // (a workgroup has 2048 ids at a time; 1024 workgroups fill the card)
         int64_t share = gradient && n < 1024 ? ceil_div(1024, n) : 1;
@@ -584,9 +630,10 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
             return hipSuccess;
         };
         // dH = G W: k runs over the vocabulary
-        g.p = Operand{exps, p.vocab_ld, n, p.vocab_ld};
+        g.p = Operand{exps, p.vocab_ld, held, p.vocab_ld};
         g.q = Operand{w, w_ld, p.width, p.vocab};
         g.rows = n;
+        g.pairs = p.pairs;
         g.steps = p.vocab_ld / kDeep;
         g.out = static_cast<T*>(a.dhidden) + n0 * a.dhidden_stride;
         g.out_ld = a.dhidden_stride;
@@ -594,10 +641,11 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         if (e != hipSuccess) return e;
         // dW = G^T H: k runs over the chunk's tokens; with several chunks the sum
         // stays in fp32 until the last
-        g.p = Operand{exps, p.vocab_ld, p.vocab_ld, n};
-        g.q = Operand{oh.base, h_ld, p.width_ld, n};
+        g.p = Operand{exps, p.vocab_ld, p.vocab_ld, held, p.pairs ? n : 0};
+        g.q = Operand{oh.base, h_ld, p.width_ld, n, p.pairs ? n : 0, true};
         g.rows = p.vocab;
-        g.steps = ceil_div(n, kDeep);
+        g.pairs = 0;
+        g.steps = ceil_div(held, kDeep);
         g.out = a.dweight;
         g.out_ld = a.dweight_stride;
         g.sum = reinterpret_cast<float*>(a.space + p.off_sum);
@@ -611,6 +659,14 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
 // Rows up to which tiles of 64 are taken instead of 256.  At 16 tokens x 50257 x 1600
 // they take 29, 30 and 44 us for the three products, against 38, 41 and 65.
 constexpr int64_t kFewRows = 128;
+
+// Tokens up to which an entry of G is held as two 2-byte numbers, the second what the
+// first's rounding took away.  Of few tokens a single entry can make up most of a
+// gradient, which is then off by that entry's rounding (4 tokens x 22719 x 57 fp16: the
+// weight's gradient by 4.2e-4 of its norm, 2.2e-4 in pairs, as much as its own rounding).
+// The second halves are rows of their own in the same tile of 64 and cost no product: 16
+// tokens x 50257 x 1600 bf16 take 142 us, 138 without.
+constexpr int64_t kPairs = 32;
 
 // Rounds of tiles over the card.
 int64_t rounds_of(int64_t rows, int64_t cols, const TileChoice& c, int64_t splits)
@@ -665,6 +721,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chu
                     : rounds_of(p.chunk, vocab, wide, 1) * 6 < rounds_of(p.chunk, vocab, narrow, 1) * 5 ? wide : narrow;
     p.vocab_ld = round_up(vocab, p.logits_tile.nj == 5 ? 320 : 64);      // whole pieces, whole steps
     p.pieces = p.vocab_ld / (16 * p.logits_tile.nj);
+    p.pairs = gradient && p.chunk <= kPairs;
     p.hidden_tile = choose(p.chunk, width, p.vocab_ld / kDeep, true, &p.hidden_splits);
     p.weight_tile = choose(vocab, width, ceil_div(p.chunk, kDeep), p.chunk >= tokens, &p.weight_splits);
     if (p.chunk <= kFewRows) p.weight_tile = TileChoice{2, 4};           // one or two steps: storing is what takes the time
@@ -680,7 +737,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chu
     p.off_target = take(p.chunk * 4);
     p.off_lse = take(tokens * 4);
     p.off_stats = take(p.chunk * p.pieces * 8);
-    p.off_exp = take(gradient ? p.chunk * p.vocab_ld * 2 : 0);
+    p.off_exp = take(gradient ? (p.pairs ? pair_rows(p.chunk) : p.chunk) * p.vocab_ld * 2 : 0);
     p.off_split = take(gradient ? (parts_hidden > parts_weight ? parts_hidden : parts_weight) * 4 : 0);
     p.off_sum = take(gradient && p.chunk < tokens ? vocab * width * 4 : 0);
     p.off_hidden = take(tokens * p.width_ld * 2);
