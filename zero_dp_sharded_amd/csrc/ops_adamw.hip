@@ -1,14 +1,16 @@
 // AdamW over the tensors of a model at once, with moments in 32 or in 8 bits.
 //
 // One launch updates every tensor: a table in device memory, made when the handle
-// is, cuts the tensors into chunks, a workgroup each.  A lane has 4 elements side by
+// is, cuts the tensors into chunks, of one workgroup or several.  A lane has 4 elements side by
 // side, so that every load and store of a wave is whole lines (512 bytes of 2-byte
 // gradients, 1 KiB of fp32), and a wave's 256 elements are a block of the 8-bit
 // states.  Bound by memory: per element and step 28 bytes with fp32 moments and 2-byte
-// storage, 16 with 8-bit moments; with the latter only because the arithmetic is
-// spare (a division by a step's constant in 3 operations, one hash for both moments'
-// noise, powers of two by ldexp): at 5 TB/s a wave has about 400 cycles for 256
-// elements of 16 bytes.
+// storage, 16 with 8-bit moments, and the check reads the gradient once more.  326M
+// elements take 1463 us with the check, 6.7 TB/s, as a copy past the caches does.  With
+// 8-bit moments the arithmetic binds as well, spare as it is (a division by a step's
+// constant in 3 operations, one hash for both moments' noise, powers of two by ldexp):
+// 117 vector instructions an element, 1000 us, 5.2 TB/s.  Up to 2M elements it is two
+// launches and their latency: 1.8M in 16.7 us.
 //
 // The arithmetic is that of the shard's Adam (each operation rounded to fp32 in
 // the order written, no fused multiply-adds), so that a tensor's update has the same bits
@@ -581,7 +583,7 @@ hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t 
     }
     // Past the caches, all of it.  With fp32 moments 8 streams share the memory, and a wave
     // of 256 elements a workgroup, 18 to a CU (held there by LDS that is asked for and
-    // not used), is what it serves best: 326M elements in 1471 us with the check, 6.2 TB/s
+    // not used), is what it serves best: 326M elements in 1471 us with the check
     // (16 a CU: 1488, 14: 1542, 20: 1527; workgroups of 4 waves of 1024 elements: 1720,
     // and 1883 through the caches).  With 8-bit moments the arithmetic wants all the waves
     // there are: workgroups of 4 of 1024 elements and no limit 1010 us, 5.2 TB/s (through
