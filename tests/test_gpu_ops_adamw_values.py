@@ -1,0 +1,61 @@
+"""AdamW over tensors at values where its arithmetic leaves fp32's usual range, bit for
+bit against the same operations one by one in numpy (every one rounded once, so there
+is no tolerance)."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import zero_dp_sharded_amd as zs
+from test_gpu_ops_adamw import DEV, f32, step_by_hand
+
+pytestmark = pytest.mark.gpu
+
+
+class One:
+    """One fp32 tensor with the given moments, and its gradient."""
+
+    def __init__(self, p, m, v, g):
+        place = lambda x: torch.as_tensor(x, dtype=torch.float32).to(DEV)
+        self.tensors = [zs.AdamWTensor(place(g), place(p), None, place(m), place(v))]
+        self.grads = [self.tensors[0].grad]
+
+
+def bits(x):
+    """The bits, every NaN the same."""
+    b = x.cpu().numpy().view(np.uint32).copy()
+    b[np.isnan(x.cpu().numpy())] = 0x7fc00000
+    return b
+
+
+def one_step(model, hp, t, checked=True):
+    """The step by hand and on the GPU: (master, m, v) of both, as bits."""
+    _, _, new = step_by_hand(model, hp, 1.0, t, 32, 0, 0.0, checked=checked)
+    h = zs.zero_adamw_init(model.tensors, hp=hp, ls=zs.LossScaleCfg(init_scale=1.0, dynamic=0), checked=checked)
+    try:
+        zs.zero_adamw_step(h)
+        torch.cuda.synchronize()
+    finally:
+        zs.zero_adamw_destroy(h)
+    x = model.tensors[0]
+    p, _, m, v = new[0]
+    return [bits(z) for z in (x.master, x.exp_avg, x.exp_avg_sq)], [bits(z) for z in (p, m, v)]
+
+
+@pytest.mark.parametrize("t0,beta1,beta2", [(0, 0.9, 0.999), (0, 0.9, 0.95), (3, 0.9, 0.999), (0, 0.5, 0.9999), (900, 0.9, 0.999)])
+def test_bias_corrected_moments_past_the_largest_number(t0, beta1, beta2):
+    """Moments whose quotient by the bias correction passes fp32's range: it is infinite, as
+    the division makes it, the root of an infinite second moment stops the element, and
+    nothing becomes NaN that is a number by the formula."""
+    big = np.float32(3.4e38) * np.exp2(-np.arange(0, 64, 0.25, dtype=np.float64)).astype(np.float32)
+    n = big.size
+    m = np.concatenate([np.zeros(n), big, -big, np.full(n, 1e-3)]).astype(np.float32)
+    v = np.concatenate([big, np.full(n, 1e-6), np.full(n, 2.0), big]).astype(np.float32)
+    p = np.linspace(-1, 1, 4 * n).astype(np.float32)
+    hp = zs.AdamHParams(lr=1e-2, beta1=beta1, beta2=beta2, weight_decay=0.1, initial_step=t0)
+    got, want = one_step(One(p, m, v, np.zeros(4 * n)), hp, t0 + 1)
+    for name, a, b in zip(("master", "m", "v"), got, want):
+        assert np.array_equal(a, b), (name, int((a != b).sum()), np.flatnonzero(a != b)[:5])
+    # an element without a first moment keeps its value but for the decay, however large the second
+    assert np.isfinite(got[0][:n].view(np.float32)).all()

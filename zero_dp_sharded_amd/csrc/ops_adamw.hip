@@ -138,13 +138,16 @@ __device__ __forceinline__ int block_of(int e) { return e < kExpLeast ? kExpLeas
 
 // x / c for a constant c in (0, 1], r its reciprocal, rounded: the quotient's
 // remainder is exact, and one step with it rounds as the division does (Markstein).
-// Where the remainder could fall below fp32's range the division itself is taken.
+// Where the remainder could fall below fp32's range, or the quotient pass it (then the
+// remainder is infinite, and the step inf - inf), the division itself is taken.  (r is at
+// least 1: a quotient below 2^126 has an x below it too.)
 __device__ __forceinline__ float divide_by(float x, float c, float r)
 {
     const float q = x * r;
     const float exact = fmaf(fmaf(-q, c, x), r, q);
     const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
-    if (__builtin_expect(b - 1 < 0x0d000000u - 1 || b >= 0x7e800000u, 0)) return x / c;    // below 2^-101, above 2^126
+    const uint32_t big = __builtin_bit_cast(uint32_t, q) & 0x7fffffffu;
+    if (__builtin_expect(b - 1 < 0x0d000000u - 1 || big >= 0x7e800000u, 0)) return x / c;    // x below 2^-101, q above 2^126
     return exact;
 }
 
