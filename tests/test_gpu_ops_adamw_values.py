@@ -59,3 +59,14 @@ def test_bias_corrected_moments_past_the_largest_number(t0, beta1, beta2):
         assert np.array_equal(a, b), (name, int((a != b).sum()), np.flatnonzero(a != b)[:5])
     # an element without a first moment keeps its value but for the decay, however large the second
     assert np.isfinite(got[0][:n].view(np.float32)).all()
+
+
+def test_zeros_keep_their_signs():
+    """Every sign of a zero parameter, moment and gradient, with and without decay."""
+    z = [0.0, -0.0]
+    p, m, g = (np.array(a, dtype=np.float32).ravel() for a in np.meshgrid(z, z, z))
+    for wd in (0.0, 0.1):
+        hp = zs.AdamHParams(lr=1e-2, weight_decay=wd)
+        got, want = one_step(One(p, m, np.zeros(8), g), hp, 1)
+        for name, a, b in zip(("master", "m", "v"), got, want):
+            assert np.array_equal(a, b), (name, wd, a, b)

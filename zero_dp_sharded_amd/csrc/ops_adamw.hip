@@ -144,7 +144,7 @@ __device__ __forceinline__ int block_of(int e) { return e < kExpLeast ? kExpLeas
 __device__ __forceinline__ float divide_by(float x, float c, float r)
 {
     const float q = x * r;
-    const float exact = fmaf(fmaf(-q, c, x), r, q);
+    const float exact = fmaf(-fmaf(q, c, -x), r, q);      // (so, and not by x - q c: a -0 stays one)
     const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
     const uint32_t big = __builtin_bit_cast(uint32_t, q) & 0x7fffffffu;
     if (__builtin_expect(b - 1 < 0x0d000000u - 1 || big >= 0x7e800000u, 0)) return x / c;    // x below 2^-101, q above 2^126
