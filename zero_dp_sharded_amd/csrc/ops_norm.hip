@@ -281,13 +281,20 @@ __global__ __launch_bounds__(WAVES * 64) void backward_kernel(NormBackward a)
         const float mean = nmean, rstd = nrstd;
         float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                // (past the width g is 0, and dw, db stay out of the result)
                 x[k][e] = ((float)nx[k][e] - mean) * rstd;
                 g[k][e] = (float)ng[k][e];
             }
+            // past the width g is 0, but -mean * rstd may be infinite: both are 0 there
+            const int left = (int)a.width - (k * NW * 64 + lane) * W;
+            if (left < W) {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (e >= left) x[k][e] = 0.0f;
+            }
+        }
         if (AHEAD && row + stride < a.rows) {
             fetch(row + stride);
             nmean = a.mean[row + stride];
@@ -378,7 +385,8 @@ __global__ __launch_bounds__(1024) void backward_long_kernel(NormBackward a)
             }
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float xhat = (x[e] - mean) * rstd;
+                // (past the width: 0, as in backward_kernel)
+                const float xhat = c + e < a.width ? (x[e] - mean) * rstd : 0.0f;
                 if (turn == 0) {
                     sg += g[e];
                     sgx = fmaf(g[e], xhat, sgx);
