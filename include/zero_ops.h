@@ -91,7 +91,8 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
  * the gradients are rounded to type once.  grad_scale is the loss scale the
  * gradients carry (and 1 / Nd, or a weight of the micro-batch, where wanted).
  * dhidden and dweight are given both or neither (NULL: the loss alone); they
- * are written, not added to.  losses, lse and targets hold `tokens` elements;
+ * are written, not added to.  A token that is left out enters nothing but its own lse: its
+ * hidden state need not be finite.  losses, lse and targets hold `tokens` elements;
  * lse may be NULL.  A target outside [0, vocab) that is not ignore_index gives
  * loss NaN and NaN gradients, which a checked step skips.
  * tokens = 0: loss 0, dweight zeros.

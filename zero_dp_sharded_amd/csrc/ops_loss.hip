@@ -230,12 +230,19 @@ struct JoinArgs {
     void* exps;               // NULL: the loss alone
     int pairs;                // they are in pairs
     int64_t pieces, vocab, vocab_ld, ignore;
+    const void* hidden;       // rows of width_ld, hidden_ld apart
+    void* kept;               // the same rows side by side (or where they are), of ignored tokens zeros
+    int64_t hidden_ld, width_ld;
 };
 
 // A token: lse, its loss, and from its exponentials its row of G.  Where there are few
 // tokens, several workgroups a token (blockIdx.y) share its row, and each finds lse.  A
 // target outside the vocabulary that is not ignore_index has loss NaN and a row of NaN:
 // the gradients then carry NaN, and a checked step is skipped.
+//
+// The hidden states go into the workspace for the weight's gradient, with zeros for the
+// tokens that are left out: their rows of G are zeros, but 0 times what is not finite is NaN
+// (8192 tokens of width 1600: 52 MB more in a pass of 1.7 GB).
 //
 // PAST: rows of more than the last cache's 256 MiB in all go past the caches (8192 tokens
 // x 50257 bf16: the loss and its gradients 3823 -> 3777 us; of 2048 tokens, which the
@@ -268,6 +275,15 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a)
         a.losses[n] = counts && known ? lse - z : nothing;
     }
     if (a.exps == nullptr) return;
+    const T* hidden = static_cast<const T*>(a.hidden) + n * a.hidden_ld;
+    T* kept = static_cast<T*>(a.kept) + n * a.width_ld;
+    if (hidden != kept || !counts) {
+        for (int64_t c = (blockIdx.y * 256 + threadIdx.x) * 8; c < a.width_ld; c += gridDim.y * 2048) {
+            vec_t<T, 8> x = {};
+            if (counts) x = load_vec<T, 8>(hidden + c);
+            *reinterpret_cast<vec_t<T, 8>*>(kept + c) = x;
+        }
+    }
     T* exps = static_cast<T*>(a.exps) + (a.pairs ? pair_row(n) : n) * a.vocab_ld;
     const float target = expm1f(z - lse) * kHold<T>;
     const T own = to_type<T>(target);
@@ -607,8 +623,9 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         else if (p.logits_tile.nj == 4) e = logits<T, 8, 4>(l, s);
         else e = logits<T, 8, 5>(l, s);
         if (e != hipSuccess) return e;
+        T* kept = reinterpret_cast<T*>(a.space + p.off_hidden) + n0 * p.width_ld;
         const JoinArgs j{stats, target_logit, a.targets + n0, a.losses + n0, lse + n0, exps, p.pairs,
-                         p.pieces, p.vocab, p.vocab_ld, a.ignore_index};
+                         p.pieces, p.vocab, p.vocab_ld, a.ignore_index, oh.base, kept, h_ld, p.width_ld};
         // (a workgroup has 2048 ids at a time; 1024 workgroups fill the card)
         int64_t share = gradient && n < 1024 ? ceil_div(1024, n) : 1;
         if (share > ceil_div(p.vocab_ld, 2048)) share = ceil_div(p.vocab_ld, 2048);
@@ -651,7 +668,7 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         // dW = G^T H: k runs over the chunk's tokens; with several chunks the sum
         // stays in fp32 until the last
         g.p = Operand{exps, p.vocab_ld, p.vocab_ld, held, p.pairs ? n : 0};
-        g.q = Operand{oh.base, h_ld, p.width_ld, n, p.pairs ? n : 0, true};
+        g.q = Operand{kept, p.width_ld, p.width_ld, n, p.pairs ? n : 0, true};
         g.rows = p.vocab;
         g.pairs = 0;
         g.steps = ceil_div(held, kDeep);
