@@ -34,6 +34,9 @@ COPY_SOURCES = ["hbm_copy.hip"]
 # launch path that only shards beyond 8.6e9 elements reach runs in the tests
 SPLIT_LAUNCH_DIR = os.path.join(HERE, "variants", "split_launch")
 SPLIT_LAUNCH_DEFINES = {"ZK_MAX_LAUNCH_ITEMS": 1024}
+# the operators' library split likewise, after 2048 work-items (rows beyond 2^25, arrays
+# beyond 8.6e9 elements)
+OPS_SPLIT_LAUNCH_DEFINES = {"ZO_MAX_LAUNCH_ITEMS": 2048}
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -99,6 +102,9 @@ def build(verbose: bool = False) -> str:
     _link(_compile(COPY_SOURCES, objdir, verbose), COPY_LIB, verbose)
     build_variant(SPLIT_LAUNCH_DEFINES, SPLIT_LAUNCH_DIR, verbose,
                   objdir=os.path.join(ROOT, "_build", "split_launch"))
+    extra = [f"-D{k}={v}" for k, v in OPS_SPLIT_LAUNCH_DEFINES.items()]
+    _link(_compile(OPS_SOURCES, os.path.join(ROOT, "_build", "split_launch"), verbose, extra),
+          os.path.join(SPLIT_LAUNCH_DIR, "libzeroops.so"), verbose)
     return LIB
 
 

@@ -570,20 +570,22 @@ hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t 
     if (sums > kAdamwPartials) sums = kAdamwPartials;
     if (sums > 0) norm_kernel<<<dim3((unsigned)sums), kThreads, 0, s>>>(a);
     const bool small = a.chunk == kAdamwSmallChunk;
-    if (small && sums > 0 && sums <= kAdamwInline) {
-        const dim3 grid((unsigned)a.nchunks);
-        if (bits == 32) update_kernel<32, 4, 1, false, true><<<grid, kThreads, 0, s>>>(a, sums);
-        else update_kernel<8, 4, 1, false, true><<<grid, kThreads, 0, s>>>(a, sums);
+    // `parts` workgroups of `threads` lanes a chunk
+    auto update = [&](auto kernel, int threads, int64_t parts, int lds, int64_t partials) {
+        in_launches(a.nchunks, threads * (int)parts, [&](int64_t first, int64_t count) {
+            AdamwLaunch from = a;
+            from.chunks += first;
+            kernel<<<dim3((unsigned)(count * parts)), threads, lds, s>>>(from, partials);
+        });
         return hipGetLastError();
-    }
+    };
+    if (small && sums > 0 && sums <= kAdamwInline)
+        return bits == 32 ? update(update_kernel<32, 4, 1, false, true>, kThreads, 1, 0, sums)
+                          : update(update_kernel<8, 4, 1, false, true>, kThreads, 1, 0, sums);
     decide_kernel<<<1, kThreads, 0, s>>>(a, sums);
-    if (a.nchunks == 0) return hipGetLastError();
-    if (small) {
-        const dim3 grid((unsigned)a.nchunks);
-        if (bits == 32) update_kernel<32, 4, 1, false, false><<<grid, kThreads, 0, s>>>(a, 0);
-        else update_kernel<8, 4, 1, false, false><<<grid, kThreads, 0, s>>>(a, 0);
-        return hipGetLastError();
-    }
+    if (small)
+        return bits == 32 ? update(update_kernel<32, 4, 1, false, false>, kThreads, 1, 0, 0)
+                          : update(update_kernel<8, 4, 1, false, false>, kThreads, 1, 0, 0);
     // Past the caches, all of it.  With fp32 moments 8 streams share the memory, and a wave
     // of 256 elements a workgroup, 18 to a CU (held there by LDS that is asked for and
     // not used), is what it serves best: 326M elements in 1471 us with the check
@@ -591,13 +593,8 @@ hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t 
     // and 1883 through the caches).  With 8-bit moments the arithmetic wants all the waves
     // there are: workgroups of 4 of 1024 elements and no limit 1010 us, 5.2 TB/s (through
     // the caches 1050; 16 waves of 256 elements 1550).
-    if (bits == 32) {
-        const int lds = kLds / 18 - 1024;
-        update_kernel<32, 1, 1, true, false><<<dim3((unsigned)(a.nchunks * (a.chunk / kStateBlock))), 64, lds, s>>>(a, 0);
-    } else {
-        update_kernel<8, 4, 4, true, false><<<dim3((unsigned)a.nchunks), kThreads, 0, s>>>(a, 0);
-    }
-    return hipGetLastError();
+    if (bits == 32) return update(update_kernel<32, 1, 1, true, false>, 64, a.chunk / kStateBlock, kLds / 18 - 1024, 0);
+    return update(update_kernel<8, 4, 4, true, false>, kThreads, 1, 0, 0);
 }
 
 int64_t adamw_chunk(int64_t elements) { return elements < kAdamwLarge ? kAdamwSmallChunk : kAdamwChunk; }
@@ -619,9 +616,15 @@ hipError_t adamw_set_grads(TensorEntry* tensors, const void* const* grads, int64
 template <bool NT>
 static void pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n, bool is_signed, hipStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(n, kThreads * 4));
-    if (is_signed) pack_kernel<true, NT><<<grid, kThreads, 0, s>>>(x, codes, exps, n);
-    else pack_kernel<false, NT><<<grid, kThreads, 0, s>>>(x, codes, exps, n);
+    constexpr int64_t kGroup = kThreads * 4;       // elements of a workgroup
+    auto run = [&](auto kernel) {
+        in_launches(ceil_div(n, kGroup), kThreads, [&](int64_t first, int64_t count) {
+            const int64_t e = first * kGroup;
+            kernel<<<dim3((unsigned)count), kThreads, 0, s>>>(x + e, codes + e, exps + e / kStateBlock, n - e);
+        });
+    };
+    if (is_signed) run(pack_kernel<true, NT>);
+    else run(pack_kernel<false, NT>);
 }
 
 hipError_t moments_pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n, bool is_signed, hipStream_t s)
@@ -635,9 +638,15 @@ hipError_t moments_pack(const float* x, uint8_t* codes, int8_t* exps, int64_t n,
 template <typename T, bool NT>
 static void unpack(const uint8_t* codes, const int8_t* exps, void* out, int64_t n, bool is_signed, hipStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(n, kUnpack * kThreads * Vec<T>::W));
-    if (is_signed) unpack_kernel<T, true, NT><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
-    else unpack_kernel<T, false, NT><<<grid, kThreads, 0, s>>>(codes, exps, static_cast<T*>(out), n);
+    constexpr int64_t kGroup = (int64_t)kUnpack * kThreads * Vec<T>::W;
+    auto run = [&](auto kernel) {
+        in_launches(ceil_div(n, kGroup), kThreads, [&](int64_t first, int64_t count) {
+            const int64_t e = first * kGroup;
+            kernel<<<dim3((unsigned)count), kThreads, 0, s>>>(codes + e, exps + e / kStateBlock, static_cast<T*>(out) + e, n - e);
+        });
+    };
+    if (is_signed) run(unpack_kernel<T, true, NT>);
+    else run(unpack_kernel<T, false, NT>);
 }
 
 hipError_t moments_unpack(const uint8_t* codes, const int8_t* exps, void* out, int64_t n, int type, bool is_signed,

@@ -56,6 +56,22 @@ __device__ __forceinline__ double wave_sum(double x)
     return x;
 }
 
+// Work-items of one launch: HIP counts a grid's in 32 bits, and larger work goes in
+// consecutive launches.  (Defined smaller in a build of the tests.)
+#ifndef ZO_MAX_LAUNCH_ITEMS
+#define ZO_MAX_LAUNCH_ITEMS (int64_t(1) << 31)
+#endif
+constexpr int64_t kMaxLaunchItems = ZO_MAX_LAUNCH_ITEMS;
+
+// `groups` workgroups of `lanes` lanes: launch(first, count) for each launch.
+template <typename F>
+void in_launches(int64_t groups, int lanes, F launch)
+{
+    const int64_t most = kMaxLaunchItems / lanes;
+    for (int64_t first = 0; first < groups; first += most)
+        launch(first, groups - first < most ? groups - first : most);
+}
+
 __host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 

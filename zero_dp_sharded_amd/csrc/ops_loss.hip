@@ -490,11 +490,13 @@ struct Repack {
 };
 
 template <typename T>
-__global__ __launch_bounds__(256) void repack_kernel(Repack<T> a, Repack<T> b, int64_t first, int64_t width, int64_t ld)
+__global__ __launch_bounds__(256) void repack_kernel(Repack<T> a, Repack<T> b, int64_t base, int64_t first, int64_t width,
+                                                     int64_t ld)
 {
-    const bool second = blockIdx.x >= first;
+    const int64_t group = base + blockIdx.x;
+    const bool second = group >= first;
     const Repack<T> r = second ? b : a;
-    const int64_t at = ((blockIdx.x - (second ? first : 0)) * 256 + threadIdx.x) * 8;
+    const int64_t at = ((group - (second ? first : 0)) * 256 + threadIdx.x) * 8;
     if (at >= r.rows * ld) return;
     const int64_t i = at / ld, c = at % ld;
     const T* x = r.x + i * r.stride + c;
@@ -509,6 +511,9 @@ __global__ __launch_bounds__(256) void repack_kernel(Repack<T> a, Repack<T> b, i
 }
 
 // ------------------------------------------------------------------ launches
+//
+// (Of all of them only the copies could pass a launch's work-items: a product's tiles are
+// fewer than 2^22, by what memory its operands take, and the rest goes by chunks of tokens.)
 
 // What the products' loads need of an address and a stride.
 bool loads_as_it_is(const void* p, int64_t stride)
@@ -589,8 +594,9 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
     if (many > 0) {
         const int64_t first = ceil_div(copies[0].rows * p.width_ld, 2048);
         const int64_t all = first + (many > 1 ? ceil_div(copies[1].rows * p.width_ld, 2048) : 0);
-        if (all > 0)
-            repack_kernel<T><<<dim3((unsigned)all), 256, 0, s>>>(copies[0], copies[many - 1], first, p.width, p.width_ld);
+        in_launches(all, 256, [&](int64_t base, int64_t count) {
+            repack_kernel<T><<<dim3((unsigned)count), 256, 0, s>>>(copies[0], copies[many - 1], base, first, p.width, p.width_ld);
+        });
     }
     auto total = [&](float* loss) {
         total_kernel<<<1, 1024, 0, s>>>(a.targets, a.losses, p.tokens, a.ignore_index, a.grad_scale, kHold<T>, alpha, loss);

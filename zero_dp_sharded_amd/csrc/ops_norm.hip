@@ -460,25 +460,52 @@ __global__ __launch_bounds__(1024) void fold_kernel(const float* partial, int64_
 
 constexpr int64_t kLongRows = 64;      // workgroups over the rows of very long ones
 
+// The arrays from row `first` on.
+template <typename T>
+NormForward from_row(NormForward a, int64_t first)
+{
+    a.x = static_cast<const T*>(a.x) + first * a.x_stride;
+    a.y = static_cast<T*>(a.y) + first * a.y_stride;
+    if (a.mean != nullptr) a.mean += first;
+    if (a.rstd != nullptr) a.rstd += first;
+    a.rows -= first;
+    return a;
+}
+
+template <typename T>
+NormBackward from_row(NormBackward a, int64_t first)
+{
+    a.dy = static_cast<const T*>(a.dy) + first * a.dy_stride;
+    a.x = static_cast<const T*>(a.x) + first * a.x_stride;
+    a.dx = static_cast<T*>(a.dx) + first * a.dx_stride;
+    a.mean += first;
+    a.rstd += first;
+    a.rows -= first;
+    return a;
+}
+
 template <typename T, typename A, bool PAST>
 hipError_t forward_rows(const NormForward& a, hipStream_t s)
 {
     constexpr int W = Vec<T>::W;
-    if (a.rows == 0) return hipSuccess;
     // lanes that a row keeps busy with one vector each; a wave keeps up to 64 elements
     // of a lane in registers
     const int64_t lanes = ceil_div(a.width, W);
-    const dim3 by4((unsigned)ceil_div(a.rows, 4)), by1((unsigned)a.rows);
+    auto run = [&](auto kernel, int threads, int rows) {
+        in_launches(ceil_div(a.rows, rows), threads, [&](int64_t first, int64_t count) {
+            kernel<<<dim3((unsigned)count), threads, 0, s>>>(from_row<T>(a, first * rows));
+        });
+    };
     constexpr int M = 8 / W;               // vectors of a lane in 8 elements
-    if (lanes <= 64 * M) forward_kernel<T, A, PAST, 1, M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 128 * M) forward_kernel<T, A, PAST, 1, 2 * M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 256 * M) forward_kernel<T, A, PAST, 1, 4 * M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 384 * M) forward_kernel<T, A, PAST, 1, 6 * M><<<by4, 256, 0, s>>>(a);
-    else if (lanes <= 512 * M) forward_kernel<T, A, PAST, 4, 2 * M><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 768 * M) forward_kernel<T, A, PAST, 4, 3 * M><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 1024 * M) forward_kernel<T, A, PAST, 4, 4 * M><<<by1, 256, 0, s>>>(a);
-    else if (lanes <= 2048 * M) forward_kernel<T, A, PAST, 16, 2 * M><<<by1, 1024, 0, s>>>(a);
-    else forward_long_kernel<T, A, PAST><<<by1, 1024, 0, s>>>(a);
+    if (lanes <= 64 * M) run(forward_kernel<T, A, PAST, 1, M>, 256, 4);
+    else if (lanes <= 128 * M) run(forward_kernel<T, A, PAST, 1, 2 * M>, 256, 4);
+    else if (lanes <= 256 * M) run(forward_kernel<T, A, PAST, 1, 4 * M>, 256, 4);
+    else if (lanes <= 384 * M) run(forward_kernel<T, A, PAST, 1, 6 * M>, 256, 4);
+    else if (lanes <= 512 * M) run(forward_kernel<T, A, PAST, 4, 2 * M>, 256, 1);
+    else if (lanes <= 768 * M) run(forward_kernel<T, A, PAST, 4, 3 * M>, 256, 1);
+    else if (lanes <= 1024 * M) run(forward_kernel<T, A, PAST, 4, 4 * M>, 256, 1);
+    else if (lanes <= 2048 * M) run(forward_kernel<T, A, PAST, 16, 2 * M>, 1024, 1);
+    else run(forward_long_kernel<T, A, PAST>, 1024, 1);
     return hipGetLastError();
 }
 
@@ -508,7 +535,9 @@ hipError_t backward_rows(const NormBackward& a, hipStream_t s)
         else if (lanes <= 1024 * M) run(backward_kernel<T, A, PAST, 4, 4, 4 * M>, 4, 1, 4 * M, 2 * kCUs);
         else if (lanes <= 2048 * M) run(backward_kernel<T, A, PAST, 8, 8, 4 * M>, 8, 1, 4 * M, kCUs);
         else {
-            backward_long_kernel<T, A, PAST><<<dim3((unsigned)a.rows), 1024, 0, s>>>(a);
+            in_launches(a.rows, 1024, [&](int64_t first, int64_t count) {
+                backward_long_kernel<T, A, PAST><<<dim3((unsigned)count), 1024, 0, s>>>(from_row<T>(a, first));
+            });
             parts = a.rows < kLongRows ? a.rows : kLongRows;
             const int64_t slab = ceil_div(a.rows, parts);
             parts = ceil_div(a.rows, slab);
