@@ -41,21 +41,23 @@ def test_the_child_loads_the_split_build():
 
 
 def test_more_rows_than_a_launch_holds():
-    """2^26 + 5 rows of 8: a wave a row would be 2^32 work-items.  Each block of rows holds
-    the same values, so every one must come out as the first (in place, and both ways)."""
+    """More than 2^26 rows of 8: a wave a row would be 2^32 work-items.  16384 blocks of the
+    same 4099 rows, so every block must come out as the rows alone do (in place)."""
     import torch
     import zero_dp_sharded_amd as zs
-    rows, width, period = (1 << 26) + 5, 8, 4099
+    blocks, period, width = 16384, 4099, 8
+    rows = blocks * period
+    assert rows > 1 << 26
     g = torch.Generator(device="cuda").manual_seed(1)
     few = torch.randn(period, width, generator=g, device="cuda").half()
     w = torch.randn(width, generator=g, device="cuda").half()
     want, mean0, rstd0 = torch.empty_like(few), torch.empty(period, device="cuda"), torch.empty(period, device="cuda")
     zs.zero_layernorm_forward(few, w, w, want, mean0, rstd0)
-    at = torch.arange(rows, device="cuda") % period
-    x = few[at]
+    x = few.expand(blocks, period, width).contiguous()
+    flat = x.view(rows, width)
     mean, rstd = torch.full((rows,), float("nan"), device="cuda"), torch.full((rows,), float("nan"), device="cuda")
-    zs.zero_layernorm_forward(x, w, w, x, mean, rstd)
-    for k in range(0, rows, 1 << 24):
-        part = slice(k, min(rows, k + (1 << 24)))
-        assert torch.equal(x[part], want[at[part]]) and torch.equal(mean[part], mean0[at[part]])
-        assert torch.equal(rstd[part], rstd0[at[part]])
+    zs.zero_layernorm_forward(flat, w, w, flat, mean, rstd)
+    for k in range(0, blocks, 1024):
+        part = slice(k, k + 1024)
+        assert (x[part] == want).all() and (mean.view(blocks, period)[part] == mean0).all()
+        assert (rstd.view(blocks, period)[part] == rstd0).all()
