@@ -70,3 +70,24 @@ def test_zeros_keep_their_signs():
         got, want = one_step(One(p, m, np.zeros(8), g), hp, 1)
         for name, a, b in zip(("master", "m", "v"), got, want):
             assert np.array_equal(a, b), (name, wd, a, b)
+
+
+@pytest.mark.parametrize("t", [1 << 40, 1 << 62])
+def test_a_counter_of_any_size_is_taken_at_once(t):
+    """The host's powers of the betas end where they no longer change; a step from there
+    has corrections of 1."""
+    hp = zs.AdamHParams(lr=1e-2)
+    p, m, v, g = (np.linspace(a, 1, 300).astype(np.float32) for a in (-1, -0.5, 0.1, -0.2))
+    model, plain = One(p, m, v, g), One(p, m, v, g)
+    h = zs.zero_adamw_init(model.tensors, hp=hp, ls=zs.LossScaleCfg(init_scale=1.0, dynamic=0))
+    k = zs.zero_adamw_init(plain.tensors, hp=dataclasses.replace(hp, bias_correction=0), ls=zs.LossScaleCfg(init_scale=1.0, dynamic=0))
+    try:
+        zs.zero_adamw_set_counters(h, t, 1.0, 5)
+        assert zs.zero_adamw_get_counters(h) == (t, 1.0, 5)
+        zs.zero_adamw_step(h)
+        zs.zero_adamw_step(k)
+        assert zs.zero_adamw_result(h).step_t == t + 1
+        assert torch.equal(model.tensors[0].master, plain.tensors[0].master)
+    finally:
+        zs.zero_adamw_destroy(h)
+        zs.zero_adamw_destroy(k)

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/zero_ops.h"
+#include "beta_pow.h"
 #include "ops_internal.h"
 
 namespace {
@@ -225,15 +226,6 @@ zero_status check_scale(const zero_loss_scale_cfg* ls, const char* who)
     if (ls->dynamic != 0 && ls->dynamic != 1) return fail(ZERO_ERR_INVALID_ARG, "%s: dynamic must be 0 or 1", who);
     if (ls->growth_interval < 1) return fail(ZERO_ERR_INVALID_ARG, "%s: growth_interval must be >= 1", who);
     return ZERO_OK;
-}
-
-double beta_pow(double beta, int64_t t)
-{
-    const double b = (double)(float)beta;
-    double p = 1.0;
-    // (a power that has fallen to 0 stays there)
-    for (int64_t k = 0; k < t && p != 0.0; ++k) p = p * b;
-    return p;
 }
 
 // The arrays of one tensor, host checks only; appended to `all`.

@@ -17,6 +17,7 @@
 #include <unordered_set>
 
 #include "../../include/zero_shard.h"
+#include "beta_pow.h"
 #include "zero_kernels.h"
 #include "zero_layout.h"
 
@@ -223,15 +224,6 @@ uint32_t lds_reserve_for(int lds_per_cu, int lds_per_block_max, int per_cu)
     if (r > lds_per_block_max) r = lds_per_block_max;
     if (r < 0) r = 0;
     return (uint32_t)(r & ~(int64_t)511);
-}
-
-// beta^t as a product of t copies of (double)(float)beta, as the header says.
-double beta_pow(double beta, int64_t t)
-{
-    const double b = (double)(float)beta;
-    double p = 1.0;
-    for (int64_t k = 0; k < t; ++k) p = p * b;
-    return p;
 }
 
 void next_scale(zero_shard_s* h, int overflow, double* scale, int64_t* good)
