@@ -179,7 +179,9 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
                             zero_adamw_t* out);
 
 /* Other gradient arrays, one for each tensor of the handle, from the next step on
- * `stream` on (an enqueue, 256 pointers a launch). */
+ * `stream` on (an enqueue, 256 pointers a launch).  As at init, they must not overlap an
+ * array that the step writes; the old ones must outlive the steps that read them.
+ * Errors: STATE, INVALID_ARG (NULL, n not the handle's, misaligned, overlaps), HIP. */
 zero_status zero_adamw_set_grads(zero_adamw_t h, const void* const* grads, int32_t n, void* stream);
 
 /*

@@ -280,6 +280,7 @@ struct zero_adamw_s {
     zo::AdamwState* host_state = nullptr;      // pinned
     std::vector<int64_t> numel;
     std::vector<int32_t> type;
+    std::vector<Array> written;                // by address; they overlap no other
 };
 
 namespace {
@@ -569,6 +570,8 @@ zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const z
                 h->numel.push_back(t.numel);
                 h->type.push_back(t.type);
             }
+            for (const Array* a : order)
+                if (a->written) h->written.push_back(*a);
             std::lock_guard<std::mutex> lk(g_live_mu);
             g_live.insert(h);
         } catch (...) {
@@ -591,6 +594,10 @@ zero_status zero_adamw_set_grads(zero_adamw_t h, const void* const* grads, int32
         const int e = type_bytes(h->type[i]);
         const Array a = flat("a gradient", grads[i], (size_t)h->numel[i] * e, e, false);
         if (const zero_status s = check_arrays(&a, 1, who)) return s;
+        const auto w = std::upper_bound(h->written.begin(), h->written.end(), a.begin(),
+                                        [](uintptr_t at, const Array& x) { return at < x.end(); });
+        if (w != h->written.end() && overlap(a, *w))
+            return fail(ZERO_ERR_INVALID_ARG, "%s: gradient %d overlaps a tensor's %s", who, (int)i, w->name);
         if (const zero_status s = on_device(a, h->device, who)) return s;
     }
     for (int32_t i = 0; i < n; i += zo::kGradsPerLaunch) {
