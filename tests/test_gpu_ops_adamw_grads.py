@@ -44,3 +44,32 @@ def test_gradients_that_overlap_what_the_step_writes_are_refused(bits):
         assert all(torch.equal(a, b) for a, b in zip(model.arrays(), again.arrays()))
     finally:
         zs.zero_adamw_destroy(h)
+
+
+def test_old_gradients_outlive_a_step_that_still_waits():
+    """A step is enqueued on a stream that is busy, the handle gets other gradients, the old
+    ones are let go, and their memory is asked for again on their own stream."""
+    sizes = [70001, 4096, 300000]
+    model, want = make(sizes, ["fp32"], 32, seed=9), make(sizes, ["fp32"], 32, seed=9)
+    kw = dict(hp=HP, ls=zs.LossScaleCfg(dynamic=0))
+    h, k = zs.zero_adamw_init(model.tensors, **kw), zs.zero_adamw_init(want.tensors, **kw)
+    try:
+        zs.zero_adamw_step(k)
+        torch.cuda.synchronize()
+        mine = [g.clone() for g in model.grads]
+        zs.zero_adamw_set_grads(h, mine)
+        places = {g.data_ptr() for g in mine}
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)
+        zs.zero_adamw_step(h, stream=s)
+        zs.zero_adamw_set_grads(h, model.grads, stream=s)
+        del mine
+        others = [torch.full((n,), float("nan"), device=DEV) for n in sizes for _ in range(2)]
+        torch.cuda.synchronize()
+        assert not places & {g.data_ptr() for g in others}
+        assert all(torch.equal(a, b) for a, b in zip(model.arrays(), want.arrays()))
+    finally:
+        zs.zero_adamw_destroy(h)
+        zs.zero_adamw_destroy(k)

@@ -304,8 +304,17 @@ class AdamWTensor:
             -1.0 if self.weight_decay is None else self.weight_decay, self.lr_scale)
 
 
-# the tensors of each live handle made through this binding (kept from being freed
-# under it), and the gradients given since
+@dataclass
+class _Held:
+    """What a live handle made through this binding reads and writes, kept from being
+    freed under it."""
+    tensors: list
+    grads: list
+    # those that steps of these gradients were enqueued on and not waited for, as hipStream_t (a
+    # stream that is not torch's must live as long)
+    streams: set
+
+
 _adamw = {}
 
 
@@ -318,46 +327,68 @@ def zero_adamw_init(tensors: Sequence[AdamWTensor], *, hp: AdamHParams, ls: Loss
     h = _vp()
     _check(lib().zero_adamw_init(arr, len(tensors), ctypes.byref(hp.to_c()), ctypes.byref(ls.to_c()),
                                  ctypes.byref(cfg), ctypes.byref(h)), "zero_adamw_init")
-    _adamw[h.value] = [list(tensors), [t.grad for t in tensors]]
+    _adamw[h.value] = _Held(list(tensors), [t.grad for t in tensors], set())
     return h.value
 
 
 def zero_adamw_set_grads(h: int, grads: Sequence, stream=None) -> None:
-    """Other gradient tensors, of the same types and sizes, for the steps that follow."""
+    """Other gradient tensors, of the same types and sizes, for the steps that follow.  The
+    old ones are let go, but their memory is not used again before the steps that were
+    enqueued through this binding have read them (of a graph's replays the caller knows)."""
     torch or _load()
     known = _adamw.get(h)
     if known is not None:
-        if len(grads) != len(known[1]):
-            raise ValueError(f"expected {len(known[1])} gradients, got {len(grads)}")
-        ptrs = [_flat(f"gradient {i}", g, old.dtype, old.numel()) for i, (g, old) in enumerate(zip(grads, known[1]))]
+        if len(grads) != len(known.grads):
+            raise ValueError(f"expected {len(known.grads)} gradients, got {len(grads)}")
+        ptrs = [_flat(f"gradient {i}", g, old.dtype, old.numel()) for i, (g, old) in enumerate(zip(grads, known.grads))]
     else:
         ptrs = [g.data_ptr() for g in grads]
     _check(lib().zero_adamw_set_grads(h, (_vp * len(ptrs))(*ptrs), len(ptrs), _current(stream)),
            "zero_adamw_set_grads")
     if known is not None:
-        known[1] = list(grads)
+        for s in known.streams:
+            used = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+            for g in known.grads:
+                if g.numel():
+                    g.record_stream(used)
+        known.grads, known.streams = list(grads), set()
 
 
 def zero_adamw_step(h: int, hp: Optional[AdamHParams] = None, stream=None) -> None:
     """Enqueue one step of every tensor (capturable in a graph)."""
     torch or _load()
     hpc = ctypes.byref(hp.to_c()) if hp is not None else None
-    _check(lib().zero_adamw_step(h, hpc, _current(stream)), "zero_adamw_step")
+    s = _current(stream)
+    _check(lib().zero_adamw_step(h, hpc, s), "zero_adamw_step")
+    known = _adamw.get(h)
+    if known is not None:
+        known.streams.add(s)
 
 
 def zero_adamw_result(h: int, stream=None) -> StepInfo:
     """The last step's result; waits for it."""
     torch or _load()
     out = ZeroStepInfo()
-    _check(lib().zero_adamw_result(h, _current(stream), ctypes.byref(out)), "zero_adamw_result")
+    s = _current(stream)
+    _check(lib().zero_adamw_result(h, s, ctypes.byref(out)), "zero_adamw_result")
+    _waited(h, s)
     return StepInfo.from_c(out)
+
+
+def _waited(h: int, stream: int) -> None:
+    """The stream's steps have ended."""
+    known = _adamw.get(h)
+    if known is not None:
+        known.streams.discard(stream)
 
 
 def zero_adamw_get_counters(h: int, stream=None):
     torch or _load()
     t, s, g = _i64(), _f64(), _i64()
-    _check(lib().zero_adamw_get_counters(h, _current(stream), ctypes.byref(t), ctypes.byref(s),
+    at = _current(stream)
+    _check(lib().zero_adamw_get_counters(h, at, ctypes.byref(t), ctypes.byref(s),
                                          ctypes.byref(g)), "zero_adamw_get_counters")
+    _waited(h, at)
     return t.value, s.value, g.value
 
 
