@@ -498,7 +498,12 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const float* x, uint8_t*
 {
     const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
     const int lane = threadIdx.x & 63;
-    const f4 v = load4<NT>(x, e, n);
+    f4 v = load4<NT>(x, e, n);
+    if constexpr (!SIGNED) {
+        // negative inputs are 0, for the block's exponent too (a NaN stays one)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = v[k] < 0.0f ? 0.0f : v[k];
+    }
     uint32_t top = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const float* x, uint8_t*
     for (int k = 0; k < 4; ++k) {
         // to the nearest: half a code, less half of the noise's last place
         if constexpr (SIGNED) c |= encode_m(v[k], be, 32767) << (8 * k);
-        else c |= encode_v(v[k] > 0.0f ? v[k] : 0.0f, be, 32767) << (8 * k);
+        else c |= encode_v(v[k], be, 32767) << (8 * k);
     }
     store_codes<NT>(codes, e, n, c);
     if (lane == 0 && e < n) exps[e / kStateBlock] = (int8_t)be;
