@@ -118,7 +118,7 @@ zero_status zero_vocab_loss_workspace(int64_t tokens, int64_t vocab, int64_t wid
 
 /* Errors: INVALID_ARG (NULL or misaligned arrays, one gradient without the other,
  * sizes < 0, vocab or width < 1, strides < width, max_tokens outside [0, 65535],
- * grad_scale not finite, workspace too small, overlaps), UNSUPPORTED (ZERO_FP32;
+ * grad_scale not finite in fp32, workspace too small, overlaps), UNSUPPORTED (ZERO_FP32;
  * width > 2^20, vocab > 2^21 - 64, tokens > 2^31 - 1), HIP. */
 zero_status zero_vocab_loss(const zero_vocab_loss_desc* desc, const void* hidden, const void* weight,
                             const int64_t* targets, float* losses, float* lse, float* loss,

@@ -452,7 +452,8 @@ zero_status zero_vocab_loss(const zero_vocab_loss_desc* d, const void* hidden, c
     if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
     if (t == ZERO_FP32) return fail(ZERO_ERR_UNSUPPORTED, "%s: hidden states and weight are of a 2-byte type", who);
     if (const zero_status s = check_loss_sizes(d->tokens, d->vocab, d->width, d->max_tokens, who)) return s;
-    if (!std::isfinite(d->grad_scale)) return fail(ZERO_ERR_INVALID_ARG, "%s: grad_scale must be finite", who);
+    // (an infinite factor would make NaN of the gradients that are 0)
+    if (!std::isfinite((float)d->grad_scale)) return fail(ZERO_ERR_INVALID_ARG, "%s: grad_scale must be finite in fp32", who);
     const bool gradient = dweight != nullptr;
     if (d->tokens > 0 && gradient != (dhidden != nullptr))
         return fail(ZERO_ERR_INVALID_ARG, "%s: dhidden and dweight are given both or neither", who);
