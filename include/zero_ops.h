@@ -218,7 +218,8 @@ zero_status zero_adamw_destroy(zero_adamw_t h);
 /*
  * Between fp32 (or, out, bf16: it holds every such value exactly) and 8-bit moments
  * as above: n elements in blocks of 256, is_signed 1 for exp_avg's format and 0 for
- * exp_avg_sq's (whose negative inputs become 0).  pack rounds to the nearest.
+ * exp_avg_sq's (whose negative inputs become 0).  pack rounds to the nearest (a value within
+ * 2^-17 of a step above the middle goes down).
  * Errors: INVALID_ARG (NULL with n > 0, n < 0, is_signed not 0 or 1, out_type neither
  * ZERO_FP32 nor ZERO_BF16, misaligned or overlapping arrays), HIP.
  */

@@ -91,3 +91,29 @@ def test_a_counter_of_any_size_is_taken_at_once(t):
     finally:
         zs.zero_adamw_destroy(h)
         zs.zero_adamw_destroy(k)
+
+
+@pytest.mark.parametrize("signed,least", [(True, -14), (False, -30)])
+def test_codes_at_the_borders_of_the_noise(signed, least):
+    """Values below the code's least normal exponent, as near to a border of the rounding as
+    fp32 has them on either side: the held value is the definition's."""
+    from test_gpu_ops_adamw import held, unpack
+    r = 32767
+    x = []
+    for code in range(9):
+        border = code + 1 - (r + 0.5) / 65536                       # of steps: from here on the code is the next
+        at = np.float32(border)
+        for away in range(-6, 7):
+            x.append(np.float32(at) + np.float32(away) * np.spacing(at))
+    x = np.array(x, dtype=np.float32) * np.float32(2.0 ** (least - 3))
+    for e in (-90, -1, 0, 17):
+        values = np.zeros(512, dtype=np.float32)
+        values[:x.size] = x * np.float32(2.0 ** e)
+        values[200], values[300:300 + x.size] = 1.875 * 2.0 ** e, -x * np.float32(2.0 ** e) if signed else x * np.float32(2.0 ** e)
+        values[511] = 1.5 * 2.0 ** e
+        v = torch.from_numpy(values).to(DEV)
+        codes, exps = torch.empty(512, dtype=torch.uint8, device=DEV), torch.empty(2, dtype=torch.int8, device=DEV)
+        zs.zero_moments_pack(v, codes, exps, signed=signed)
+        assert (exps == e).all()
+        want = held(v, torch.full((512,), r, device=DEV), least, signed)
+        assert torch.equal(unpack(codes, exps, signed).double(), want), e

@@ -100,24 +100,33 @@ __device__ __forceinline__ int block_exp(uint32_t bits)
     return e < kExpLeast ? kExpLeast : e > kExpNaN ? kExpNaN : e;
 }
 
-// A value to a code: scaled so that the code's least normal exponent is fp32's, the
-// code is the top bits of the float's magnitude, and noise below them, added, rounds.
-// LEAST: 14 (m) or 30 (v).
-template <int LEAST>
-__device__ __forceinline__ uint32_t encode(float x, int block, uint32_t r16)
+// Four values to codes, side by side: scaled so that the code's least normal exponent is
+// fp32's, the code is the top bits of the float's magnitude, and 16 bits of noise below them,
+// added, round.  LEAST: 14 (m) or 30 (v).  Below the least normal exponent the scaling would
+// round by itself, to 2^-20 of a code's step, and could carry a value past the noise's border:
+// there the bits are those of the value as an integer, cut off.  (They are the fewest: one
+// test for four.)
+template <int LEAST, bool SIGNED>
+__device__ __forceinline__ uint32_t encode(f4 x, int block, const uint32_t (&noise)[4])
 {
-    const float z = __builtin_amdgcn_ldexpf(fabsf(x), LEAST - 126 - block);
-    return (__builtin_bit_cast(uint32_t, z) + (r16 << 4) + 8) >> 20;
-}
-
-__device__ __forceinline__ uint32_t encode_m(float x, int block, uint32_t r16)
-{
-    return (encode<14>(x, block, r16) & 127) | (__builtin_bit_cast(uint32_t, x) >> 24 & 128);
-}
-
-__device__ __forceinline__ uint32_t encode_v(float x, int block, uint32_t r16)
-{
-    return encode<30>(x, block, r16) & 255;
+    uint32_t z[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_ldexpf(fabsf(x[k]), LEAST - 126 - block));
+    const uint32_t a = z[0] < z[1] ? z[0] : z[1], b = z[2] < z[3] ? z[2] : z[3];
+    if (__builtin_expect((a < b ? a : b) <= 0x800000u, 0)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (z[k] <= 0x800000u) z[k] = (uint32_t)__builtin_amdgcn_ldexpf(fabsf(x[k]), LEAST + 23 - block);
+    }
+    uint32_t codes = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t c = (z[k] + (noise[k] << 4) + 8) >> 20;
+        const float xk = x[k];      // (the bits of a vector's element itself come out as an older value's)
+        if constexpr (SIGNED) codes |= ((c & 127) | (__builtin_bit_cast(uint32_t, xk) >> 24 & 128)) << (8 * k);
+        else codes |= (c & 255) << (8 * k);
+    }
+    return codes;
 }
 
 // The code in bits 8 k to 8 k + 7, and what it stands for.
@@ -428,14 +437,15 @@ __device__ __forceinline__ void update_part(const AdamwLaunch& a, const TensorEn
                     top_v = y > top_v ? y : top_v;
                 }
             const int em = block_exp(wave_max(top_m)), ev = block_exp(wave_max(top_v));
-            uint32_t xm = 0, xv = 0;
+            uint32_t low[4], high[4];
             const uint32_t at = key + (uint32_t)e * 0xDDB3D743u;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t r = mix(at + k * 0xDDB3D743u);
-                xm |= encode_m(m[u][k], em, r & 0xffffu) << (8 * k);
-                xv |= encode_v(v[u][k], ev, r >> 16) << (8 * k);
+                low[k] = r & 0xffffu;
+                high[k] = r >> 16;
             }
+            const uint32_t xm = encode<14, true>(m[u], em, low), xv = encode<30, false>(v[u], ev, high);
             store_codes<NT>(static_cast<uint8_t*>(t.m), e, n, xm);
             store_codes<NT>(static_cast<uint8_t*>(t.v), e, n, xv);
             const int64_t first = e - lane * 4;       // the wave's block
@@ -511,13 +521,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const float* x, uint8_t*
         top = b > top ? b : top;
     }
     const int be = block_exp(wave_max(top));
-    uint32_t c = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        // to the nearest: half a code, less half of the noise's last place
-        if constexpr (SIGNED) c |= encode_m(v[k], be, 32767) << (8 * k);
-        else c |= encode_v(v[k], be, 32767) << (8 * k);
-    }
+    // to the nearest: half a code's step, less half of the noise's last place
+    const uint32_t half[4] = {32767, 32767, 32767, 32767};
+    const uint32_t c = encode<SIGNED ? 14 : 30, SIGNED>(v, be, half);
     store_codes<NT>(codes, e, n, c);
     if (lane == 0 && e < n) exps[e / kStateBlock] = (int8_t)be;
 }
