@@ -137,7 +137,10 @@ zero_status zero_vocab_loss(const zero_vocab_loss_desc* desc, const void* hidden
  *    mantissa, for exp_avg_sq 5 and 3 bits.  With field f and mantissa k, c is
  *    (1 + k/8) * 2^(f - 15) or (f = 0) k * 2^-17 for exp_avg, and
  *    (1 + k/8) * 2^(f - 31) or k * 2^-33 for exp_avg_sq.  e = 127 marks a block
- *    that held a value not finite (or above 1.875 * 2^126): it stands for NaN.
+ *    that held a value not finite (or above 1.875 * 2^126): it stands for NaN.  No
+ *    exponent is below -100: less is read as -100.  An exp_avg_sq below 2^-33 of its block's
+ *    largest may be held as 0, and its element's next updates are then too large: gradients
+ *    that differ by more than 2^15 within 256 elements want 32 bits.
  *    All bytes 0 are all zeros.
  * weight_decay < 0 takes the hyper-parameters'; the learning rate is lr * lr_scale.
  * Arrays must not overlap and must outlive the handle.

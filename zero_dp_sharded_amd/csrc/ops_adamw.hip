@@ -21,8 +21,9 @@
 //     m: sign, 4 bits of exponent, 3 of mantissa;  v (never negative): 5 and 3
 // with the largest code 1.875 * 2^e, the normal range down to 2^-14 (m) and 2^-30 (v)
 // of 2^e, and gradual underflow below.  v has no square root taken before it is held:
-// 5 bits of exponent cover gradients that differ by 2^16 within a block, and a v
-// that falls to 0 beside an m that does not would make the update explode.
+// 5 bits of exponent cover gradients that differ by 2^15 within a block (of constant ones no
+// update is above twice Adam's).  Further down a v falls to 0 beside an m that does not, and
+// single updates grow: 28 times Adam's at 2^16, 200 times at 2^20.
 // Rounding is up or down at random, with the odds that keep the mean: v changes by
 // a thousandth a step, less than half of a code, and rounding to the nearest would
 // hold it where it is for ever.  The random bits are a hash of (seed, step, tensor,
