@@ -18,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,8 +53,7 @@ FLAGS = [
 
 
 def _compile(sources, objdir, verbose, extra=()):
-    objs = []
-    for src in sources:
+    def one(src):
         obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
         cmd = [HIPCC, *FLAGS, *extra, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -66,8 +66,10 @@ def _compile(sources, objdir, verbose, extra=()):
             raise RuntimeError(f"hipcc failed for {src}:\n{err}")
         if verbose and err.strip():
             print(err, file=sys.stderr)
-        objs.append(obj)
-    return objs
+        return obj
+
+    with ThreadPoolExecutor(4) as pool:
+        return list(pool.map(one, sources))
 
 
 def _link(objs, lib, verbose):
