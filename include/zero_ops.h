@@ -112,7 +112,9 @@ typedef struct {
 } zero_vocab_loss_desc;
 
 /* Bytes of workspace (256-byte aligned) for these sizes, without (gradient = 0)
- * or with the gradients. */
+ * or with the gradients.  Fewer tokens may need more (their products go in more parts): a
+ * workspace for several counts is as large as the largest of their answers.  It has room for a
+ * copy of both operands, also where none is made. */
 zero_status zero_vocab_loss_workspace(int64_t tokens, int64_t vocab, int64_t width,
                                       int64_t max_tokens, int32_t gradient, int64_t* bytes);
 

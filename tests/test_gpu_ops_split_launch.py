@@ -15,8 +15,8 @@ from conftest import ROOT
 pytestmark = pytest.mark.gpu
 
 SPLIT_LIB = os.path.join(ROOT, "zero_dp_sharded_amd", "variants", "split_launch", "libzeroops.so")
-FILES = ["test_gpu_ops_norm.py", "test_gpu_ops_norm_values.py", "test_gpu_ops_norm_many.py", "test_gpu_ops_moments.py", "test_gpu_ops_adamw.py", "test_gpu_ops_adamw_values.py", "test_gpu_ops_adamw_many.py",
-         "test_gpu_ops_loss.py"]
+FILES = ["test_gpu_ops_norm.py", "test_gpu_ops_norm_values.py", "test_gpu_ops_norm_many.py", "test_gpu_ops_adamw.py",
+         "test_gpu_ops_adamw_values.py", "test_gpu_ops_adamw_many.py", "test_gpu_ops_moments.py", "test_gpu_ops_loss.py"]
 
 
 def _child(args, timeout):

@@ -719,7 +719,7 @@ TileChoice choose(int64_t rows, int64_t cols, int64_t steps, bool may_split, int
     *splits = 1;
     for (int nj = 4; nj <= (few ? 4 : 5); ++nj) {
         const TileChoice c{few ? 2 : 8, nj};
-        // no part of less than 8 steps, and no more than four rounds of them
+        // a part for every 8 steps at most (9 may go as 4 and 5), and no more than four rounds of them
         const int64_t tiles = ceil_div(rows, 32 * c.ni) * ceil_div(cols, 64 * c.nj);
         const int64_t most = may_split ? (steps + 7) / 8 : 1;
         for (int64_t k = 1; k <= most && (k == 1 || tiles * k <= 4 * kCUs); ++k) {

@@ -4,7 +4,9 @@ tensors with moments in 32 or 8 bits.
 
 A thin ctypes binding, as the package's binding of libzeroshard.so is: functions
 carry the C names, tensors become device pointers, strides and types, and the
-library's checks raise ZeroError.  There is no CPU fallback.
+library's checks raise ZeroError.  There is no CPU fallback.  Calls enqueue: a tensor given on
+a stream other than its own must live, as for any such use, until that work has ended
+(Tensor.record_stream); an AdamW handle keeps its tensors itself.
 """
 from __future__ import annotations
 
