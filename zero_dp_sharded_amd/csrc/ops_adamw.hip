@@ -6,11 +6,11 @@
 // gradients, 1 KiB of fp32), and a wave's 256 elements are a block of the 8-bit
 // states.  Bound by memory: per element and step 28 bytes with fp32 moments and 2-byte
 // storage, 16 with 8-bit moments, and the check reads the gradient once more.  326M
-// elements take 1463 us with the check, 6.7 TB/s, as a copy past the caches does.  With
+// elements take 1476 us with the check, 6.6 TB/s, as a copy past the caches does.  With
 // 8-bit moments the arithmetic binds as well, spare as it is (a division by a step's
 // constant in 3 operations, one hash for both moments' noise, powers of two by ldexp):
-// 117 vector instructions an element, 1000 us, 5.2 TB/s.  Up to 2M elements it is two
-// launches and their latency: 1.8M in 16.7 us.
+// 120 vector instructions an element, 1040 us, 5.0 TB/s.  Up to 2M elements it is two
+// launches and their latency: 1.8M in 16.5 us.
 //
 // The arithmetic is that of the shard's Adam (each operation rounded to fp32 in
 // the order written, no fused multiply-adds), so that a tensor's update has the same bits
@@ -603,8 +603,9 @@ hipError_t adamw_step(const AdamwLaunch& a, int bits, bool checked, hipStream_t 
     // not used), is what it serves best: 326M elements in 1471 us with the check
     // (16 a CU: 1488, 14: 1542, 20: 1527; workgroups of 4 waves of 1024 elements: 1720,
     // and 1883 through the caches).  With 8-bit moments the arithmetic wants all the waves
-    // there are: workgroups of 4 of 1024 elements and no limit 1010 us, 5.2 TB/s (through
-    // the caches 1050; 16 waves of 256 elements 1550).
+    // there are: workgroups of 4 of 1024 elements and no limit 1010 us (through the caches
+    // 1050; 16 waves of 256 elements 1550; timed before the smallest codes were rounded once,
+    // which made it 1040).
     if (bits == 32) return update(update_kernel<32, 1, 1, true, false>, 64, a.chunk / kStateBlock, kLds / 18 - 1024, 0);
     return update(update_kernel<8, 4, 4, true, false>, kThreads, 1, 0, 0);
 }

@@ -13,8 +13,9 @@
 // gradients cost three matrix products in all (6 tokens vocab width operations);
 // computing the logits again would make it four.  What is held are the exponentials of a
 // chunk of tokens, 2 bytes each: 0.8 GB at 8192 tokens and 50257 ids, of 288; the
-// pass over them takes 310 us of 3750 (5.3 TB/s).  The three products take 1160, 1140 and
-// 1050 us there, 1140 to 1260 TFLOP/s of the 1550 that a large library product reaches:
+// pass over them takes 330 us of 3710 (5.2 TB/s).  The three products take 1240, 1215 and
+// 1130 us there in the mean, 1060 to 1170 TFLOP/s of the 1550 that a large library product
+// reaches (at best 1157, 1122 and 1031; by the box's clock the whole takes 3710 to 3970):
 // ops_gemm.h says what bounds them.  (bf16 could do without the pass, by
 // exponentials without a maximum and the factors exp(-lse) in the second product's
 // epilogue and in a copy of H; that took 7% less, and the copy's rounding made the

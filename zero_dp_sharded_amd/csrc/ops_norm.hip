@@ -12,10 +12,10 @@
 // again from cache instead.  The backward pass reads a row while it works on the one
 // before.
 //
-// Measured: forward 8192 x 5120 fp16 27.6 us, 6.1 TB/s.  Backward 16384 x 1600 bf16 38 us
-// and 4 for the fold, 4.1 TB/s: a wave holds its row twice and its sums, so that two
+// Measured: forward 8192 x 5120 fp16 27.5 us, 6.1 TB/s.  Backward 16384 x 1600 bf16 39 us
+// and 4 for the fold, 4.0 TB/s: a wave holds its row twice and its sums, so that two
 // stand in a SIMD, and the row's sums, two chains of shuffles, are waited for (its vector
-// instructions alone would take 17 us; 4 waves a row instead of one 51).  One row of
+// instructions alone would take 18 us; 4 waves a row instead of one 51).  One row of
 // 1600: 4 us, 8.5 with the call.
 //
 // The weight's and bias's gradients are sums over all rows: each workgroup keeps
