@@ -1,4 +1,4 @@
-"""The operators' consecutive launches.  Work of more than 2^31 work-items (67M rows of up
+"""The operators' consecutive launches.  Work of more than 2^31 work-items (33M rows of up
 to 512 elements, 2M of more than 8192, 8.6e9 elements) goes in consecutive launches;
 __graft_entry__.build() also builds the library with every launch split after 2048
 work-items (zero_dp_sharded_amd/variants/split_launch/libzeroops.so), and the operators'
