@@ -2,6 +2,9 @@
  * zero_ops.h -- C ABI of libzeroops.so: operators of a training step next to the
  * owner's step of zero_shard.h, on one gfx950 GPU:
  *  - layer norm, forward and backward with the weight's and bias's gradients;
+ *  - root-mean-square norm with the residual's addition, forward (into storage or into
+ *    8 bits with scales) and backward;
+ *  - packing to 8 bits with a power of two for every 128 elements, and back;
  *  - softmax cross entropy over a vocabulary, from hidden states and the output
  *    weight, with both gradients under the loss scale and no logits in memory;
  *  - AdamW over the tensors of a model at once, with moments in 32 or in 8 bits.
@@ -76,6 +79,89 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
                                     zero_lp_dtype type, zero_lp_dtype affine, void* dx,
                                     int64_t dx_stride, void* dweight, void* dbias, void* workspace,
                                     int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ root-mean-square norm
+ *
+ * Over the last dimension, with the residual's addition in front of it:
+ *     h = x + residual, rounded to type            (residual NULL: h is x, and the
+ *                                                   argument h NULL)
+ *     rstd = 1 / sqrt(sum(h^2) / width + eps) ;  y = h * rstd * weight
+ * in fp32.  The result is y, rounded to type once; or codes and exps, y in 8 bits as
+ * zero_scaled_pack holds it (rounded once, from fp32); or both.  At least one is given.
+ * Row r of an array begins at element r * its stride; exps has a byte for every 128
+ * elements of a row, ceil(width / 128) in all.  affine is the storage of weight: type or
+ * ZERO_FP32; weight NULL is 1.  rstd (fp32, one a row) may be NULL.  h may be x or residual,
+ * and y may be x (same address and stride).  rows = 0 does nothing.
+ * Errors: INVALID_ARG (as zero_layernorm_forward; codes without exps or the reverse, h without
+ * residual or the reverse, neither y nor codes), UNSUPPORTED (width > 2^24 or rows > 2^31 - 1),
+ * HIP.
+ */
+typedef struct {
+    int64_t rows, width;
+    zero_lp_dtype type, affine;
+    double eps;
+    int64_t x_stride, residual_stride, h_stride, y_stride, codes_stride, exps_stride;
+} zero_rmsnorm_desc;
+
+zero_status zero_rmsnorm_forward(const zero_rmsnorm_desc* desc, const void* x, const void* residual,
+                                 const void* weight, void* h, void* y, float* rstd, uint8_t* codes,
+                                 uint8_t* exps, void* stream);
+
+/* Bytes of workspace zero_rmsnorm_backward needs for these sizes. */
+zero_status zero_rmsnorm_workspace(int64_t rows, int64_t width, int64_t* bytes);
+
+/*
+ * The gradients for dy, with the forward pass's h and rstd, and dh, what has come down to
+ * h by other ways (NULL: nothing):
+ *     xhat = h * rstd ;  g = dy * weight
+ *     dx = rstd * (g - xhat * mean(g * xhat)) + dh ;  dweight = sum over rows of dy * xhat
+ * in fp32, rounded once.  dx is the gradient of x and of residual alike; it may be dh.
+ * dweight may be NULL (then no workspace is needed); it is written, not added to, and
+ * zeros with rows = 0.  workspace is 16-byte aligned.
+ * Errors: as zero_layernorm_backward.
+ */
+typedef struct {
+    int64_t rows, width;
+    zero_lp_dtype type, affine;
+    int64_t dy_stride, h_stride, dh_stride, dx_stride;
+} zero_rmsnorm_grad_desc;
+
+zero_status zero_rmsnorm_backward(const zero_rmsnorm_grad_desc* desc, const void* dy, const void* h,
+                                  const void* weight, const float* rstd, const void* dh, void* dx,
+                                  void* dweight, void* workspace, int64_t workspace_bytes,
+                                  void* stream);
+
+/* ------------------------------------------------------------------ 8 bits with scales
+ *
+ * An element is an e4m3 number (a sign, 4 bits of exponent with bias 7, 3 of mantissa; largest
+ * 448, 0x7f and 0xff NaN, no infinity) times 2^(E - 127), E a byte that 128 elements side by
+ * side in a row have in common (the last block of a row may be shorter), or, square, 128
+ * x 128 elements.  E = 255 is NaN.
+ *
+ * zero_scaled_pack takes x [rows][width] to codes [rows][width] and exps
+ * [rows][ceil(width / 128)] (square: [ceil(rows / 128)][ceil(width / 128)]), to codes_t
+ * [width][rows] and exps_t [width][ceil(rows / 128)] (square: [ceil(width / 128)][ceil(rows /
+ * 128)]) of the transpose, or to both.  E is the least for which the block's largest finite
+ * element is at most 448 * 2^(E - 127), but 27 at least; elements are rounded to the nearest,
+ * ties to even, those that are not finite to NaN (and those above 1.875 * 2^127 to that, so that
+ * none becomes infinite).  Square blocks have the same numbers in
+ * both; others are rounded in each by its own scales.
+ * rows = 0 or width = 0 does nothing.
+ * Errors: INVALID_ARG (NULL x, codes without exps or the reverse, neither codes nor codes_t,
+ * unknown type, sizes < 0, strides too small, square not 0 or 1, misaligned or overlapping
+ * arrays), UNSUPPORTED (rows or width > 2^31 - 1, or more than 2^46 elements), HIP.
+ */
+zero_status zero_scaled_pack(const void* x, int64_t x_stride, int64_t rows, int64_t width,
+                             zero_lp_dtype type, int32_t square, uint8_t* codes,
+                             int64_t codes_stride, uint8_t* exps, int64_t exps_stride,
+                             uint8_t* codes_t, int64_t codes_t_stride, uint8_t* exps_t,
+                             int64_t exps_t_stride, void* stream);
+
+/* What codes and exps stand for, rounded to type (exact in fp32 and bf16 for what
+ * zero_scaled_pack writes).  Errors: as zero_scaled_pack. */
+zero_status zero_scaled_unpack(const uint8_t* codes, int64_t codes_stride, const uint8_t* exps,
+                               int64_t exps_stride, int64_t rows, int64_t width, int32_t square,
+                               zero_lp_dtype type, void* out, int64_t out_stride, void* stream);
 
 /* ------------------------------------------------------------------ vocabulary loss
  *

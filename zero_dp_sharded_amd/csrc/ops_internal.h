@@ -39,6 +39,62 @@ int64_t norm_partial_rows(int64_t rows, int64_t width);
 hipError_t norm_forward(const NormForward& a, int type, int affine, hipStream_t s);
 hipError_t norm_backward(const NormBackward& a, int type, int affine, hipStream_t s);
 
+// ------------------------------------------------------------------ root-mean-square norm
+
+struct RmsForward {
+    const void* x;
+    const void* residual;  // NULL: none, and h is x
+    const void* weight;
+    void* h;
+    void* y;               // NULL: codes alone
+    float* rstd;
+    uint8_t* codes;        // NULL: y alone
+    uint8_t* exps;
+    int64_t rows, width, x_stride, residual_stride, h_stride, y_stride, codes_stride, exps_stride;
+    float eps;
+};
+
+struct RmsBackward {
+    const void* dy;
+    const void* h;
+    const void* weight;
+    const float* rstd;
+    const void* dh;        // NULL: zeros
+    void* dx;
+    void* dweight;
+    float* partial;        // rms_partial_rows() rows of width
+    int64_t rows, width, dy_stride, h_stride, dh_stride, dx_stride;
+};
+
+int64_t rms_partial_rows(int64_t rows);
+hipError_t rms_forward(const RmsForward& a, int type, int affine, hipStream_t s);
+hipError_t rms_backward(const RmsBackward& a, int type, int affine, hipStream_t s);
+
+// ------------------------------------------------------------------ 8 bits with scales
+
+struct ScaledPack {
+    const void* x;
+    uint8_t* codes;        // NULL: the transpose alone
+    uint8_t* exps;
+    uint8_t* codes_t;      // NULL: no transpose
+    uint8_t* exps_t;
+    int64_t rows, width, x_stride, codes_stride, exps_stride, codes_t_stride, exps_t_stride;
+    int64_t tiles;         // along the width (set by the launch)
+    bool square;
+};
+
+struct ScaledUnpack {
+    const uint8_t* codes;
+    const uint8_t* exps;
+    void* out;
+    int64_t rows, width, codes_stride, exps_stride, out_stride;
+    int64_t chunks;        // of 16 along the width (set by the launch)
+    bool square;
+};
+
+hipError_t scaled_pack(const ScaledPack& a, int type, hipStream_t s);
+hipError_t scaled_unpack(const ScaledUnpack& a, int type, hipStream_t s);
+
 // ------------------------------------------------------------------ vocabulary loss
 
 struct TileChoice {            // of the products: 32 ni x 64 nj results a workgroup

@@ -1,0 +1,229 @@
+// Packing to 8 bits with a power of two for every 128 elements (ops_scaled.h), along
+// the rows of an array, along the rows of its transpose, or both from one reading; and back.
+//
+// Bound by memory.  A workgroup takes 128 x 128 elements; a lane has 8 rows of 8
+// columns, so that the largest of 128 elements along a row is one exchange among 16 lanes,
+// along a column one in LDS, and 8 codes side by side are there in either
+// direction.  The transposed codes go through LDS, to be written in runs of 128 bytes.
+
+#include "ops_common.h"
+#include "ops_internal.h"
+#include "ops_scaled.h"
+
+namespace zo {
+namespace {
+
+constexpr int kTile = kScaleBlock;
+constexpr int kRun = kTile + 16;           // bytes between columns of codes in LDS
+
+template <typename T>
+struct Block {                             // 8 x 8 elements as they lie in memory
+    vec_t<T, 8> row[8];
+};
+
+template <typename T>
+__device__ __forceinline__ vec_t<T, 8> load8(const T* p)
+{
+    if constexpr (sizeof(T) == 2) return load_vec<T, 8>(p);
+    else return __builtin_shufflevector(load_vec<T, 4>(p), load_vec<T, 4>(p + 4), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// 8 codes to p, or as many of them as `left` says.
+__device__ __forceinline__ void put8(uint8_t* p, uint2 v, int64_t left)
+{
+    if (left >= 8) {
+        __builtin_memcpy(p, &v, 8);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < left) p[k] = (uint8_t)((k < 4 ? v.x : v.y) >> (8 * (k % 4)));
+}
+
+template <typename T, bool SQUARE>
+__global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t first)
+{
+    __shared__ uint32_t big[16][kTile];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kTile * kRun];
+    const int64_t id = first + blockIdx.x;
+    const int64_t r0 = id / a.tiles * kTile, c0 = id % a.tiles * kTile;
+    const int lane = threadIdx.x & 15, band = threadIdx.x >> 4;       // columns 8 lane .., rows 8 band ..
+    const int64_t c = c0 + lane * 8, r = r0 + band * 8;
+    const T* x = static_cast<const T*>(a.x) + r * a.x_stride + c;
+    Block<T> b;
+    if (c + 8 <= a.width && r + 8 <= a.rows) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) b.row[p] = load8<T>(x + p * a.x_stride);
+    } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                b.row[p][k] = r + p < a.rows && c + k < a.width ? x[p * a.x_stride + k] : static_cast<T>(0.0f);
+    }
+    uint32_t along[8], down[8];            // the largest of the lane's rows, and of its columns
+#pragma unroll
+    for (int k = 0; k < 8; ++k) along[k] = down[k] = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t u = finite_size((float)b.row[p][k]);
+            along[p] = larger(along[p], u);
+            down[k] = larger(down[k], u);
+        }
+    uint32_t E = 0;
+    if constexpr (SQUARE) {
+        uint32_t all = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) all = larger(all, along[p]);
+        all = lanes_max<64>(all);
+        if ((threadIdx.x & 63) == 0) big[0][threadIdx.x >> 6] = all;
+        __syncthreads();
+        E = scale_of(larger(larger(big[0][0], big[0][1]), larger(big[0][2], big[0][3])));
+        if (threadIdx.x == 0) {
+            if (a.codes != nullptr) a.exps[r0 / kTile * a.exps_stride + c0 / kTile] = (uint8_t)E;
+            if (a.codes_t != nullptr) a.exps_t[c0 / kTile * a.exps_t_stride + r0 / kTile] = (uint8_t)E;
+        }
+    }
+    if (a.codes != nullptr) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            uint32_t e = E;
+            if constexpr (!SQUARE) e = scale_of(lanes_max<16>(along[p]));
+            if (r + p >= a.rows) continue;
+            if (!SQUARE && lane == 0) a.exps[(r + p) * a.exps_stride + c0 / kTile] = (uint8_t)e;
+            if (c >= a.width) continue;
+            const float inverse = inverse_scale(e);
+            const vec_t<T, 8>& v = b.row[p];
+            const uint2 out = make_uint2(codes_of((float)v[0], (float)v[1], (float)v[2], (float)v[3], inverse),
+                                         codes_of((float)v[4], (float)v[5], (float)v[6], (float)v[7], inverse));
+            put8(a.codes + (r + p) * a.codes_stride + c, out, a.width - c);
+        }
+    }
+    if (a.codes_t == nullptr) return;
+    if constexpr (!SQUARE) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) big[band][lane * 8 + k] = down[k];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        uint32_t e = E;
+        if constexpr (!SQUARE) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) m = larger(m, big[q][lane * 8 + k]);
+            e = scale_of(m);
+            if (band == 0 && c + k < a.width) a.exps_t[(c + k) * a.exps_t_stride + r0 / kTile] = (uint8_t)e;
+        }
+        const float inverse = inverse_scale(e);
+        const uint2 out = make_uint2(
+            codes_of((float)b.row[0][k], (float)b.row[1][k], (float)b.row[2][k], (float)b.row[3][k], inverse),
+            codes_of((float)b.row[4][k], (float)b.row[5][k], (float)b.row[6][k], (float)b.row[7][k], inverse));
+        *reinterpret_cast<uint2*>(turned + (lane * 8 + k) * kRun + band * 8) = out;
+    }
+    __syncthreads();
+    // 8 lanes a column, 16 codes each
+    const int64_t at = r0 + (threadIdx.x & 7) * 16;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int column = q * 32 + (threadIdx.x >> 3);
+        if (c0 + column >= a.width || at >= a.rows) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(turned + column * kRun + (threadIdx.x & 7) * 16);
+        uint8_t* to = a.codes_t + (c0 + column) * a.codes_t_stride + at;
+        if (at + 16 <= a.rows) {
+            __builtin_memcpy(to, &v, 16);
+        } else {
+            put8(to, make_uint2(v.x, v.y), a.rows - at);
+            put8(to + 8, make_uint2(v.z, v.w), a.rows - at - 8);
+        }
+    }
+}
+
+// What codes stand for: a lane 16 of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void scaled_unpack_kernel(ScaledUnpack a, int64_t first)
+{
+    const int64_t id = (first + blockIdx.x) * 256 + threadIdx.x;
+    if (id >= a.rows * a.chunks) return;
+    // (32 bits where they do: a 64-bit division is a hundred instructions)
+    int64_t row, chunk;
+    if (a.rows * a.chunks <= UINT32_MAX) {
+        row = (uint32_t)id / (uint32_t)a.chunks;
+        chunk = (uint32_t)id - (uint32_t)row * (uint32_t)a.chunks;
+    } else {
+        row = id / a.chunks;
+        chunk = id - row * a.chunks;
+    }
+    const int64_t c = chunk * 16;
+    const uint8_t* from = a.codes + row * a.codes_stride + c;
+    T* to = static_cast<T*>(a.out) + row * a.out_stride + c;
+    const float scale = scale_value(a.exps[(a.square ? row / kTile : row) * a.exps_stride + c / kTile]);
+    uint32_t v[4] = {0, 0, 0, 0};
+    const bool whole = c + 16 <= a.width;
+    if (whole) {
+        __builtin_memcpy(v, from, 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (c + k < a.width) v[k / 4] |= (uint32_t)from[k] << (8 * (k % 4));
+    }
+    float y[16];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        y[4 * q + 0] = __builtin_amdgcn_cvt_f32_fp8((int)v[q], 0) * scale;
+        y[4 * q + 1] = __builtin_amdgcn_cvt_f32_fp8((int)v[q], 1) * scale;
+        y[4 * q + 2] = __builtin_amdgcn_cvt_f32_fp8((int)v[q], 2) * scale;
+        y[4 * q + 3] = __builtin_amdgcn_cvt_f32_fp8((int)v[q], 3) * scale;
+    }
+    constexpr int W = Vec<T>::W;
+#pragma unroll
+    for (int q = 0; q < 16 / W; ++q) {
+        vec_t<T, W> o;
+#pragma unroll
+        for (int k = 0; k < W; ++k) o[k] = static_cast<T>(y[q * W + k]);
+        if (whole) {
+            store_vec<T, W>(to + q * W, o);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+                if (c + q * W + k < a.width) to[q * W + k] = o[k];
+        }
+    }
+}
+
+template <typename T>
+hipError_t pack(ScaledPack a, hipStream_t s)
+{
+    a.tiles = ceil_div(a.width, kTile);
+    in_launches(ceil_div(a.rows, kTile) * a.tiles, 256, [&](int64_t first, int64_t count) {
+        if (a.square) scaled_pack_kernel<T, true><<<dim3((unsigned)count), 256, 0, s>>>(a, first);
+        else scaled_pack_kernel<T, false><<<dim3((unsigned)count), 256, 0, s>>>(a, first);
+    });
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t unpack(ScaledUnpack a, hipStream_t s)
+{
+    a.chunks = ceil_div(a.width, 16);
+    in_launches(ceil_div(a.rows * a.chunks, 256), 256, [&](int64_t first, int64_t count) {
+        scaled_unpack_kernel<T><<<dim3((unsigned)count), 256, 0, s>>>(a, first);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t scaled_pack(const ScaledPack& a, int type, hipStream_t s)
+{
+    return type == 1 ? pack<_Float16>(a, s) : type == 2 ? pack<__bf16>(a, s) : pack<float>(a, s);
+}
+
+hipError_t scaled_unpack(const ScaledUnpack& a, int type, hipStream_t s)
+{
+    return type == 1 ? unpack<_Float16>(a, s) : type == 2 ? unpack<__bf16>(a, s) : unpack<float>(a, s);
+}
+
+}  // namespace zo

@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <unordered_set>
@@ -131,9 +132,13 @@ zero_status on_device(const Array& a, int dev, const char* who)
     return ZERO_OK;
 }
 
+struct Pair {
+    int a, b;                 // a < b
+};
+
 // Host checks of a call's arrays: alignment, and that a written one overlaps no
-// other (`same`: the one pair that may be the same array).
-zero_status check_arrays(const Array* a, int n, const char* who, int same_a = -1, int same_b = -1)
+// other (`same`: pairs that may be the same array).
+zero_status check_arrays(const Array* a, int n, const char* who, std::initializer_list<Pair> same = {})
 {
     for (int i = 0; i < n; ++i) {
         if (empty(a[i])) continue;
@@ -141,7 +146,8 @@ zero_status check_arrays(const Array* a, int n, const char* who, int same_a = -1
             return fail(ZERO_ERR_INVALID_ARG, "%s: %s is not aligned to %zu bytes", who, a[i].name, a[i].align);
         for (int j = 0; j < i; ++j) {
             if (empty(a[j]) || !(a[i].written || a[j].written)) continue;
-            if (i == same_b && j == same_a && a[i].p == a[j].p && (a[i].step == a[j].step || a[i].rows == 1)) continue;
+            const bool may = std::any_of(same.begin(), same.end(), [&](const Pair& s) { return s.a == j && s.b == i; });
+            if (may && a[i].p == a[j].p && (a[i].step == a[j].step || a[i].rows == 1)) continue;
             if (overlap(a[i], a[j]))
                 return fail(ZERO_ERR_INVALID_ARG, "%s: %s overlaps %s", who, a[i].name, a[j].name);
         }
@@ -196,6 +202,35 @@ zero_status check_stride(int64_t stride, int64_t rows, int64_t width, const char
 }
 
 int64_t norm_workspace(int64_t rows, int64_t width) { return zo::norm_partial_rows(rows, width) * 2 * width * 4; }
+
+// ------------------------------------------------------------------ 8 bits with scales
+
+int64_t scale_blocks(int64_t n) { return (n + 127) / 128; }
+
+// The exponents of [rows][width] codes.
+Array exponents(const char* name, const void* p, int64_t rows, int64_t width, int64_t stride, bool square, bool written)
+{
+    return table(name, p, square ? scale_blocks(rows) : rows, scale_blocks(width), stride, 1, written);
+}
+
+constexpr int64_t kMaxScaled = (int64_t)1 << 46;       // elements
+
+zero_status check_scaled(int64_t rows, int64_t width, int32_t square, const char* who)
+{
+    if (rows < 0 || width < 0) return fail(ZERO_ERR_INVALID_ARG, "%s: rows and width must be >= 0", who);
+    if (square != 0 && square != 1) return fail(ZERO_ERR_INVALID_ARG, "%s: square must be 0 or 1", who);
+    if (rows > kMaxGrid || width > kMaxGrid || (width > 0 && rows > kMaxScaled / width))
+        return fail(ZERO_ERR_UNSUPPORTED, "%s: rows or width above 2^31 - 1, or more than 2^46 elements", who);
+    return ZERO_OK;
+}
+
+// Strides of codes and their exponents.
+zero_status check_scaled_strides(int64_t stride, int64_t exps_stride, int64_t rows, int64_t width, bool square, const char* name,
+                                 const char* exps_name, const char* who)
+{
+    if (const zero_status s = check_stride(stride, rows, width, name, who)) return s;
+    return check_stride(exps_stride, square ? scale_blocks(rows) : rows, scale_blocks(width), exps_name, who);
+}
 
 // ------------------------------------------------------------------ AdamW
 
@@ -369,7 +404,7 @@ zero_status zero_layernorm_forward(const void* x, int64_t x_stride, const void* 
     const Array a[] = {table("x", x, rows, width, x_stride, e, false), table("y", y, rows, width, y_stride, e, true),
                        flat("weight", weight, (size_t)width * ae, ae, false), flat("bias", bias, (size_t)width * ae, ae, false),
                        flat("mean", mean, (size_t)rows * 4, 4, true), flat("rstd", rstd, (size_t)rows * 4, 4, true)};
-    if (const zero_status s = check_arrays(a, 6, who, 0, 1)) return s;
+    if (const zero_status s = check_arrays(a, 6, who, {{0, 1}})) return s;
     if (const zero_status s = check_place(a, 6, stream, who)) return s;
     const zo::NormForward f{x, weight, bias, y, mean, rstd, rows, width, x_stride, y_stride, (float)eps};
     const hipError_t err = zo::norm_forward(f, t, at, static_cast<hipStream_t>(stream));
@@ -415,6 +450,140 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
     const zo::NormBackward b{dy, x, weight, mean, rstd, dx, dweight, dbias, sums ? static_cast<float*>(workspace) : nullptr,
                              rows, width, dy_stride, x_stride, dx_stride};
     const hipError_t err = zo::norm_backward(b, t, at, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
+zero_status zero_rmsnorm_forward(const zero_rmsnorm_desc* d, const void* x, const void* residual, const void* weight, void* h,
+                                 void* y, float* rstd, uint8_t* codes, uint8_t* exps, void* stream)
+{
+    const char* who = "zero_rmsnorm_forward";
+    if (!d) return fail(ZERO_ERR_INVALID_ARG, "%s: desc is NULL", who);
+    const int32_t t = enum_value(d->type), at = enum_value(d->affine);
+    const int64_t rows = d->rows, width = d->width;
+    if (const zero_status s = check_norm(rows, width, t, at, who)) return s;
+    if (!(std::isfinite((float)d->eps) && d->eps >= 0.0)) return fail(ZERO_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
+    if (rows == 0) return ZERO_OK;
+    if (!x) return fail(ZERO_ERR_INVALID_ARG, "%s: x is NULL", who);
+    if ((residual != nullptr) != (h != nullptr)) return fail(ZERO_ERR_INVALID_ARG, "%s: residual and h are given both or neither (NULL)", who);
+    if ((codes != nullptr) != (exps != nullptr)) return fail(ZERO_ERR_INVALID_ARG, "%s: codes and exps are given both or neither (NULL)", who);
+    if (!y && !codes) return fail(ZERO_ERR_INVALID_ARG, "%s: y and codes are both NULL", who);
+    if (const zero_status s = check_stride(d->x_stride, rows, width, "x", who)) return s;
+    if (residual) {
+        if (const zero_status s = check_stride(d->residual_stride, rows, width, "residual", who)) return s;
+        if (const zero_status s = check_stride(d->h_stride, rows, width, "h", who)) return s;
+    }
+    if (y)
+        if (const zero_status s = check_stride(d->y_stride, rows, width, "y", who)) return s;
+    if (codes)
+        if (const zero_status s = check_scaled_strides(d->codes_stride, d->exps_stride, rows, width, false, "codes", "exps", who)) return s;
+    const int e = type_bytes(t), ae = type_bytes(at);
+    const Array a[] = {table("x", x, rows, width, d->x_stride, e, false), table("residual", residual, rows, width, d->residual_stride, e, false),
+                       table("h", h, rows, width, d->h_stride, e, true), table("y", y, rows, width, d->y_stride, e, true),
+                       flat("weight", weight, (size_t)width * ae, ae, false), flat("rstd", rstd, (size_t)rows * 4, 4, true),
+                       table("codes", codes, rows, width, d->codes_stride, 1, true), exponents("exps", exps, rows, width, d->exps_stride, false, true)};
+    if (const zero_status s = check_arrays(a, 8, who, {{0, 2}, {1, 2}, {0, 3}})) return s;
+    if (const zero_status s = check_place(a, 8, stream, who)) return s;
+    const zo::RmsForward f{x, residual, weight, h, y, rstd, codes, exps, rows, width, d->x_stride, d->residual_stride, d->h_stride,
+                           d->y_stride, d->codes_stride, d->exps_stride, (float)d->eps};
+    const hipError_t err = zo::rms_forward(f, t, at, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
+static int64_t rms_workspace(int64_t rows, int64_t width) { return zo::rms_partial_rows(rows) * width * 4; }
+
+zero_status zero_rmsnorm_workspace(int64_t rows, int64_t width, int64_t* bytes)
+{
+    const char* who = "zero_rmsnorm_workspace";
+    if (!bytes) return fail(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+    if (const zero_status s = check_norm(rows, width, ZERO_FP32, ZERO_FP32, who)) return s;
+    *bytes = rms_workspace(rows, width);
+    return ZERO_OK;
+}
+
+zero_status zero_rmsnorm_backward(const zero_rmsnorm_grad_desc* d, const void* dy, const void* h, const void* weight, const float* rstd,
+                                  const void* dh, void* dx, void* dweight, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    const char* who = "zero_rmsnorm_backward";
+    if (!d) return fail(ZERO_ERR_INVALID_ARG, "%s: desc is NULL", who);
+    const int32_t t = enum_value(d->type), at = enum_value(d->affine);
+    const int64_t rows = d->rows, width = d->width;
+    if (const zero_status s = check_norm(rows, width, t, at, who)) return s;
+    if (rows > 0) {
+        if (!dy || !h || !rstd || !dx) return fail(ZERO_ERR_INVALID_ARG, "%s: dy, h, rstd or dx is NULL", who);
+        if (const zero_status s = check_stride(d->dy_stride, rows, width, "dy", who)) return s;
+        if (const zero_status s = check_stride(d->h_stride, rows, width, "h", who)) return s;
+        if (const zero_status s = check_stride(d->dx_stride, rows, width, "dx", who)) return s;
+        if (dh)
+            if (const zero_status s = check_stride(d->dh_stride, rows, width, "dh", who)) return s;
+    } else if (!dweight) {
+        return ZERO_OK;
+    }
+    const int64_t need = rms_workspace(rows, width);
+    if (dweight && (!workspace || workspace_bytes < need))
+        return fail(ZERO_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %lld are needed", who,
+                    (long long)(workspace ? workspace_bytes : 0), (long long)need);
+    const int e = type_bytes(t), ae = type_bytes(at);
+    const Array a[] = {table("dy", dy, rows, width, d->dy_stride, e, false), table("h", h, rows, width, d->h_stride, e, false),
+                       table("dh", dh, rows, width, d->dh_stride, e, false), table("dx", dx, rows, width, d->dx_stride, e, true),
+                       flat("weight", weight, (size_t)width * ae, ae, false), flat("rstd", rstd, (size_t)rows * 4, 4, false),
+                       flat("dweight", dweight, (size_t)width * ae, ae, true),
+                       flat("workspace", dweight ? workspace : nullptr, (size_t)need, 16, true)};
+    if (const zero_status s = check_arrays(a, 8, who, {{2, 3}})) return s;
+    if (const zero_status s = check_place(a, 8, stream, who)) return s;
+    const zo::RmsBackward b{dy, h, weight, rstd, dh, dx, dweight, dweight ? static_cast<float*>(workspace) : nullptr, rows, width,
+                            d->dy_stride, d->h_stride, d->dh_stride, d->dx_stride};
+    const hipError_t err = zo::rms_backward(b, t, at, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
+zero_status zero_scaled_pack(const void* x, int64_t x_stride, int64_t rows, int64_t width, zero_lp_dtype type, int32_t square,
+                             uint8_t* codes, int64_t codes_stride, uint8_t* exps, int64_t exps_stride, uint8_t* codes_t,
+                             int64_t codes_t_stride, uint8_t* exps_t, int64_t exps_t_stride, void* stream)
+{
+    const char* who = "zero_scaled_pack";
+    const int32_t t = enum_value(type);
+    if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
+    if (const zero_status s = check_scaled(rows, width, square, who)) return s;
+    if (rows == 0 || width == 0) return ZERO_OK;
+    if (!x) return fail(ZERO_ERR_INVALID_ARG, "%s: x is NULL", who);
+    if ((codes != nullptr) != (exps != nullptr) || (codes_t != nullptr) != (exps_t != nullptr))
+        return fail(ZERO_ERR_INVALID_ARG, "%s: codes and exps are given both or neither (NULL)", who);
+    if (!codes && !codes_t) return fail(ZERO_ERR_INVALID_ARG, "%s: codes and codes_t are both NULL", who);
+    if (const zero_status s = check_stride(x_stride, rows, width, "x", who)) return s;
+    if (codes)
+        if (const zero_status s = check_scaled_strides(codes_stride, exps_stride, rows, width, square, "codes", "exps", who)) return s;
+    if (codes_t)
+        if (const zero_status s = check_scaled_strides(codes_t_stride, exps_t_stride, width, rows, square, "codes_t", "exps_t", who)) return s;
+    const int e = type_bytes(t);
+    const Array a[] = {table("x", x, rows, width, x_stride, e, false), table("codes", codes, rows, width, codes_stride, 1, true),
+                       exponents("exps", exps, rows, width, exps_stride, square, true),
+                       table("codes_t", codes_t, width, rows, codes_t_stride, 1, true),
+                       exponents("exps_t", exps_t, width, rows, exps_t_stride, square, true)};
+    if (const zero_status s = check_arrays(a, 5, who)) return s;
+    if (const zero_status s = check_place(a, 5, stream, who)) return s;
+    const zo::ScaledPack p{x, codes, exps, codes_t, exps_t, rows, width, x_stride, codes_stride, exps_stride, codes_t_stride,
+                           exps_t_stride, 0, square != 0};
+    const hipError_t err = zo::scaled_pack(p, t, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
+zero_status zero_scaled_unpack(const uint8_t* codes, int64_t codes_stride, const uint8_t* exps, int64_t exps_stride, int64_t rows,
+                               int64_t width, int32_t square, zero_lp_dtype type, void* out, int64_t out_stride, void* stream)
+{
+    const char* who = "zero_scaled_unpack";
+    const int32_t t = enum_value(type);
+    if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
+    if (const zero_status s = check_scaled(rows, width, square, who)) return s;
+    if (rows == 0 || width == 0) return ZERO_OK;
+    if (!codes || !exps || !out) return fail(ZERO_ERR_INVALID_ARG, "%s: codes, exps or out is NULL", who);
+    if (const zero_status s = check_scaled_strides(codes_stride, exps_stride, rows, width, square, "codes", "exps", who)) return s;
+    if (const zero_status s = check_stride(out_stride, rows, width, "out", who)) return s;
+    const Array a[] = {table("codes", codes, rows, width, codes_stride, 1, false), exponents("exps", exps, rows, width, exps_stride, square, false),
+                       table("out", out, rows, width, out_stride, type_bytes(t), true)};
+    if (const zero_status s = check_arrays(a, 3, who)) return s;
+    if (const zero_status s = check_place(a, 3, stream, who)) return s;
+    const zo::ScaledUnpack u{codes, exps, out, rows, width, codes_stride, exps_stride, out_stride, 0, square != 0};
+    const hipError_t err = zo::scaled_unpack(u, t, static_cast<hipStream_t>(stream));
     return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
 }
 

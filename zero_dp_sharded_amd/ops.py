@@ -1,6 +1,6 @@
-"""The training operators of libzeroops.so (include/zero_ops.h): layer norm, the
-softmax cross entropy over a vocabulary with its gradients, and AdamW over many
-tensors with moments in 32 or 8 bits.
+"""The training operators of libzeroops.so (include/zero_ops.h): layer norm, RMS norm with
+the residual's addition, packing to 8 bits with scales, the softmax cross entropy over a
+vocabulary with its gradients, and AdamW over many tensors with moments in 32 or 8 bits.
 
 A thin ctypes binding, as the package's binding of libzeroshard.so is: functions
 carry the C names, tensors become device pointers, strides and types, and the
@@ -26,13 +26,26 @@ _ptr = ctypes.POINTER
 
 OPS_SYMBOLS = (
     "zero_layernorm_forward", "zero_layernorm_workspace", "zero_layernorm_backward",
-    "zero_vocab_loss_workspace", "zero_vocab_loss", "zero_adamw_init", "zero_adamw_set_grads",
+    "zero_rmsnorm_forward", "zero_rmsnorm_workspace", "zero_rmsnorm_backward", "zero_scaled_pack",
+    "zero_scaled_unpack", "zero_vocab_loss_workspace", "zero_vocab_loss", "zero_adamw_init", "zero_adamw_set_grads",
     "zero_adamw_step", "zero_adamw_result", "zero_adamw_get_counters", "zero_adamw_set_counters",
     "zero_adamw_destroy", "zero_moments_pack", "zero_moments_unpack", "zero_ops_last_error",
     "zero_ops_abi_version",
 )
 
 BLOCK = 256            # elements that share one exponent of 8-bit moments
+SCALE_BLOCK = 128      # elements that share one scale of packed arrays
+
+
+class ZeroRmsnormDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("width", _i64), ("type", ctypes.c_int), ("affine", ctypes.c_int),
+                ("eps", _f64), ("x_stride", _i64), ("residual_stride", _i64), ("h_stride", _i64),
+                ("y_stride", _i64), ("codes_stride", _i64), ("exps_stride", _i64)]
+
+
+class ZeroRmsnormGradDesc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("width", _i64), ("type", ctypes.c_int), ("affine", ctypes.c_int),
+                ("dy_stride", _i64), ("h_stride", _i64), ("dh_stride", _i64), ("dx_stride", _i64)]
 
 
 class ZeroVocabLossDesc(ctypes.Structure):
@@ -70,6 +83,15 @@ def lib() -> ctypes.CDLL:
         L.zero_layernorm_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64,
                                               ctypes.c_int, ctypes.c_int, _vp, _i64, _vp, _vp, _vp,
                                               _i64, _vp]
+        L.zero_rmsnorm_forward.argtypes = [_ptr(ZeroRmsnormDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                           _vp, _vp]
+        L.zero_rmsnorm_workspace.argtypes = [_i64, _i64, _ptr(_i64)]
+        L.zero_rmsnorm_backward.argtypes = [_ptr(ZeroRmsnormGradDesc), _vp, _vp, _vp, _vp, _vp, _vp,
+                                            _vp, _vp, _i64, _vp]
+        L.zero_scaled_pack.argtypes = [_vp, _i64, _i64, _i64, ctypes.c_int, _i32, _vp, _i64, _vp, _i64,
+                                       _vp, _i64, _vp, _i64, _vp]
+        L.zero_scaled_unpack.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _i32, ctypes.c_int, _vp, _i64,
+                                         _vp]
         L.zero_vocab_loss_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, _ptr(_i64)]
         L.zero_vocab_loss.argtypes = [_ptr(ZeroVocabLossDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _i64, _vp]
@@ -232,6 +254,121 @@ def zero_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=N
         _flat("mean", mean, torch.float32, rows), _flat("rstd", rstd, torch.float32, rows), rows,
         width, t, at, dxp, dxs, _flat("dweight", dweight, adt, width),
         _flat("dbias", dbias, adt, width), wp, wn, _current(stream)), "zero_layernorm_backward")
+
+
+# ------------------------------------------------------------------ root-mean-square norm
+
+def zero_rmsnorm_forward(x, residual, weight, h, y, rstd=None, codes=None, exps=None, *, eps: float = 1e-6,
+                         stream=None) -> None:
+    """h = x + residual and y = h * rstd * weight over the last of x's two dimensions;
+    rstd (fp32, one a row) for the backward pass.  residual and h may both be None (h is x),
+    weight may be None (of x's type or fp32), and y where codes (float8_e4m3fn, x's shape) and
+    exps (uint8, [rows, ceil(width / 128)]) are given: the result as zero_scaled_pack holds it."""
+    torch or _load()
+    rows, width = _matrix("x", x)
+    t = _type_of("x", x)
+    d = ZeroRmsnormDesc(rows=rows, width=width, type=t, affine=t if weight is None else _type_of("weight", weight),
+                        eps=eps)
+    xp, d.x_stride = _rows("x", x, x.dtype, rows, width)
+    rp = hp = yp = cp = ep = None
+    if residual is not None:
+        rp, d.residual_stride = _rows("residual", residual, x.dtype, rows, width)
+    if h is not None:
+        hp, d.h_stride = _rows("h", h, x.dtype, rows, width)
+    if y is not None:
+        yp, d.y_stride = _rows("y", y, x.dtype, rows, width)
+    if codes is not None:
+        cp, d.codes_stride = _rows("codes", codes, torch.float8_e4m3fn, rows, width)
+    if exps is not None:
+        ep, d.exps_stride = _rows("exps", exps, torch.uint8, rows, -(-width // SCALE_BLOCK))
+    _check(lib().zero_rmsnorm_forward(
+        ctypes.byref(d), xp, rp, _flat("weight", weight, None, width), hp, yp,
+        _flat("rstd", rstd, torch.float32, rows), cp, ep, _current(stream)), "zero_rmsnorm_forward")
+
+
+def zero_rmsnorm_workspace(rows: int, width: int) -> int:
+    """Bytes of workspace for zero_rmsnorm_backward."""
+    n = _i64()
+    _check(lib().zero_rmsnorm_workspace(rows, width, ctypes.byref(n)), "zero_rmsnorm_workspace")
+    return n.value
+
+
+def zero_rmsnorm_backward(dy, h, weight, rstd, dx, dh=None, dweight=None, workspace=None, *,
+                          stream=None) -> None:
+    """dx (of x and of the residual alike) and, where given, dweight, for dy, the forward
+    pass's h and rstd, and dh, the gradient that h has by other ways (None: none; dx may be
+    dh).  workspace: uint8, zero_rmsnorm_workspace(rows, width) bytes, needed with dweight."""
+    torch or _load()
+    rows, width = _matrix("h", h)
+    t = _type_of("h", h)
+    given = weight if weight is not None else dweight
+    adt = None if given is None else given.dtype
+    d = ZeroRmsnormGradDesc(rows=rows, width=width, type=t, affine=t if given is None else _type_of("weight", given))
+    hp, d.h_stride = _rows("h", h, h.dtype, rows, width)
+    dyp, d.dy_stride = _rows("dy", dy, h.dtype, rows, width)
+    dxp, d.dx_stride = _rows("dx", dx, h.dtype, rows, width)
+    dhp = None
+    if dh is not None:
+        dhp, d.dh_stride = _rows("dh", dh, h.dtype, rows, width)
+    sp, sn = _space(workspace)
+    _check(lib().zero_rmsnorm_backward(
+        ctypes.byref(d), dyp, hp, _flat("weight", weight, adt, width), _flat("rstd", rstd, torch.float32, rows),
+        dhp, dxp, _flat("dweight", dweight, adt, width), sp, sn, _current(stream)), "zero_rmsnorm_backward")
+
+
+# ------------------------------------------------------------------ 8 bits with scales
+
+def _exps(name: str, t, rows: int, width: int) -> tuple:
+    """(address, row stride, square) of the exponents of [rows, width] codes; square is None
+    where both forms are the same."""
+    _tensor(name, t, torch.uint8)
+    blocks, down = -(-width // SCALE_BLOCK), -(-rows // SCALE_BLOCK)
+    if t.dim() == 2 and t.shape == (rows, blocks):
+        square = None if rows == down else False
+    elif t.dim() == 2 and t.shape == (down, blocks):
+        square = True
+    else:
+        raise ValueError(f"{name}: expected shape ({rows}, {blocks}) or ({down}, {blocks}), got {tuple(t.shape)}")
+    p, stride = _rows(name, t, torch.uint8, t.shape[0], blocks)
+    return p, stride, square
+
+
+def zero_scaled_pack(x, codes=None, exps=None, codes_t=None, exps_t=None, *, stream=None) -> None:
+    """x [rows, width] in 8 bits: codes (float8_e4m3fn, [rows, width]) and exps (uint8), of the
+    transpose codes_t [width, rows] and exps_t, or both.  exps is [rows, ceil(width / 128)] for
+    a scale for every 128 elements of a row, or [ceil(rows / 128), ceil(width / 128)] for
+    one for every 128 x 128; exps_t likewise."""
+    torch or _load()
+    rows, width = _matrix("x", x)
+    xp, xs = _rows("x", x, x.dtype, rows, width)
+    cp = ep = ctp = etp = None
+    cs = es = cts = ets = 0
+    forms = set()
+    if codes is not None:
+        cp, cs = _rows("codes", codes, torch.float8_e4m3fn, rows, width)
+    if exps is not None:
+        ep, es, form = _exps("exps", exps, rows, width)
+        forms.add(form)
+    if codes_t is not None:
+        ctp, cts = _rows("codes_t", codes_t, torch.float8_e4m3fn, width, rows)
+    if exps_t is not None:
+        etp, ets, form = _exps("exps_t", exps_t, width, rows)
+        forms.add(form)
+    if forms >= {True, False}:
+        raise ValueError("exps and exps_t: one is of squares and the other of rows")
+    _check(lib().zero_scaled_pack(xp, xs, rows, width, _type_of("x", x), int(True in forms), cp, cs, ep, es, ctp,
+                                  cts, etp, ets, _current(stream)), "zero_scaled_pack")
+
+
+def zero_scaled_unpack(codes, exps, out, *, stream=None) -> None:
+    """What codes and exps (as zero_scaled_pack's, either form) stand for, into out."""
+    torch or _load()
+    rows, width = _matrix("codes", codes)
+    cp, cs = _rows("codes", codes, torch.float8_e4m3fn, rows, width)
+    ep, es, square = _exps("exps", exps, rows, width)
+    op, os_ = _rows("out", out, None, rows, width)
+    _check(lib().zero_scaled_unpack(cp, cs, ep, es, rows, width, int(bool(square)), _type_of("out", out), op, os_,
+                                    _current(stream)), "zero_scaled_unpack")
 
 
 # ------------------------------------------------------------------ vocabulary loss
