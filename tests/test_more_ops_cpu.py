@@ -121,3 +121,43 @@ def test_scaled_unsupported_and_empty():
         assert call(rows=0)[0] == zs.ZERO_OK and call(width=0)[0] == zs.ZERO_OK
     # the exponents of squares are fewer
     assert "overlaps" not in pack(square=1, et=at(2, 599))[1]
+
+
+# ------------------------------------------------------------------ the product
+
+def product(a=at(0), ae=at(1), b=at(2), be=at(3), bias=at(4), out=at(5), ws=at(6), wn=1 << 29, desc=True, **d):
+    f = dict(m=100, n=200, k=300, type=3, b_square=0, a_stride=300, a_exps_stride=3, b_stride=300, b_exps_stride=3, out_stride=200)
+    f.update(d)
+    c = ops.ZeroScaledProductDesc(**f)
+    return error(ops.lib().zero_scaled_product, ctypes.byref(c) if desc else None, a, ae, b, be, bias, out, ws, wn, None)
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(desc=False), "NULL"), (dict(a=None), "NULL"), (dict(ae=None), "NULL"), (dict(b=None), "NULL"), (dict(be=None), "NULL"),
+    (dict(out=None), "NULL"), (dict(type=0), "unknown type"), (dict(b_square=2), "b_square"), (dict(m=-1), "m, n and k"),
+    (dict(n=-1), "m, n and k"), (dict(k=-1), "m, n and k"), (dict(a_stride=299), "stride"), (dict(b_stride=1), "stride"),
+    (dict(a_exps_stride=2), "stride"), (dict(b_exps_stride=2), "stride"), (dict(out_stride=199), "stride"), (dict(ws=None), "workspace"),
+    (dict(wn=100), "workspace"), (dict(ws=at(6, 128)), "aligned"), (dict(out=at(5, 2)), "aligned"), (dict(bias=at(4, 1)), "aligned"),
+    (dict(out=at(0)), "overlaps"), (dict(out=at(3)), "overlaps"), (dict(ws=at(2)), "overlaps"), (dict(out=at(4)), "overlaps"),
+])
+def test_product_refuses(kw, word):
+    s, msg = product(**kw)
+    assert s == zs.ZERO_ERR_INVALID_ARG and word in msg, (s, msg)
+
+
+def test_product_unsupported_and_empty():
+    assert ctypes.sizeof(ops.ZeroScaledProductDesc) == 72
+    for kw in (dict(m=1 << 31), dict(n=1 << 31), dict(m=1 << 25, n=1 << 20), dict(k=(1 << 22) + 1), dict(a_exps_stride=(1 << 22) + 1)):
+        assert product(**kw)[0] == zs.ZERO_ERR_UNSUPPORTED, kw
+    assert product(m=0, a=None, out=None)[0] == zs.ZERO_OK and product(n=0, b=None, out=None)[0] == zs.ZERO_OK
+    # operands may be one array
+    assert "overlaps" not in product(b=at(0), be=at(1))[1]
+    for bad in ((-1, 1, 1), (1 << 31, 1, 1), (1, 1, (1 << 22) + 1)):
+        with pytest.raises(zs.ZeroError):
+            zs.zero_scaled_product_workspace(*bad)
+    assert zs.zero_scaled_product_workspace(1, 6400, 1600) == 256
+    import torch
+    sizes = [zs.zero_scaled_product_workspace(500, 700, 900, t) for t in (torch.float16, torch.bfloat16, torch.float32)]
+    assert sizes[0] == sizes[1] and zs.zero_scaled_product_workspace(500, 700, 900) == max(sizes)
+    with pytest.raises(TypeError):
+        zs.zero_scaled_product_workspace(1, 1, 1, torch.int8)

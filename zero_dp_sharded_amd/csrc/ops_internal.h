@@ -88,12 +88,38 @@ struct ScaledUnpack {
     const uint8_t* exps;
     void* out;
     int64_t rows, width, codes_stride, exps_stride, out_stride;
-    int64_t chunks;        // of 16 along the width (set by the launch)
+    int64_t fill;          // columns written, those past the width as zeros (0: the width)
+    int64_t chunks;        // of 16 along them (set by the launch)
     bool square;
 };
 
 hipError_t scaled_pack(const ScaledPack& a, int type, hipStream_t s);
 hipError_t scaled_unpack(const ScaledUnpack& a, int type, hipStream_t s);
+
+struct ProductPlan {           // what a product's sizes settle
+    int64_t m, n, k;
+    int64_t k_ld;              // the depth in whole chunks of 16
+    bool exact;                // by bf16 products (fp32 results)
+    int ni;                    // tiles of 32 ni x 256; 0: few rows, no tiles
+    int splits;                // parts of the depth (few rows: waves that share it)
+    int64_t off_part, off_a, off_b;        // byte offsets into the workspace
+    int64_t bytes;
+};
+
+struct ScaledProduct {
+    const uint8_t* a;
+    const uint8_t* a_exps;
+    const uint8_t* b;
+    const uint8_t* b_exps;
+    const void* bias;
+    void* out;
+    char* space;
+    int64_t a_stride, a_exps_stride, b_stride, b_exps_stride, out_stride;
+    bool square;               // b's scales
+};
+
+ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type);
+hipError_t scaled_product(const ScaledProduct& a, const ProductPlan& p, int type, hipStream_t s);
 
 // ------------------------------------------------------------------ vocabulary loss
 

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t 
     }
 }
 
-// What codes stand for: a lane 16 of a row.
+// What codes stand for, and zeros behind the width up to `fill`: a lane 16 of a row.
 template <typename T>
 __global__ __launch_bounds__(256) void scaled_unpack_kernel(ScaledUnpack a, int64_t first)
 {
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void scaled_unpack_kernel(ScaledUnpack a, int6
     const int64_t c = chunk * 16;
     const uint8_t* from = a.codes + row * a.codes_stride + c;
     T* to = static_cast<T*>(a.out) + row * a.out_stride + c;
-    const float scale = scale_value(a.exps[(a.square ? row / kTile : row) * a.exps_stride + c / kTile]);
+    const float scale = c < a.width ? scale_value(a.exps[(a.square ? row / kTile : row) * a.exps_stride + c / kTile]) : 0.0f;
     uint32_t v[4] = {0, 0, 0, 0};
     const bool whole = c + 16 <= a.width;
     if (whole) {
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(256) void scaled_unpack_kernel(ScaledUnpack a, int6
         } else {
 #pragma unroll
             for (int k = 0; k < W; ++k)
-                if (c + q * W + k < a.width) to[q * W + k] = o[k];
+                if (c + q * W + k < a.fill) to[q * W + k] = c + q * W + k < a.width ? o[k] : static_cast<T>(0.0f);
         }
     }
 }
@@ -207,7 +207,8 @@ hipError_t pack(ScaledPack a, hipStream_t s)
 template <typename T>
 hipError_t unpack(ScaledUnpack a, hipStream_t s)
 {
-    a.chunks = ceil_div(a.width, 16);
+    if (a.fill < a.width) a.fill = a.width;
+    a.chunks = ceil_div(a.fill, 16);
     in_launches(ceil_div(a.rows * a.chunks, 256), 256, [&](int64_t first, int64_t count) {
         scaled_unpack_kernel<T><<<dim3((unsigned)count), 256, 0, s>>>(a, first);
     });

@@ -1,0 +1,926 @@
+// Matrix product of 8-bit operands with a power of two for every 128 elements of the depth
+// (ops_scaled.h): C[i][j] = sum_k A[i][k] B[j][k], both with k along their rows.
+//
+// The matrix instruction takes 16 x 16 x 128 codes and a scale byte of each operand's row for
+// them, so a block is one instruction: the scales cost no arithmetic, and sums stay in its fp32
+// accumulators from the first block to the last.  (With scales that are no powers of two,
+// every instruction's 4 results a lane would be multiplied and added by the vector unit: as
+// many cycles again.)
+//
+// Large: a workgroup of 4 waves (2 by 2) takes 32 NI x 256 results, 128 deep at a time, both
+// operands' pieces straight to LDS, double buffered.  A wave has 16 NI x 128 results, and
+// with NI = 8 a SIMD's registers to itself: what is read from LDS is two thirds of what 8 waves
+// would read.  (Which of a row's chunks stands at which k of an instruction does not
+// matter, as long as both operands agree.)
+//
+// Few rows: B is what costs.  A wave takes 16 of its rows straight to registers, the waves of a
+// workgroup share the depth and add their sums in LDS: one launch, no workspace.
+
+#include <type_traits>
+
+#include "ops_common.h"
+#include "ops_gemm.h"
+#include "ops_internal.h"
+#include "ops_scaled.h"
+
+namespace zo {
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+constexpr int kBlock = kScaleBlock;
+constexpr int kAllDone = 0x0070;        // s_waitcnt vmcnt(0) lgkmcnt(0)
+
+constexpr int kThreads = 256;
+
+// Workgroups go round the dies; each die gets a run of tiles that lie together.
+constexpr uint32_t kDies = 8;
+
+// The n-th tile in that order: 8 tiles of i by all of j, column by column, so that a die's L2 serves
+// the tiles that share an operand.
+__device__ __forceinline__ void tile_at(uint32_t n, uint32_t ti, uint32_t tj, uint32_t& i, uint32_t& j)
+{
+    constexpr uint32_t kGroup = 8;
+    const uint32_t per = kGroup * tj, g = n / per, first = g * kGroup;
+    const uint32_t high = ti - first < kGroup ? ti - first : kGroup;
+    i = __builtin_amdgcn_readfirstlane(first + (n - g * per) % high);
+    j = __builtin_amdgcn_readfirstlane((n - g * per) / high);
+}
+
+// The tile of workgroup `id` of as many as there are tiles.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti, uint32_t tj, uint32_t& i, uint32_t& j)
+{
+    const uint32_t die = id % kDies, q = tiles / kDies, r = tiles % kDies;
+    tile_at(die * q + (die < r ? die : r) + id / kDies, ti, tj, i, j);
+}
+
+// ------------------------------------------------------------------ tiles
+
+struct TileArgs {
+    const uint8_t* a;
+    const uint8_t* b;
+    const uint8_t* a_exps;
+    const uint8_t* b_exps;
+    int64_t a_ld, b_ld, a_exps_ld, b_exps_ld;
+    int64_t depth;
+    int blocks;                // of the depth
+    void* out;
+    const void* bias;
+    float* part;               // splits: fp32 parts [split][rows][cols], else NULL
+    int64_t rows, cols, out_ld;
+    uint32_t ti, tj;
+    int splits;                // each at least one block
+};
+
+// One load of 256 bytes into LDS at byte address `lds`: the lane's 4 bytes at offset v.  As
+// load_to_lds.
+__device__ __forceinline__ void load_words_to_lds(uint32_t v, const u4& rsrc, uint32_t lds)
+{
+    const uint32_t m = __builtin_amdgcn_readfirstlane(lds);
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(m), "v"(v), "s"(rsrc));
+}
+
+// The scales of up to 256 rows and 2 steps in LDS: the two words of 4 bytes that a row's two may
+// lie in, as they are aligned in memory, [2][256].  Whole words are read: those that the first
+// and the last byte lie in have others before and behind them.
+struct Scales {
+    static constexpr int kBytes = 2 * 256 * 4;
+    Piece piece;
+    uint32_t from;             // a lane's row: its next byte, from the words' beginning on
+    int skew;                  // of the rows that a lane needs: the first byte's place in its word
+
+    // The steps from -back on (0 or 1).
+    __device__ __forceinline__ void begin(const uint8_t* x, int64_t ld, int rows, int64_t blocks, int back, int wave, int row)
+    {
+        const int over = (int)(reinterpret_cast<uintptr_t>(x) & 3);
+        piece.base = reinterpret_cast<const char*>(x) - over;
+        piece.left = whole_words(over + (rows - 1) * ld + blocks);
+        const int mine = wave * 64 + (threadIdx.x & 63);
+        from = mine < rows ? (uint32_t)(over + mine * (int)ld - back) : kOutOfRange;
+        skew = over + row * (int)ld - back;
+    }
+    // The next 2 steps', to LDS at `lds`.
+    __device__ __forceinline__ void issue(uint32_t lds, int wave)
+    {
+        const u4 rsrc = piece.descriptor();
+        const uint32_t at = from & ~3u;
+        load_words_to_lds(at, rsrc, lds + wave * 256);
+        load_words_to_lds(at + 4, rsrc, lds + 1024 + wave * 256);
+        from += 2;
+    }
+    // Where the scale of step s is (counted from -back on), of row `row`.
+    __device__ __forceinline__ uint32_t at(uint32_t lds, int row, int s) const
+    {
+        const int byte = ((skew + (s & ~1)) & 3) + (s & 1);
+        return lds + row * 4 + (byte >> 2) * 1024 + (byte & 3);
+    }
+};
+
+// One operand's rows of a tile: 32 Q rows of 128 codes in LDS, chunk c of 16 codes of a row at
+// place c ^ key(row), so that the rows that one read touches lie in different banks.  A
+// wave loads 8 rows at a time.
+//
+// Fragments: lane l has row l % 16 of a product, chunks g and g + 4 with g = l / 16.  Product t
+// takes rows 16 t + r; with RUNS products 4 u to 4 u + 3 take rows 64 u + 16 (r / 4) + 4 (t % 4) + r % 4,
+// and the four give each lane 16 results side by side.
+template <int Q, bool RUNS>
+struct Rows {
+    static constexpr int kBytes = Q * 32 * kBlock;
+    Piece piece;
+    int64_t left;              // codes of a row from here on
+    uint32_t voff, apart, addr;
+    int chunk;                 // a lane's, in 16 codes
+
+    static __device__ __forceinline__ int key(int row) { return RUNS ? (row & 3) | ((row >> 4) & 1) << 2 : row & 7; }
+    __device__ __forceinline__ void lanes(int64_t ld, int wave, int lane)
+    {
+        const int row = wave * 8 + (lane >> 3);            // (32 rows on the key is the same)
+        chunk = ((lane & 7) ^ key(row)) * 16;
+        voff = (uint32_t)(row * ld + chunk);
+        apart = (uint32_t)(32 * ld);
+    }
+    __device__ __forceinline__ void begin(const uint8_t* x, int64_t ld, int64_t row0, int64_t rows, int64_t k0, int64_t depth)
+    {
+        piece.base = reinterpret_cast<const char*>(x) + row0 * ld + k0;
+        const int64_t all = rows - row0 < Q * 32 ? rows - row0 : Q * 32;
+        piece.left = whole_words((all - 1) * ld + depth - k0);
+        piece.step = kBlock;
+        left = depth - k0;
+    }
+    __device__ __forceinline__ void issue(uint32_t lds, int wave)
+    {
+        const u4 rsrc = piece.descriptor();
+        uint32_t first = chunk >= left ? kOutOfRange : voff;
+        const uint32_t by = chunk >= left ? 0 : apart;
+        asm volatile("" : "+v"(first));      // (added to here, not kept Q times in registers)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) load_to_lds(first + q * by, rsrc, lds + (q * 4 + wave) * 1024);
+        piece.advance();
+        left -= kBlock;
+    }
+    // first: the wave's first row
+    __device__ __forceinline__ void reader(uint32_t lds, int first, int lane)
+    {
+        const int r = lane & 15, g = lane >> 4;
+        const int row = first + (RUNS ? (r >> 2) * 16 + (r & 3) : r);
+        addr = lds + row * 128 + ((g ^ key(row)) << 4);
+    }
+    __device__ __forceinline__ v8i get(uint32_t stage, int t) const
+    {
+        const uint32_t on = RUNS ? (t >> 2) * 8192 + (t & 3) * 512 : t * 2048;
+        const u4 lo = *(ZO_LDS const u4*)(uintptr_t)(addr + stage + on);
+        const u4 hi = *(ZO_LDS const u4*)(uintptr_t)((addr ^ 64) + stage + on);
+        return __builtin_bit_cast(v8i, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+template <int NI, bool SQUARE>
+struct Tile {
+    static constexpr int NJ = 8;
+    static constexpr int kTileI = 32 * NI, kTileJ = 32 * NJ;
+    static constexpr int H = NI / 2, HJ = NJ / 2;  // products of half a step
+    using PSide = Rows<NI, false>;
+    using QSide = Rows<NJ, true>;
+    static constexpr int kStageBytes = PSide::kBytes + QSide::kBytes;
+    static constexpr int kScaleBytes = 2 * Scales::kBytes;         // of both operands
+    static constexpr int kLds = 2 * (kStageBytes + kScaleBytes);
+    static constexpr int NQ = SQUARE ? 1 : NJ;     // scales of B that a lane needs (a wave's 128 rows are one square's)
+
+    PSide p;
+    QSide q;
+    Scales pe, qe;
+    int wave;
+    uint32_t smem, scales;                         // LDS: the stages, the scales
+    uint32_t ps[2][NI], qs[2][NQ];                 // of a step, and the next
+    v8i a[NJ], b[NI];
+
+    __device__ __forceinline__ Tile(const TileArgs& t, uint32_t lds) : smem(lds), scales(lds + 2 * kStageBytes)
+    {
+        const int lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        p.lanes(t.a_ld, wave, lane);
+        q.lanes(t.b_ld, wave, lane);
+        p.reader(smem, (wave >> 1) * 16 * NI, lane);
+        q.reader(smem + PSide::kBytes, (wave & 1) * 128, lane);
+    }
+    // The next step's loads have arrived, for every wave; and every wave has all that it reads
+    // of this stage.
+    __device__ __forceinline__ void turn()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(kAllDone);      // (the builtin: the compiler counts on it)
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void issue(uint32_t stage)
+    {
+        p.issue(smem + stage, wave);
+        q.issue(smem + stage + PSide::kBytes, wave);
+    }
+    // Scales of 2 steps, of an even or an odd pair.
+    __device__ __forceinline__ void issue_scales(int pair)
+    {
+        const uint32_t to = scales + (pair & 1) * kScaleBytes;
+        pe.issue(to, wave);
+        qe.issue(to + Scales::kBytes, wave);
+    }
+    static __device__ __forceinline__ uint32_t byte_at(uint32_t at) { return *(ZO_LDS const uint8_t*)(uintptr_t)at; }
+    __device__ __forceinline__ int row_i() const { return (wave >> 1) * 16 * NI + (threadIdx.x & 15); }
+    __device__ __forceinline__ int row_j() const
+    {
+        const int r = threadIdx.x & 15;
+        return SQUARE ? (wave & 1) : (wave & 1) * 128 + (r >> 2) * 16 + (r & 3);
+    }
+    template <int F>
+    __device__ __forceinline__ void read_scales(int s)
+    {
+        const uint32_t from = scales + ((s >> 1) & 1) * kScaleBytes;
+        const uint32_t pa = pe.at(from, row_i(), s), qa = qe.at(from + Scales::kBytes, row_j(), s);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) ps[F][k] = byte_at(pa + k * 64);
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) qs[F][k] = byte_at(qa + (k >> 2) * 256 + (k & 3) * 16);
+    }
+    // Steps go in pairs, the first of a pair through the first stage; of an odd count the first is the
+    // second of its pair.
+    // Start on the tile at (i0, j0), `steps` blocks from b0 on.
+    __device__ __forceinline__ void begin(const TileArgs& t, int64_t i0, int64_t j0, int b0, int steps)
+    {
+        p.begin(t.a, t.a_ld, i0, t.rows, (int64_t)b0 * kBlock, t.depth);
+        q.begin(t.b, t.b_ld, j0, t.cols, (int64_t)b0 * kBlock, t.depth);
+        const int64_t i = t.rows - i0, j = t.cols - j0;
+        const int back = steps & 1;
+        pe.begin(t.a_exps + i0 * t.a_exps_ld + b0, t.a_exps_ld, (int)(i < kTileI ? i : kTileI), t.blocks - b0, back, wave, row_i());
+        if constexpr (SQUARE) qe.begin(t.b_exps + (j0 >> 7) * t.b_exps_ld + b0, t.b_exps_ld, j > 128 ? 2 : 1, t.blocks - b0, back, wave, row_j());
+        else qe.begin(t.b_exps + j0 * t.b_exps_ld + b0, t.b_exps_ld, (int)(j < kTileJ ? j : kTileJ), t.blocks - b0, back, wave, row_j());
+        issue_scales(0);
+        issue(back ? kStageBytes : 0);
+        if (steps > 1) issue(back ? 0 : kStageBytes);
+        issue_scales(1);
+    }
+    // (Of the second stage, the last step's.)  The codes behind the depth's end, in the last block's chunk that it ends in, are other
+    // rows': zeros instead.  (Both sides: 0 times NaN is none.)
+    __device__ __forceinline__ void cut(const TileArgs& t)
+    {
+        const int chunk = (int)((t.depth - 1) % kBlock) >> 4, tail = (int)(t.depth & 15);
+        for (int row = threadIdx.x; row < kTileI + kTileJ; row += kThreads) {
+            const bool second = row >= kTileI;
+            const int r = second ? row - kTileI : row;
+            const int key = second ? QSide::key(r) : PSide::key(r);
+            ZO_LDS u4* to = (ZO_LDS u4*)(uintptr_t)(smem + kStageBytes + (second ? PSide::kBytes : 0) + r * 128 + ((chunk ^ key) << 4));
+            u4 v = *to;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int keep = tail - 4 * k;             // bytes of this word
+                v[k] = keep >= 4 ? v[k] : keep <= 0 ? 0 : v[k] & ((1u << (8 * keep)) - 1);
+            }
+            *to = v;
+        }
+        __syncthreads();
+    }
+    // A quarter of a step: rows half J of B by half I of A, and between its products `read` of 0 to 3.
+    // The instruction is written out because its sums have to stay where they are: the
+    // builtin's result may go to other registers, and with 256 of 512 of them sums the compiler
+    // moves 100 a step.  (What it reads has been written by an s_nop 1 before at least; what it
+    // writes is read by the next step's products, and by `settled`.)
+    template <int F, int J, int I, typename R>
+    __device__ __forceinline__ void multiply(f4 (&acc)[NI][NJ], R read)
+    {
+#pragma unroll
+        for (int j = 0; j < HJ; ++j) {
+            read(j);
+#pragma unroll
+            for (int i = I * H; i < (I + 1) * H; ++i)
+                asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                             : "+a"(acc[i][J * HJ + j])
+                             : "v"(a[J * HJ + j]), "v"(b[i]), "v"(qs[F][SQUARE ? 0 : J * HJ + j]), "v"(ps[F][i]));
+        }
+    }
+    // The sums can be read: an instruction of 16 passes writes its last 18 wait states on.
+    static __device__ __forceinline__ void settled(f4 (&acc)[NI][NJ])
+    {
+        asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) asm volatile("" : "+a"(acc[i][j]));
+    }
+    template <int J>
+    __device__ __forceinline__ void read_a(uint32_t stage, int k)
+    {
+        a[J * HJ + k] = q.get(stage, J * HJ + k);
+    }
+    template <int I>
+    __device__ __forceinline__ void read_b(uint32_t stage, int k)
+    {
+        if (k < H) b[I * H + k] = p.get(stage, I * H + k);
+    }
+    // What the first step, at parity F, begins with.
+    template <int F>
+    __device__ __forceinline__ void first(int s)
+    {
+        constexpr uint32_t stage = F ? kStageBytes : 0;
+#pragma unroll
+        for (int k = 0; k < HJ; ++k) read_a<0>(stage, k);
+#pragma unroll
+        for (int k = 0; k < H; ++k) read_b<F>(stage, k);
+        read_scales<F>(s);
+    }
+    // A step, in quarters.  Each is multiplied while what the next one lacks is read: first what the
+    // step has, then its other half of A's rows, then of B's; behind the barrier the next step's
+    // first halves, each into registers that the quarter before has freed.  So the halves of A's
+    // rows change places from step to step (F, the stage too).
+    template <int F, typename B>
+    __device__ __forceinline__ void half_step(f4 (&acc)[NI][NJ], B behind)
+    {
+        constexpr uint32_t stage = F ? kStageBytes : 0;
+        multiply<F, 0, F>(acc, [&](int k) { read_b<1 - F>(stage, k); });
+        multiply<F, 0, 1 - F>(acc, [&](int k) { read_a<1>(stage, k); });
+        turn();
+        behind();
+    }
+    template <int F>
+    __device__ __forceinline__ void other_half(int s, f4 (&acc)[NI][NJ])
+    {
+        constexpr uint32_t other = F ? 0 : kStageBytes;
+        read_scales<1 - F>(s + 1);
+        multiply<F, 1, 1 - F>(acc, [&](int k) { read_a<0>(other, k); });
+        multiply<F, 1, F>(acc, [&](int k) { read_b<1 - F>(other, k); });
+    }
+    // acc[ti][tj][e]: i = row_of(ti), j = column_of(tj) + e, within the tile.  `last` says whether the
+    // share's last block is the depth's.  `free` is called when both stages have been read.
+    // (No branch within the steps that repeat: with one the compiler keeps fewer sums in place.)
+    template <typename N>
+    __device__ __forceinline__ void run(const TileArgs& t, int steps, bool last, f4 (&acc)[NI][NJ], N free)
+    {
+#pragma unroll
+        for (int ti = 0; ti < NI; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < NJ; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
+        turn();
+        const bool ends = last && (t.depth & 15) != 0;
+        const int back = steps & 1, pairs = (steps + 1) / 2;
+        int pair = back;
+        if (back) {
+            if (ends && steps == 1) cut(t);
+            first<1>(1);
+            if (steps > 1) {
+                half_step<1>(acc, [&] {
+                    issue(kStageBytes);
+                    issue_scales(0);
+                });
+                other_half<1>(1, acc);
+            }
+        } else {
+            first<0>(0);
+        }
+        for (; pair + 1 < pairs; ++pair) {
+            half_step<0>(acc, [&] { issue(0); });
+            other_half<0>(2 * pair, acc);
+            half_step<1>(acc, [&] {
+                issue(kStageBytes);
+                issue_scales(pair);                    // (of the pair two on)
+            });
+            other_half<1>(2 * pair + 1, acc);
+        }
+        if (steps > 1) {
+            half_step<0>(acc, [&] {
+                if (ends) cut(t);
+            });
+            other_half<0>(2 * pair, acc);
+        }
+        half_step<1>(acc, free);
+        multiply<1, 1, 0>(acc, [](int) {});
+        multiply<1, 1, 1>(acc, [](int) {});
+        settled(acc);
+    }
+    static __device__ __forceinline__ int column_of(int tj, int wave, int lane) { return (wave & 1) * 128 + (tj >> 2) * 64 + (lane >> 4) * 16 + (tj & 3) * 4; }
+    static __device__ __forceinline__ int row_of(int ti, int wave, int lane) { return (wave >> 1) * 16 * NI + ti * 16 + (lane & 15); }
+};
+
+// A lane's 16 results of a row side by side, twice.
+template <typename T, int NI, bool SQUARE>
+__device__ __forceinline__ void tile_out(const TileArgs& t, int64_t split, int64_t bi, int64_t bj, f4 (&acc)[NI][8])
+{
+    using G = Tile<NI, SQUARE>;
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));      // (addresses are made here, and not kept in registers over the products)
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int run = 0; run < 2; ++run) {
+        const int64_t j = bj * G::kTileJ + G::column_of(4 * run, wave, lane);
+        if (j >= t.cols) continue;
+        const bool whole = j + 16 <= t.cols;
+        float bias[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            bias[k] = t.bias != nullptr && t.part == nullptr && j + k < t.cols ? (float)static_cast<const T*>(t.bias)[j + k] : 0.0f;
+#pragma unroll
+        for (int ti = 0; ti < NI; ++ti) {
+            const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
+            if (i >= t.rows) continue;
+            if (t.part != nullptr) {
+                float* to = t.part + (split * t.rows + i) * t.cols + j;
+                if (whole) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) store_vec<float, 4>(to + 4 * q, acc[ti][4 * run + q]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (j + k < t.cols) to[k] = acc[ti][4 * run + (k >> 2)][k & 3];
+                }
+                continue;
+            }
+            T* to = static_cast<T*>(t.out) + i * t.out_ld + j;
+            constexpr int W = Vec<T>::W;
+            if (whole) {
+#pragma unroll
+                for (int q = 0; q < 16 / W; ++q) {
+                    vec_t<T, W> y;
+#pragma unroll
+                    for (int e = 0; e < W; ++e) y[e] = static_cast<T>(acc[ti][4 * run + ((q * W + e) >> 2)][e & 3] + bias[q * W + e]);
+                    store_vec<T, W>(to + q * W, y);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (j + k < t.cols) to[k] = static_cast<T>(acc[ti][4 * run + (k >> 2)][k & 3] + bias[k]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t lds_address(char* smem) { return (uint32_t)(uintptr_t)(ZO_LDS char*)smem; }
+
+// A die's workgroups walk its tiles (each tile once for every split of the depth), and load the
+// next while they store a tile's results.
+template <typename T, int NI, bool SQUARE>
+__global__ __launch_bounds__(kThreads, NI == 2 ? 2 : 1) void tile_kernel(TileArgs t)
+{
+    using G = Tile<NI, SQUARE>;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const uint32_t tiles = t.ti * t.tj, all = tiles * t.splits;
+    const uint32_t die = blockIdx.x % kDies, q = all / kDies, r = all % kDies;
+    const uint32_t mine = q + (die < r ? 1 : 0);
+    const uint32_t stride = (gridDim.x + kDies - 1 - die) / kDies;       // workgroups of the die
+    uint32_t at = blockIdx.x / kDies;
+    if (at >= mine) return;
+    G g(t, lds_address(smem));
+    uint32_t bi = 0, bj = 0;
+    int split = 0, b0 = 0, steps = 0;
+    auto place = [&] {
+        // (a die's share of all splits' tiles, one split after the other)
+        const uint32_t n = die * q + (die < r ? die : r) + at;
+        split = __builtin_amdgcn_readfirstlane(n / tiles);
+        tile_at(n - (uint32_t)split * tiles, t.ti, t.tj, bi, bj);
+        b0 = (int)((int64_t)t.blocks * split / t.splits);
+        steps = (int)((int64_t)t.blocks * (split + 1) / t.splits) - b0;
+        g.begin(t, (int64_t)bi * G::kTileI, (int64_t)bj * G::kTileJ, b0, steps);
+    };
+    place();
+    for (;;) {
+        f4 acc[NI][8];
+        const uint32_t i = bi, j = bj;
+        const int now = steps, part = split;
+        const bool last = b0 + steps == t.blocks;
+        at += stride;
+        g.run(t, now, last, acc, [&] {
+            if (at < mine) place();
+        });
+        tile_out<T, NI, SQUARE>(t, part, i, j, acc);
+        if (at >= mine) return;
+    }
+}
+
+// The parts of a split product, added in the order of the splits: W results a lane.
+template <typename T, int W>
+__global__ __launch_bounds__(256) void join_parts_kernel(const float* part, int splits, int64_t rows, int64_t cols, const T* bias, T* out,
+                                                         int64_t out_ld, int64_t first)
+{
+    const int64_t all = rows * cols, at = ((first + blockIdx.x) * 256 + threadIdx.x) * W;
+    if (at >= all) return;
+    const int64_t i = at / cols, j = at - i * cols;
+    float s[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) s[e] = bias != nullptr ? (float)bias[j + e] : 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < splits; ++k) {
+        const vec_t<float, W> x = *reinterpret_cast<const vec_t<float, W>*>(part + k * all + at);
+#pragma unroll
+        for (int e = 0; e < W; ++e) s[e] += x[e];
+    }
+    vec_t<T, W> y;
+#pragma unroll
+    for (int e = 0; e < W; ++e) y[e] = static_cast<T>(s[e]);
+    store_vec<T, W>(out + i * out_ld + j, y);
+}
+
+// Codes whose rows cannot be loaded as they lie, to rows of ld (a multiple of 16) with zeros
+// behind the depth: of one array or, from workgroup `first` on, of another.
+struct Recode {
+    const uint8_t* x;
+    uint8_t* out;
+    int64_t stride, rows;
+};
+
+__global__ __launch_bounds__(256) void recode_kernel(Recode a, Recode b, int64_t base, int64_t first, int64_t depth, int64_t ld)
+{
+    const int64_t group = base + blockIdx.x;
+    const bool second = group >= first;
+    const Recode r = second ? b : a;
+    const int64_t at = ((group - (second ? first : 0)) * 256 + threadIdx.x) * 16;
+    if (at >= r.rows * ld) return;
+    const int64_t i = at / ld, c = at - i * ld;
+    const uint8_t* x = r.x + i * r.stride + c;
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (c + 16 <= depth) {
+        __builtin_memcpy(v, x, 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (c + k < depth) v[k / 4] |= (uint32_t)x[k] << (8 * (k % 4));
+    }
+    *reinterpret_cast<uint4*>(r.out + at) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// ------------------------------------------------------------------ fp32 results
+//
+// The 8-bit instructions align 8 products at a time to the largest of them and keep 13 bits
+// below it (measured: 1.3e-5 of a result's size in the mean, 2^-15.5 at most of the absolute sum).
+// Of a 2-byte result that is a hundredth or a tenth of its rounding, of one in fp32 a hundred
+// times its own; so those are summed by bf16 instructions, whose products are exact.  The operands'
+// values, which bf16 holds, are written out first: 3 bytes a code in 5 TB/s, against the
+// products' 2 operations for each of 256 results it meets.
+
+struct ExactArgs {
+    Operand a, b;
+    float* out;                // fp32 results; of a split [split][rows][cols]
+    const float* bias;
+    int64_t rows, cols, out_ld, split_ld;
+    uint32_t ti, tj;
+    int64_t steps;             // of the whole depth
+    int splits;
+};
+
+template <int NI, int NJ>
+__global__ __launch_bounds__(kGemmThreads, 2) void exact_kernel(ExactArgs t)
+{
+    using G = Gemm<__bf16, kInner, kInner, NI, NJ>;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const uint32_t tiles = t.ti * t.tj;
+    const int64_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
+    uint32_t bi, bj;
+    tile_of(blockIdx.x % tiles, tiles, t.ti, t.tj, bi, bj);
+    const int64_t s0 = t.steps * split / t.splits, s1 = t.steps * (split + 1) / t.splits;
+    f4 acc[NI][NJ];
+    G g(t.a, t.b, lds_address(smem));
+    g.begin(t.a, t.b, (int64_t)bi * G::kTileI, (int64_t)bj * G::kTileJ, s0 * kDeep, (int)(s1 - s0));
+    g.run((int)(s1 - s0), acc, [] {});
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int ti = 0; ti < NI; ++ti) {
+        const int64_t i = (int64_t)bi * G::kTileI + G::row_of(ti, wave, lane);
+        if (i >= t.rows) continue;
+        float* to = t.out + split * t.split_ld + i * t.out_ld;
+#pragma unroll
+        for (int tj = 0; tj < NJ; ++tj) {
+            const int64_t j = (int64_t)bj * G::kTileJ + G::column_of(tj, wave, lane);
+            f4 y = acc[ti][tj];
+            if (t.bias != nullptr) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] += j + e < t.cols ? t.bias[j + e] : 0.0f;
+            }
+            if (j + 4 <= t.cols) {
+                store_vec<float, 4>(to + j, y);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < t.cols) to[j + e] = y[e];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ few rows
+
+struct FewArgs {
+    const uint8_t* a;
+    const uint8_t* b;
+    const uint8_t* a_exps;
+    const uint8_t* b_exps;
+    int64_t a_ld, b_ld, a_exps_ld, b_exps_ld;
+    int64_t rows, cols, depth, out_ld;
+    const void* bias;
+    void* out;
+    int waves;                 // of a workgroup
+    int square;
+};
+
+// A lane's 32 codes of block s of a row; zeros behind the depth.
+__device__ __forceinline__ v8i codes_at(const uint8_t* row, int64_t k, int64_t depth)
+{
+    v8i v;
+    if (k + 32 <= depth) {
+        __builtin_memcpy(&v, row + k, 32);
+        return v;
+    }
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (k + 4 * w + e < depth) x |= (uint32_t)row[k + 4 * w + e] << (8 * e);
+        v[w] = (int)x;
+    }
+    return v;
+}
+
+// The codes' products with their scales, added to c: in 8 bits, or exactly, as bf16 (a quarter of the
+// depth at a time).
+template <bool EXACT>
+__device__ __forceinline__ f4 product_of(const v8i& a, const v8i& b, f4 c, uint32_t scale_a, uint32_t scale_b)
+{
+    if constexpr (!EXACT) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, (int)scale_a, 0, (int)scale_b);
+    } else {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        const float sa = scale_value(scale_a), sb = scale_value(scale_b);
+        auto part = [](const v8i& x, int q, float s) {
+            const b2 v[4] = {
+                __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], s, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], s, true),
+                __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], s, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], s, true)};
+            s8 y;
+            __builtin_memcpy(&y, v, 16);
+            return y;
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c = Mfma<__bf16>::run(part(a, q, sa), part(b, q, sb), c);
+        return c;
+    }
+}
+
+// 16 rows of B and 16 MT of A.  Wave w takes blocks w, w + waves, ...
+template <typename T, int MT>
+__global__ __launch_bounds__(1024) void few_kernel(FewArgs f, int64_t first)
+{
+    constexpr bool EXACT = std::is_same<T, float>::value;
+    __shared__ float sums[16][MT][16][17];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t n0 = (first + blockIdx.x) * 16;
+    const int64_t n = n0 + r < f.cols ? n0 + r : f.cols - 1;
+    const uint8_t* b = f.b + n * f.b_ld;
+    const uint8_t* be = f.b_exps + (f.square ? n / kBlock : n) * f.b_exps_ld;
+    const uint8_t* a[MT];
+    const uint8_t* ae[MT];
+    f4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int64_t m = t * 16 + r < f.rows ? t * 16 + r : f.rows - 1;
+        a[t] = f.a + m * f.a_ld;
+        ae[t] = f.a_exps + m * f.a_exps_ld;
+        acc[t] = f4{0, 0, 0, 0};
+    }
+    const int whole = (int)(f.depth / kBlock), blocks = (int)ceil_div(f.depth, kBlock);
+    for (int s = wave; s < whole; s += f.waves) {
+        v8i x;
+        __builtin_memcpy(&x, b + (int64_t)s * kBlock + g * 32, 32);
+        const uint32_t scale = be[s];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            v8i y;
+            __builtin_memcpy(&y, a[t] + (int64_t)s * kBlock + g * 32, 32);
+            acc[t] = product_of<EXACT>(x, y, acc[t], scale, ae[t][s]);
+        }
+    }
+    if (blocks > whole && wave == whole % f.waves) {
+        const int64_t k = (int64_t)whole * kBlock + g * 32;
+        const v8i x = codes_at(b, k, f.depth);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = product_of<EXACT>(x, codes_at(a[t], k, f.depth), acc[t], be[whole], ae[t][whole]);
+    }
+    // a lane: column (of A's rows) r, results 4 g to 4 g + 3 of B's rows
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave][t][r][4 * g + e] = acc[t][e];
+    __syncthreads();
+    for (int k = threadIdx.x; k < MT * 256; k += f.waves * 64) {
+        const int64_t m = k >> 4, j = n0 + (k & 15);
+        if (m >= f.rows || j >= f.cols) continue;
+        float s = 0.0f;
+        for (int w = 0; w < f.waves; ++w) s += sums[w][m >> 4][m & 15][k & 15];
+        if (f.bias != nullptr) s += (float)static_cast<const T*>(f.bias)[j];
+        static_cast<T*>(f.out)[m * f.out_ld + j] = static_cast<T>(s);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+
+// Rows up to which B goes straight to registers.
+constexpr int64_t kFewRows = 32;
+
+template <typename K>
+hipError_t allow(K kernel, int lds)
+{
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+}
+
+template <typename T, int NI, bool SQUARE>
+hipError_t tiles(TileArgs t, hipStream_t s)
+{
+    using G = Tile<NI, SQUARE>;
+    static const hipError_t allowed = allow(tile_kernel<T, NI, SQUARE>, G::kLds);
+    if (allowed != hipSuccess) return allowed;
+    t.ti = (uint32_t)ceil_div(t.rows, G::kTileI);
+    t.tj = (uint32_t)ceil_div(t.cols, G::kTileJ);
+    const int64_t all = (int64_t)t.ti * t.tj * t.splits, stand = kCUs * (NI == 2 ? 2 : 1);
+    tile_kernel<T, NI, SQUARE><<<dim3((unsigned)(all < stand ? all : stand)), kThreads, G::kLds, s>>>(t);
+    return hipSuccess;
+}
+
+template <typename T, int NI>
+hipError_t tiles(const TileArgs& t, bool square, hipStream_t s)
+{
+    return square ? tiles<T, NI, true>(t, s) : tiles<T, NI, false>(t, s);
+}
+
+// What the tiles' loads need of an address and a row stride.
+bool loads_as_it_is(const void* p, int64_t stride)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && stride % 4 == 0 && stride <= (1 << 22);
+}
+
+template <int NI, int NJ>
+hipError_t exact(ExactArgs t, hipStream_t s)
+{
+    using G = Gemm<__bf16, kInner, kInner, NI, NJ>;
+    static const hipError_t allowed = allow(exact_kernel<NI, NJ>, G::kLds);
+    if (allowed != hipSuccess) return allowed;
+    t.ti = (uint32_t)ceil_div(t.rows, G::kTileI);
+    t.tj = (uint32_t)ceil_div(t.cols, G::kTileJ);
+    exact_kernel<NI, NJ><<<dim3(t.ti * t.tj * t.splits), kGemmThreads, G::kLds, s>>>(t);
+    return hipSuccess;
+}
+
+// fp32 results: the operands' values in bf16, and their product.
+hipError_t exact(const ScaledProduct& a, const ProductPlan& p, float* part, hipStream_t s)
+{
+    void* wide_a = a.space + p.off_a;
+    void* wide_b = a.space + p.off_b;
+    hipError_t e = scaled_unpack(ScaledUnpack{a.a, a.a_exps, wide_a, p.m, p.k, a.a_stride, a.a_exps_stride, p.k_ld, p.k_ld, 0, false}, 2, s);
+    if (e == hipSuccess) e = scaled_unpack(ScaledUnpack{a.b, a.b_exps, wide_b, p.n, p.k, a.b_stride, a.b_exps_stride, p.k_ld, p.k_ld, 0, a.square}, 2, s);
+    if (e != hipSuccess) return e;
+    ExactArgs t{};
+    t.a = Operand{wide_a, p.k_ld, p.m, p.k_ld};
+    t.b = Operand{wide_b, p.k_ld, p.n, p.k_ld};
+    t.rows = p.m;
+    t.cols = p.n;
+    t.steps = ceil_div(p.k_ld, kDeep);
+    t.splits = p.splits;
+    t.out = p.splits > 1 ? part : static_cast<float*>(a.out);
+    t.out_ld = p.splits > 1 ? p.n : a.out_stride;
+    t.split_ld = p.m * p.n;
+    t.bias = p.splits > 1 ? nullptr : static_cast<const float*>(a.bias);
+    return p.ni == 8 ? exact<8, 4>(t, s) : exact<2, 4>(t, s);
+}
+
+template <typename T>
+hipError_t product(const ScaledProduct& a, const ProductPlan& p, hipStream_t s)
+{
+    if (p.m == 0 || p.n == 0) return hipSuccess;
+    float* part = reinterpret_cast<float*>(a.space + p.off_part);
+    auto join = [&](int splits) {
+        const T* bias = static_cast<const T*>(a.bias);
+        T* out = static_cast<T*>(a.out);
+        const int wide = p.n % 4 == 0 ? 4 : 1;
+        in_launches(ceil_div(p.m * p.n, 256 * wide), 256, [&](int64_t first, int64_t count) {
+            if (wide == 4) join_parts_kernel<T, 4><<<dim3((unsigned)count), 256, 0, s>>>(part, splits, p.m, p.n, bias, out, a.out_stride, first);
+            else join_parts_kernel<T, 1><<<dim3((unsigned)count), 256, 0, s>>>(part, splits, p.m, p.n, bias, out, a.out_stride, first);
+        });
+    };
+    if (p.k == 0) {                            // a sum of nothing
+        join(0);
+        return hipGetLastError();
+    }
+    if (p.ni == 0) {
+        const FewArgs f{a.a, a.b, a.a_exps, a.b_exps, a.a_stride, a.b_stride, a.a_exps_stride, a.b_exps_stride, p.m, p.n, p.k, a.out_stride,
+                        a.bias, a.out, p.splits, a.square};
+        in_launches(ceil_div(p.n, 16), p.splits * 64, [&](int64_t first, int64_t count) {
+            if (p.m <= 16) few_kernel<T, 1><<<dim3((unsigned)count), p.splits * 64, 0, s>>>(f, first);
+            else few_kernel<T, 2><<<dim3((unsigned)count), p.splits * 64, 0, s>>>(f, first);
+        });
+        return hipGetLastError();
+    }
+    if constexpr (std::is_same<T, float>::value) {
+        const hipError_t e = exact(a, p, part, s);
+        if (e == hipSuccess && p.splits > 1) join(p.splits);
+        return e != hipSuccess ? e : hipGetLastError();
+    } else {
+    const uint8_t* ac = a.a;
+    const uint8_t* bc = a.b;
+    int64_t a_ld = a.a_stride, b_ld = a.b_stride;
+    Recode copies[2];
+    int many = 0;
+    if (!loads_as_it_is(ac, a_ld)) {
+        uint8_t* to = reinterpret_cast<uint8_t*>(a.space + p.off_a);
+        copies[many++] = Recode{ac, to, a_ld, p.m};
+        ac = to;
+        a_ld = p.k_ld;
+    }
+    if (!loads_as_it_is(bc, b_ld)) {
+        uint8_t* to = reinterpret_cast<uint8_t*>(a.space + p.off_b);
+        copies[many++] = Recode{bc, to, b_ld, p.n};
+        bc = to;
+        b_ld = p.k_ld;
+    }
+    if (many > 0) {
+        const int64_t first = ceil_div(copies[0].rows * p.k_ld, 4096);
+        const int64_t all = first + (many > 1 ? ceil_div(copies[1].rows * p.k_ld, 4096) : 0);
+        in_launches(all, 256, [&](int64_t base, int64_t count) {
+            recode_kernel<<<dim3((unsigned)count), 256, 0, s>>>(copies[0], copies[many - 1], base, first, p.k, p.k_ld);
+        });
+    }
+    TileArgs t{};
+    t.a = ac;
+    t.b = bc;
+    t.a_ld = a_ld;
+    t.b_ld = b_ld;
+    t.depth = p.k;
+    t.a_exps = a.a_exps;
+    t.b_exps = a.b_exps;
+    t.a_exps_ld = a.a_exps_stride;
+    t.b_exps_ld = a.b_exps_stride;
+    t.blocks = (int)ceil_div(p.k, kBlock);
+    t.out = a.out;
+    t.bias = a.bias;
+    t.part = p.splits > 1 ? part : nullptr;
+    t.rows = p.m;
+    t.cols = p.n;
+    t.out_ld = a.out_stride;
+    t.splits = p.splits;
+    hipError_t e = p.ni == 8 ? tiles<T, 8>(t, a.square, s) : p.ni == 4 ? tiles<T, 4>(t, a.square, s) : tiles<T, 2>(t, a.square, s);
+    if (e != hipSuccess) return e;
+    if (p.splits > 1) join(p.splits);
+    return hipGetLastError();
+    }
+}
+
+}  // namespace
+
+ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type)
+{
+    ProductPlan p{};
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    p.k_ld = round_up(k, 16);
+    const int64_t blocks = ceil_div(k, kBlock);
+    if (m <= kFewRows) {
+        // waves of a workgroup, which share the depth: as many as find work, up to 16
+        p.splits = 1;
+        while (p.splits < 16 && p.splits * 2 <= blocks) p.splits *= 2;
+        p.bytes = 256;
+        return p;
+    }
+    // The tile and the parts of the depth by what they should take: a step of 256 x 256 x 128
+    // about 1.6 us, of 128 rows 0.9, of 64 0.6; in bf16 3.2 and, two to a CU, 1.6; a round's beginning and
+    // end 4; parts go through memory at 4 TB/s, and through a launch.
+    p.exact = type == 3;
+    double best = 0.0;
+    p.splits = 1;
+    for (int ni = 8; ni >= 2; ni /= 2) {
+        if (p.exact && ni == 4) continue;
+        const int64_t tiles = ceil_div(m, 32 * ni) * ceil_div(n, 256), stand = kCUs * (p.exact && ni == 2 ? 2 : 1);
+        const double step = p.exact ? (ni == 8 ? 3.2 : 1.6) : ni == 8 ? 1.6 : ni == 4 ? 0.9 : 0.6;
+        const int64_t most = blocks / 4 > 1 ? blocks / 4 : 1;
+        for (int64_t c = 1; c <= most && (c == 1 || tiles * c <= 4 * kCUs); ++c) {
+            const double t = ceil_div(tiles * c, stand) * (ceil_div(blocks, c) * step + 4.0) + (c > 1 ? 2.0 * c * m * n * 4 / 4e6 + 5.0 : 0.0);
+            if (best == 0.0 || t < best) {
+                best = t;
+                p.ni = ni;
+                p.splits = (int)c;
+            }
+        }
+    }
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t off = at;
+        at += round_up(bytes, 256);
+        return off;
+    };
+    p.off_part = take(p.splits > 1 ? p.splits * m * n * 4 : 0);
+    p.off_a = take(m * p.k_ld * (p.exact ? 2 : 1));
+    p.off_b = take(n * p.k_ld * (p.exact ? 2 : 1));
+    p.bytes = at > 256 ? at : 256;
+    return p;
+}
+
+hipError_t scaled_product(const ScaledProduct& a, const ProductPlan& p, int type, hipStream_t s)
+{
+    return type == 1 ? product<_Float16>(a, p, s) : type == 2 ? product<__bf16>(a, p, s) : product<float>(a, p, s);
+}
+
+}  // namespace zo

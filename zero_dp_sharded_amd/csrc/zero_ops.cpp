@@ -582,8 +582,64 @@ zero_status zero_scaled_unpack(const uint8_t* codes, int64_t codes_stride, const
                        table("out", out, rows, width, out_stride, type_bytes(t), true)};
     if (const zero_status s = check_arrays(a, 3, who)) return s;
     if (const zero_status s = check_place(a, 3, stream, who)) return s;
-    const zo::ScaledUnpack u{codes, exps, out, rows, width, codes_stride, exps_stride, out_stride, 0, square != 0};
+    const zo::ScaledUnpack u{codes, exps, out, rows, width, codes_stride, exps_stride, out_stride, 0, 0, square != 0};
     const hipError_t err = zo::scaled_unpack(u, t, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
+static zero_status check_product_sizes(int64_t m, int64_t n, int64_t k, const char* who)
+{
+    if (m < 0 || n < 0 || k < 0) return fail(ZERO_ERR_INVALID_ARG, "%s: m, n and k must be >= 0", who);
+    if (m > kMaxGrid || n > kMaxGrid || (n > 0 && m > ((int64_t)1 << 40) / n))
+        return fail(ZERO_ERR_UNSUPPORTED, "%s: m or n above 2^31 - 1, or m * n above 2^40", who);
+    if (k > (1 << 22)) return fail(ZERO_ERR_UNSUPPORTED, "%s: k above 2^22", who);
+    return ZERO_OK;
+}
+
+zero_status zero_scaled_product_workspace(int64_t m, int64_t n, int64_t k, zero_lp_dtype type, int64_t* bytes)
+{
+    const char* who = "zero_scaled_product_workspace";
+    if (!bytes) return fail(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+    const int32_t t = enum_value(type);
+    if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
+    if (const zero_status s = check_product_sizes(m, n, k, who)) return s;
+    *bytes = zo::product_plan(m, n, k, t).bytes;
+    return ZERO_OK;
+}
+
+zero_status zero_scaled_product(const zero_scaled_product_desc* d, const uint8_t* a, const uint8_t* a_exps, const uint8_t* b,
+                                const uint8_t* b_exps, const void* bias, void* out, void* workspace, int64_t workspace_bytes,
+                                void* stream)
+{
+    const char* who = "zero_scaled_product";
+    if (!d) return fail(ZERO_ERR_INVALID_ARG, "%s: desc is NULL", who);
+    const int32_t t = enum_value(d->type);
+    if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
+    const int64_t m = d->m, n = d->n, k = d->k;
+    if (const zero_status s = check_product_sizes(m, n, k, who)) return s;
+    if (d->b_square != 0 && d->b_square != 1) return fail(ZERO_ERR_INVALID_ARG, "%s: b_square must be 0 or 1", who);
+    if (m == 0 || n == 0) return ZERO_OK;
+    const bool square = d->b_square != 0;
+    if (!out || (k > 0 && (!a || !a_exps || !b || !b_exps))) return fail(ZERO_ERR_INVALID_ARG, "%s: a, a_exps, b, b_exps or out is NULL", who);
+    if (const zero_status s = check_scaled_strides(d->a_stride, d->a_exps_stride, m, k, false, "a", "a_exps", who)) return s;
+    if (const zero_status s = check_scaled_strides(d->b_stride, d->b_exps_stride, n, k, square, "b", "b_exps", who)) return s;
+    if (const zero_status s = check_stride(d->out_stride, m, n, "out", who)) return s;
+    if (d->a_exps_stride > (1 << 22) || d->b_exps_stride > (1 << 22))
+        return fail(ZERO_ERR_UNSUPPORTED, "%s: a stride of exponents above 2^22", who);
+    const zo::ProductPlan plan = zo::product_plan(m, n, k, t);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %lld are needed", who,
+                    (long long)(workspace ? workspace_bytes : 0), (long long)plan.bytes);
+    const int e = type_bytes(t);
+    const Array arrays[] = {table("a", a, m, k, d->a_stride, 1, false), exponents("a_exps", a_exps, m, k, d->a_exps_stride, false, false),
+                            table("b", b, n, k, d->b_stride, 1, false), exponents("b_exps", b_exps, n, k, d->b_exps_stride, square, false),
+                            flat("bias", bias, (size_t)n * e, e, false), table("out", out, m, n, d->out_stride, e, true),
+                            flat("workspace", workspace, (size_t)plan.bytes, 256, true)};
+    if (const zero_status s = check_arrays(arrays, 7, who)) return s;
+    if (const zero_status s = check_place(arrays, 7, stream, who)) return s;
+    const zo::ScaledProduct p{a, a_exps, b, b_exps, bias, out, static_cast<char*>(workspace), d->a_stride, d->a_exps_stride, d->b_stride,
+                              d->b_exps_stride, d->out_stride, square};
+    const hipError_t err = zo::scaled_product(p, plan, t, static_cast<hipStream_t>(stream));
     return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
 }
 

@@ -1,5 +1,5 @@
 """The training operators of libzeroops.so (include/zero_ops.h): layer norm, RMS norm with
-the residual's addition, packing to 8 bits with scales, the softmax cross entropy over a
+the residual's addition, packing to 8 bits with scales and the product of what is packed, the softmax cross entropy over a
 vocabulary with its gradients, and AdamW over many tensors with moments in 32 or 8 bits.
 
 A thin ctypes binding, as the package's binding of libzeroshard.so is: functions
@@ -27,7 +27,7 @@ _ptr = ctypes.POINTER
 OPS_SYMBOLS = (
     "zero_layernorm_forward", "zero_layernorm_workspace", "zero_layernorm_backward",
     "zero_rmsnorm_forward", "zero_rmsnorm_workspace", "zero_rmsnorm_backward", "zero_scaled_pack",
-    "zero_scaled_unpack", "zero_vocab_loss_workspace", "zero_vocab_loss", "zero_adamw_init", "zero_adamw_set_grads",
+    "zero_scaled_unpack", "zero_scaled_product_workspace", "zero_scaled_product", "zero_vocab_loss_workspace", "zero_vocab_loss", "zero_adamw_init", "zero_adamw_set_grads",
     "zero_adamw_step", "zero_adamw_result", "zero_adamw_get_counters", "zero_adamw_set_counters",
     "zero_adamw_destroy", "zero_moments_pack", "zero_moments_unpack", "zero_ops_last_error",
     "zero_ops_abi_version",
@@ -46,6 +46,12 @@ class ZeroRmsnormDesc(ctypes.Structure):
 class ZeroRmsnormGradDesc(ctypes.Structure):
     _fields_ = [("rows", _i64), ("width", _i64), ("type", ctypes.c_int), ("affine", ctypes.c_int),
                 ("dy_stride", _i64), ("h_stride", _i64), ("dh_stride", _i64), ("dx_stride", _i64)]
+
+
+class ZeroScaledProductDesc(ctypes.Structure):
+    _fields_ = [("m", _i64), ("n", _i64), ("k", _i64), ("type", ctypes.c_int), ("b_square", _i32),
+                ("a_stride", _i64), ("a_exps_stride", _i64), ("b_stride", _i64), ("b_exps_stride", _i64),
+                ("out_stride", _i64)]
 
 
 class ZeroVocabLossDesc(ctypes.Structure):
@@ -92,6 +98,9 @@ def lib() -> ctypes.CDLL:
                                        _vp, _i64, _vp, _i64, _vp]
         L.zero_scaled_unpack.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _i32, ctypes.c_int, _vp, _i64,
                                          _vp]
+        L.zero_scaled_product_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, _ptr(_i64)]
+        L.zero_scaled_product.argtypes = [_ptr(ZeroScaledProductDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _i64, _vp]
         L.zero_vocab_loss_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, _ptr(_i64)]
         L.zero_vocab_loss.argtypes = [_ptr(ZeroVocabLossDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _i64, _vp]
@@ -156,6 +165,13 @@ def _type_of(name: str, t) -> int:
     if code is None:
         raise TypeError(f"{name}: expected float16, bfloat16 or float32, got {t.dtype}")
     return code
+
+
+def _code(dtype) -> int:
+    torch or _load()
+    if dtype not in _CODES:
+        raise TypeError(f"expected float16, bfloat16 or float32, got {dtype}")
+    return _CODES[dtype]
 
 
 def _tensor(name: str, t, dtype) -> None:
@@ -369,6 +385,35 @@ def zero_scaled_unpack(codes, exps, out, *, stream=None) -> None:
     op, os_ = _rows("out", out, None, rows, width)
     _check(lib().zero_scaled_unpack(cp, cs, ep, es, rows, width, int(bool(square)), _type_of("out", out), op, os_,
                                     _current(stream)), "zero_scaled_unpack")
+
+
+def zero_scaled_product_workspace(m: int, n: int, k: int, dtype=None) -> int:
+    """Bytes of workspace for zero_scaled_product with results of the dtype (None: of any)."""
+    most = 0
+    for t in (ZERO_FP32, ZERO_BF16) if dtype is None else (_code(dtype),):
+        out = _i64()
+        _check(lib().zero_scaled_product_workspace(m, n, k, t, ctypes.byref(out)), "zero_scaled_product_workspace")
+        most = max(most, out.value)
+    return most
+
+
+def zero_scaled_product(a, a_exps, b, b_exps, out, bias=None, workspace=None, *, stream=None) -> None:
+    """out [m, n] = A B^T (+ bias [n], of out's type) for packed A [m, k] (scales by rows) and B
+    [n, k] (scales by rows or squares).  workspace: uint8, zero_scaled_product_workspace bytes."""
+    torch or _load()
+    (m, k), (n, _) = _matrix("a", a), _matrix("b", b)
+    d = ZeroScaledProductDesc(m=m, n=n, k=k, type=_type_of("out", out))
+    ap, d.a_stride = _rows("a", a, torch.float8_e4m3fn, m, k)
+    bp, d.b_stride = _rows("b", b, torch.float8_e4m3fn, n, k)
+    aep, d.a_exps_stride, form = _exps("a_exps", a_exps, m, k)
+    if form:
+        raise ValueError("a_exps: expected a scale for every 128 elements of a row")
+    bep, d.b_exps_stride, form = _exps("b_exps", b_exps, n, k)
+    d.b_square = int(bool(form))
+    op, d.out_stride = _rows("out", out, out.dtype, m, n)
+    sp, sn = _space(workspace)
+    _check(lib().zero_scaled_product(ctypes.byref(d), ap, aep, bp, bep, _flat("bias", bias, out.dtype, n), op, sp, sn,
+                                     _current(stream)), "zero_scaled_product")
 
 
 # ------------------------------------------------------------------ vocabulary loss
