@@ -8,6 +8,8 @@
  *    of what is packed so;
  *  - softmax cross entropy over a vocabulary, from hidden states and the output
  *    weight, with both gradients under the loss scale and no logits in memory;
+ *  - log probabilities of given tokens with entropy and top alternatives, from hidden states
+ *    and the output weight, and their gradients;
  *  - AdamW over the tensors of a model at once, with moments in 32 or in 8 bits.
  * The gradients that the first two write are what a rank contributes to
  * zero_bucket_reduce (in the storage format, carrying the loss scale), or what
@@ -250,6 +252,77 @@ zero_status zero_vocab_loss(const zero_vocab_loss_desc* desc, const void* hidden
                             const int64_t* targets, float* losses, float* lse, float* loss,
                             void* dhidden, void* dweight, void* workspace, int64_t workspace_bytes,
                             void* stream);
+
+/* ------------------------------------------------------------------ log probabilities
+ *
+ * hidden [tokens][width] and weight [vocab][width] of one 2-byte type, ids int64, one a row:
+ *     z = hidden weight^T ;  lse_n = log(sum_v exp(z_nv)) ;  p = exp(z - lse)
+ *     logprobs_n = z_n,id - lse_n         (0 where the id is ignore_index, NaN where it is
+ *                                          another outside [0, vocab))
+ *     entropy_n = -sum_v p_nv log(p_nv)
+ *     top_ids, top_logprobs [tokens][top]: the ids of the `top` largest z of a row in their
+ *         order, of equal ones the lower id first, and z - lse of each; NaN ranks last
+ * in fp32.  ids and logprobs are both given or both NULL, top_ids and top_logprobs where top > 0;
+ * entropy may be NULL.  lse, entropy and alternatives are every row's, whatever its id.
+ * tokens = 0 does nothing.  A row whose logits are all -infinity has lse -infinity and
+ * NaN for the rest; one with a logit of +infinity or NaN has NaN.
+ * Tokens are taken max_tokens at a time (0: 8192), with the workspace's size in proportion
+ * (with alternatives: 4 bytes for each of a chunk's logits).
+ * Performance: as zero_vocab_loss's operands.
+ */
+typedef struct {
+    int64_t tokens, vocab, width;
+    zero_lp_dtype type;          /* ZERO_FP16 or ZERO_BF16 */
+    int32_t top;                 /* 0 to 64, and at most vocab */
+    int64_t max_tokens;
+    int64_t ignore_index;
+    int64_t hidden_stride, weight_stride; /* elements a row */
+} zero_token_logprobs_desc;
+
+/* Bytes of workspace (256-byte aligned) for these sizes, of zero_token_logprobs (gradient = 0)
+ * or of zero_token_logprobs_backward (1: top is not looked at).  A workspace for several counts
+ * of tokens is as large as the largest of their answers. */
+zero_status zero_token_logprobs_workspace(int64_t tokens, int64_t vocab, int64_t width,
+                                          int64_t max_tokens, int32_t top, int32_t gradient,
+                                          int64_t* bytes);
+
+/* Errors: INVALID_ARG (NULL or misaligned arrays, one of a pair without the other, sizes < 0,
+ * vocab or width < 1, strides < width, max_tokens outside [0, 65535], top outside [0, 64] or above
+ * vocab, workspace too small, overlaps), UNSUPPORTED (ZERO_FP32; width > 2^20, vocab > 2^21 -
+ * 64, tokens > 2^31 - 1), HIP. */
+zero_status zero_token_logprobs(const zero_token_logprobs_desc* desc, const void* hidden,
+                                const void* weight, const int64_t* ids, float* logprobs, float* lse,
+                                float* entropy, int64_t* top_ids, float* top_logprobs,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The gradients of sum(dlogprobs * logprobs) + sum(dentropy * entropy), with the forward pass's
+ * lse and entropy:
+ *     G_nv = dlogprobs_n * ([v = id_n] - p_nv) - dentropy_n * p_nv * (log(p_nv) + entropy_n)
+ *     dhidden = G weight ;  dweight = G^T hidden
+ * dentropy may be NULL (then entropy may be too).  dlogprobs of a row whose id is ignore_index is not
+ * used; a row with neither gradient enters nothing, whatever its hidden state holds.  A row
+ * whose id is another outside [0, vocab) has NaN gradients.  Both results are written, not added to,
+ * and carry what scale dlogprobs and dentropy carry; dweight is zeros with tokens = 0.
+ * G is held in 2 bytes between the products, with the power of two that brings the largest row's
+ * |dlogprobs| + |dentropy| (1 + log vocab) to the top of the range: in fp16 entries below 2^-39 of
+ * that are lost.
+ * Errors: as zero_token_logprobs.
+ */
+typedef struct {
+    int64_t tokens, vocab, width;
+    zero_lp_dtype type;
+    int64_t max_tokens;
+    int64_t ignore_index;
+    int64_t hidden_stride, weight_stride, dhidden_stride, dweight_stride;
+} zero_token_logprobs_grad_desc;
+
+zero_status zero_token_logprobs_backward(const zero_token_logprobs_grad_desc* desc,
+                                         const void* hidden, const void* weight, const int64_t* ids,
+                                         const float* lse, const float* entropy,
+                                         const float* dlogprobs, const float* dentropy,
+                                         void* dhidden, void* dweight, void* workspace,
+                                         int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ AdamW over tensors
  *

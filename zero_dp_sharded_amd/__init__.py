@@ -512,4 +512,5 @@ from .ops import (AdamWTensor, zero_adamw_destroy, zero_adamw_get_counters,  # n
                   zero_moments_unpack, zero_ops_abi_version, zero_ops_last_error,
                   zero_rmsnorm_backward, zero_rmsnorm_forward, zero_rmsnorm_workspace,
                   zero_scaled_pack, zero_scaled_product, zero_scaled_product_workspace,
-                  zero_scaled_unpack, zero_vocab_loss, zero_vocab_loss_workspace)
+                  zero_scaled_unpack, zero_token_logprobs, zero_token_logprobs_backward,
+                  zero_token_logprobs_workspace, zero_vocab_loss, zero_vocab_loss_workspace)

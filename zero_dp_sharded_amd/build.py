@@ -27,8 +27,8 @@ LIB = os.path.join(HERE, "libzeroshard.so")
 SOURCES = ["zero_kernels.hip", "zero_shard.cpp", "zero_state_bytes.cpp"]
 # the training operators (include/zero_ops.h)
 OPS_LIB = os.path.join(HERE, "libzeroops.so")
-OPS_SOURCES = ["ops_norm.hip", "ops_rms.hip", "ops_pack.hip", "ops_product.hip", "ops_loss.hip", "ops_adamw.hip",
-               "zero_ops.cpp"]
+OPS_SOURCES = ["ops_norm.hip", "ops_rms.hip", "ops_pack.hip", "ops_product.hip", "ops_loss.hip", "ops_logprobs.hip",
+               "ops_adamw.hip", "zero_ops.cpp"]
 # benchmark helper: plain HBM copy (ceiling and counter calibration)
 COPY_LIB = os.path.join(HERE, "libhbmcopy.so")
 COPY_SOURCES = ["hbm_copy.hip"]

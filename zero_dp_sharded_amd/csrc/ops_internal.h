@@ -159,6 +159,73 @@ struct Loss {
 LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chunk, bool gradient);
 hipError_t vocab_loss(const Loss& a, const LossPlan& p, int type, hipStream_t s);
 
+struct VocabChunk {            // of tokens, whose logits' gradients are there
+    const void* g;             // as the plan says
+    const void* kept;          // their hidden states, rows of the plan's width_ld
+    const void* weight;
+    int64_t weight_ld;
+    void* dhidden;             // the chunk's
+    void* dweight;
+    int64_t dhidden_stride, dweight_stride;
+    const float* alpha;        // factor of the products' results
+    char* space;
+    int64_t n;
+    bool first, last;          // of the chunks
+};
+
+hipError_t vocab_gradients(const VocabChunk& c, const LossPlan& p, int type, hipStream_t s);
+
+// ------------------------------------------------------------------ log probabilities
+
+struct LogprobPlan {           // what a call's sizes settle
+    int64_t tokens, vocab, width;
+    int64_t chunk, vocab_ld, pieces, width_ld;     // as the loss's
+    TileChoice tile;
+    int top;
+    int64_t off_given, off_stats, off_weighted, off_logits, off_hidden, off_weight;
+    int64_t bytes;
+};
+
+struct Logprobs {
+    const void* hidden;
+    const void* weight;
+    const int64_t* tokens;     // NULL: none given, and no logprobs
+    float* logprobs;
+    float* lse;
+    float* entropy;            // or NULL
+    int64_t* top_ids;
+    float* top_logprobs;
+    char* space;
+    int64_t hidden_stride, weight_stride, ignore_index;
+};
+
+struct LogprobGradPlan {
+    LossPlan loss;             // the products'
+    int64_t off_rows;
+    int64_t bytes;
+};
+
+struct LogprobsGrad {
+    const void* hidden;
+    const void* weight;
+    const int64_t* tokens;
+    const float* lse;
+    const float* entropy;
+    const float* dlogprobs;
+    const float* dentropy;     // or NULL
+    void* dhidden;
+    void* dweight;
+    char* space;
+    int64_t hidden_stride, weight_stride, dhidden_stride, dweight_stride, ignore_index;
+};
+
+constexpr int kMostAlternatives = 64;
+
+LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chunk, int top);
+LogprobGradPlan logprob_grad_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chunk);
+hipError_t logprobs_forward(const Logprobs& a, const LogprobPlan& p, int type, hipStream_t s);
+hipError_t logprobs_backward(const LogprobsGrad& a, const LogprobGradPlan& p, int type, hipStream_t s);
+
 // ------------------------------------------------------------------ AdamW over tensors
 
 constexpr int kStateBlock = 256;       // elements that share an exponent (8-bit states)

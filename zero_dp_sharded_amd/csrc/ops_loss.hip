@@ -31,46 +31,10 @@
 #include "ops_common.h"
 #include "ops_gemm.h"
 #include "ops_internal.h"
+#include "ops_vocab.h"
 
 namespace zo {
 namespace {
-
-constexpr int64_t kLastCache = 256 << 20;
-constexpr float kLog2e = 1.44269504088896340736f;
-template <typename T> constexpr float kHoldLog2 = 32.0f;        // factor of what is held
-template <> constexpr float kHoldLog2<_Float16> = 15.0f;
-template <typename T> constexpr float kHold = (float)(1ull << (int)kHoldLog2<T>);
-
-// The n-th tile of those that die `die` of 8 takes.  Workgroups go round the dies;
-// each die gets a run of tiles that lie together (8 tiles of i by all of j, column by
-// column), so that its L2 serves the operands' pieces to the tiles that share them.
-constexpr uint32_t kDies = 8;
-
-__device__ __forceinline__ uint32_t tiles_of(uint32_t die, uint32_t all)
-{
-    return all / kDies + (die < all % kDies ? 1 : 0);
-}
-
-__device__ __forceinline__ void tile_of(uint32_t die, uint32_t at, uint32_t ti, uint32_t tj, int64_t& i, int64_t& j)
-{
-    constexpr uint32_t kGroup = 8;
-    const uint32_t q = ti * tj / kDies, r = ti * tj % kDies;
-    const uint32_t n = die * q + (die < r ? die : r) + at;
-    const uint32_t per = kGroup * tj, g = n / per;
-    const uint32_t first = g * kGroup;
-    const uint32_t high = ti - first < kGroup ? ti - first : kGroup;
-    // (the same for all lanes: kept where that costs no vector register)
-    i = __builtin_amdgcn_readfirstlane(first + (n - g * per) % high);
-    j = __builtin_amdgcn_readfirstlane((n - g * per) / high);
-}
-
-template <typename T>
-__device__ __forceinline__ T to_type(float x)
-{
-    return static_cast<T>(x);
-}
-
-__device__ __forceinline__ uint32_t lds_address(char* smem) { return (uint32_t)(uintptr_t)(ZO_LDS char*)smem; }
 
 // ------------------------------------------------------------------ the logits
 
@@ -481,53 +445,10 @@ __global__ __launch_bounds__(256) void join_splits_kernel(const float* part, int
     store_vec<T, W>(out + at / cols * out_ld + at % cols, y);
 }
 
-// Rows of any stride and alignment to rows of ld, a multiple of 8, zeros behind the
-// width: of one array or, from workgroup `first` on, of another.
-template <typename T>
-struct Repack {
-    const T* x;
-    T* out;
-    int64_t stride, rows;
-};
-
-template <typename T>
-__global__ __launch_bounds__(256) void repack_kernel(Repack<T> a, Repack<T> b, int64_t base, int64_t first, int64_t width,
-                                                     int64_t ld)
-{
-    const int64_t group = base + blockIdx.x;
-    const bool second = group >= first;
-    const Repack<T> r = second ? b : a;
-    const int64_t at = ((group - (second ? first : 0)) * 256 + threadIdx.x) * 8;
-    if (at >= r.rows * ld) return;
-    const int64_t i = at / ld, c = at % ld;
-    const T* x = r.x + i * r.stride + c;
-    vec_t<T, 8> y;
-    if (c + 8 <= width) {
-        y = load_vec<T, 8>(x);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = c + k < width ? x[k] : to_type<T>(0.0f);
-    }
-    *reinterpret_cast<vec_t<T, 8>*>(r.out + at) = y;
-}
-
 // ------------------------------------------------------------------ launches
 //
 // (Of all of them only the copies could pass a launch's work-items: a product's tiles are
 // fewer than 2^22, by what memory its operands take, and the rest goes by chunks of tokens.)
-
-// What the products' loads need of an address and a stride.
-bool loads_as_it_is(const void* p, int64_t stride)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && stride % 2 == 0 && stride <= (1 << 21);
-}
-
-// A kernel's LDS beyond 64 KiB is asked for once.
-template <typename K>
-hipError_t allow(K kernel, int lds)
-{
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-}
 
 template <typename T, int NI, int NJ>
 hipError_t logits(LogitsArgs l, hipStream_t s)
@@ -563,6 +484,63 @@ hipError_t grad(const GradArgs& g, const TileChoice& c, hipStream_t s)
 {
     if (c.ni == 2) return grad<T, LP, 2, 4>(g, s);
     return c.nj == 4 ? grad<T, LP, 8, 4>(g, s) : grad<T, LP, 8, 5>(g, s);
+}
+
+// Both gradients of a chunk of tokens from its rows of G.
+template <typename T>
+hipError_t gradients(const VocabChunk& c, const LossPlan& p, hipStream_t s)
+{
+    const int64_t n = c.n, held = p.pairs ? pair_rows(n) : n;        // rows of G
+    GradArgs g{};
+    g.alpha = c.alpha;
+    g.cols = p.width;
+    if (n == 0) {                          // sums over no tokens
+        g.p = Operand{c.weight, p.vocab_ld, p.vocab_ld, 0};
+        g.q = Operand{c.weight, c.weight_ld, p.width, 0};
+        g.rows = p.vocab;
+        g.splits = 1;
+        g.out = c.dweight;
+        g.out_ld = c.dweight_stride;
+        return grad<T, kOuter>(g, p.weight_tile, s);
+    }
+    // A product, in parts of its depth where that fills the card.
+    auto product = [&](auto layout, int splits, const TileChoice& tile) {
+        constexpr Layout LP = decltype(layout)::value;
+        g.splits = splits;
+        g.part = splits > 1 ? reinterpret_cast<float*>(c.space + p.off_split) : nullptr;
+        const hipError_t err = grad<T, LP>(g, tile, s);
+        if (err != hipSuccess || splits == 1) return err;
+        T* out = static_cast<T*>(g.out);
+        const int64_t all = g.rows * g.cols;
+        if (g.cols % 4 == 0)
+            join_splits_kernel<T, 4><<<dim3((unsigned)ceil_div(all, 1024)), 256, 0, s>>>(g.part, splits, g.rows, g.cols, c.alpha, out, g.out_ld);
+        else
+            join_splits_kernel<T, 1><<<dim3((unsigned)ceil_div(all, 256)), 256, 0, s>>>(g.part, splits, g.rows, g.cols, c.alpha, out, g.out_ld);
+        return hipSuccess;
+    };
+    // dH = G W: k runs over the vocabulary
+    g.p = Operand{c.g, p.vocab_ld, held, p.vocab_ld};
+    g.q = Operand{c.weight, c.weight_ld, p.width, p.vocab};
+    g.rows = n;
+    g.pairs = p.pairs;
+    g.steps = p.vocab_ld / kDeep;
+    g.out = c.dhidden;
+    g.out_ld = c.dhidden_stride;
+    const hipError_t e = product(std::integral_constant<Layout, kInner>{}, p.hidden_splits, p.hidden_tile);
+    if (e != hipSuccess) return e;
+    // dW = G^T H: k runs over the chunk's tokens; with several chunks the sum
+    // stays in fp32 until the last
+    g.p = Operand{c.g, p.vocab_ld, p.vocab_ld, held, p.pairs ? n : 0};
+    g.q = Operand{c.kept, p.width_ld, p.width_ld, n, p.pairs ? n : 0, true};
+    g.rows = p.vocab;
+    g.pairs = 0;
+    g.steps = ceil_div(held, kDeep);
+    g.out = c.dweight;
+    g.out_ld = c.dweight_stride;
+    g.sum = reinterpret_cast<float*>(c.space + p.off_sum);
+    g.sum_in = !c.first;
+    g.sum_out = !c.last;
+    return product(std::integral_constant<Layout, kOuter>{}, p.weight_splits, p.weight_tile);
 }
 
 template <typename T>
@@ -605,18 +583,8 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
     hipError_t e = hipSuccess;
     if (p.tokens == 0) {
         total(a.loss);
-        if (gradient) {                    // a sum over no tokens
-            GradArgs g{};
-            g.p = Operand{w, p.vocab_ld, p.vocab_ld, 0};
-            g.q = Operand{w, w_ld, p.width, 0};
-            g.alpha = alpha;
-            g.rows = p.vocab;
-            g.cols = p.width;
-            g.splits = 1;
-            g.out = a.dweight;
-            g.out_ld = a.dweight_stride;
-            e = grad<T, kOuter>(g, p.weight_tile, s);
-        }
+        if (gradient)
+            e = gradients<T>(VocabChunk{exps, nullptr, w, w_ld, nullptr, a.dweight, 0, a.dweight_stride, alpha, a.space, 0, true, true}, p, s);
         return e != hipSuccess ? e : hipGetLastError();
     }
     const Operand ow{w, w_ld, p.vocab, p.width_ld};
@@ -624,7 +592,6 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         const int64_t n = p.tokens - n0 < p.chunk ? p.tokens - n0 : p.chunk;
         const bool last = n0 + n == p.tokens;
         const Operand oh{h + n0 * h_ld, h_ld, n, p.width_ld};
-        const int64_t held = p.pairs ? pair_rows(n) : n;        // rows of G
         const LogitsArgs l{oh, ow, a.targets + n0, target_logit, stats, exps, p.pairs, n, p.vocab, p.vocab_ld, p.pieces, 0, 0};
         if (p.logits_tile.ni == 2) e = logits<T, 2, 4>(l, s);
         else if (p.logits_tile.nj == 4) e = logits<T, 8, 4>(l, s);
@@ -644,47 +611,8 @@ hipError_t run(const Loss& a, const LossPlan& p, hipStream_t s)
         else join_kernel<T, 5, false><<<joins, 256, 0, s>>>(j);
         if (n0 == 0 || last) total(last ? a.loss : nullptr);
         if (!gradient) continue;
-        GradArgs g{};
-        g.alpha = alpha;
-        g.cols = p.width;
-        // A product, in parts of its depth where that fills the card.
-        auto product = [&](auto layout, int splits, const TileChoice& tile) {
-            constexpr Layout LP = decltype(layout)::value;
-            g.splits = splits;
-            g.part = splits > 1 ? reinterpret_cast<float*>(a.space + p.off_split) : nullptr;
-            const hipError_t err = grad<T, LP>(g, tile, s);
-            if (err != hipSuccess || splits == 1) return err;
-            T* out = static_cast<T*>(g.out);
-            const int64_t all = g.rows * g.cols;
-            if (g.cols % 4 == 0)
-                join_splits_kernel<T, 4><<<dim3((unsigned)ceil_div(all, 1024)), 256, 0, s>>>(g.part, splits, g.rows, g.cols, alpha, out, g.out_ld);
-            else
-                join_splits_kernel<T, 1><<<dim3((unsigned)ceil_div(all, 256)), 256, 0, s>>>(g.part, splits, g.rows, g.cols, alpha, out, g.out_ld);
-            return hipSuccess;
-        };
-        // dH = G W: k runs over the vocabulary
-        g.p = Operand{exps, p.vocab_ld, held, p.vocab_ld};
-        g.q = Operand{w, w_ld, p.width, p.vocab};
-        g.rows = n;
-        g.pairs = p.pairs;
-        g.steps = p.vocab_ld / kDeep;
-        g.out = static_cast<T*>(a.dhidden) + n0 * a.dhidden_stride;
-        g.out_ld = a.dhidden_stride;
-        e = product(std::integral_constant<Layout, kInner>{}, p.hidden_splits, p.hidden_tile);
-        if (e != hipSuccess) return e;
-        // dW = G^T H: k runs over the chunk's tokens; with several chunks the sum
-        // stays in fp32 until the last
-        g.p = Operand{exps, p.vocab_ld, p.vocab_ld, held, p.pairs ? n : 0};
-        g.q = Operand{kept, p.width_ld, p.width_ld, n, p.pairs ? n : 0, true};
-        g.rows = p.vocab;
-        g.pairs = 0;
-        g.steps = ceil_div(held, kDeep);
-        g.out = a.dweight;
-        g.out_ld = a.dweight_stride;
-        g.sum = reinterpret_cast<float*>(a.space + p.off_sum);
-        g.sum_in = n0 > 0;
-        g.sum_out = !last;
-        e = product(std::integral_constant<Layout, kOuter>{}, p.weight_splits, p.weight_tile);
+        e = gradients<T>(VocabChunk{exps, kept, w, w_ld, static_cast<T*>(a.dhidden) + n0 * a.dhidden_stride, a.dweight, a.dhidden_stride,
+                                    a.dweight_stride, alpha, a.space, n, n0 == 0, last}, p, s);
     }
     return e != hipSuccess ? e : hipGetLastError();
 }
@@ -777,6 +705,11 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t max_chu
     p.off_weight = take(vocab * p.width_ld * 2);
     p.bytes = at;
     return p;
+}
+
+hipError_t vocab_gradients(const VocabChunk& c, const LossPlan& p, int type, hipStream_t s)
+{
+    return type == 1 ? gradients<_Float16>(c, p, s) : gradients<__bf16>(c, p, s);
 }
 
 hipError_t vocab_loss(const Loss& a, const LossPlan& p, int type, hipStream_t s)

@@ -4,7 +4,7 @@
 // both; and backward, with the gradient dh that comes down the residual's way:
 //     xhat = h rstd ;  g = dy w ;  dx = rstd (g - xhat mean(g xhat)) + dh
 //     dw = sum_rows dy xhat
-// All of it in fp32; h, y and the results are rounded once.  The norm is of h as it is
+// All of it in fp32 (the sum of squares in 64 bits); h, y and the results are rounded once.  The norm is of h as it is
 // held: what the backward pass reads.
 //
 // Bound by memory, as the layer norm (ops_norm.hip), and laid out as it is: a row in
@@ -22,15 +22,15 @@ namespace {
 constexpr int64_t kCaches = 32 << 20;
 
 // Sum of x over the NW waves of a row, the same in each.
-template <int NW>
-__device__ __forceinline__ float row_sum(float x, float* sh)
+template <int NW, typename F>
+__device__ __forceinline__ F row_sum(F x, F* sh)
 {
     x = lanes_sum(x);
     if constexpr (NW > 1) {
         __syncthreads();                       // the last sums have been read
         if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
         __syncthreads();
-        x = 0.0f;
+        x = 0;
 #pragma unroll
         for (int k = 0; k < NW; ++k) x += sh[k];
     }
@@ -101,15 +101,9 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint8_t* exps, int64_t
     if (c % kScaleBlock == 0) exps[c / kScaleBlock] = (uint8_t)E;
 }
 
-// 1 / sqrt(q / width + eps) for the sum q of squares; where q passes fp32, by `again`, the
-// sum of (x 2^-80)^2, which stays below 2^120.
-template <typename F>
-__device__ __forceinline__ float rstd_of(float q, float width, float eps, F again)
-{
-    if (q < INFINITY) return 1.0f / sqrtf(q / width + eps);
-    if (q != q) return q;
-    return 0x1p-80f / sqrtf(again() / width);
-}
+// The sum of squares is in 64 bits: no square passes its range, and rstd is rounded once.  (A result in 8
+// bits changes by a whole step where y lies next to a middle: with fp32 sums twice as often.)
+__device__ __forceinline__ float rstd_of(double q, int64_t width, float eps) { return (float)(1.0 / sqrt(q / (double)width + (double)eps)); }
 
 // ------------------------------------------------------------------ forward
 
@@ -118,7 +112,7 @@ template <typename T, typename A, bool PAST, int NW, int K>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_forward_kernel(RmsForward a)
 {
     constexpr int W = Vec<T>::W;
-    __shared__ float sh[NW];
+    __shared__ double sh[NW];
     const int lane = NW == 1 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t row = NW == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
     if (row >= a.rows) return;
@@ -147,15 +141,12 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_forward_kernel(Rm
 #pragma unroll
             for (int e = 0; e < W; ++e) v[k][e] = (float)in[k][e];
     }
-    auto squares = [&](float by) {
-        float q = 0.0f;
+    double q = 0.0;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int e = 0; e < W; ++e) q = fmaf(v[k][e] * by, v[k][e] * by, q);
-        return row_sum<NW>(q, sh);
-    };
-    const float rstd = rstd_of(squares(1.0f), (float)a.width, a.eps, [&] { return squares(0x1p-80f); });
+        for (int e = 0; e < W; ++e) q = fma((double)v[k][e], (double)v[k][e], q);
+    const float rstd = rstd_of(row_sum<NW>(q, sh), a.width, a.eps);
     if (lane == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
     T* y = a.y != nullptr ? static_cast<T*>(a.y) + row * a.y_stride : nullptr;
 #pragma unroll
@@ -183,12 +174,12 @@ template <typename T, typename A, bool PAST>
 __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
 {
     constexpr int W = Vec<T>::W;
-    __shared__ float sh[16];
+    __shared__ double sh[16];
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const int64_t c0 = (int64_t)threadIdx.x * W, step = 1024 * W;
     const T* from = x;                         // h: x, or the sum
-    float q = 0.0f;
+    double q = 0.0;
     if (a.residual != nullptr) {
         const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
         T* h = static_cast<T*>(a.h) + row * a.h_stride;
@@ -198,7 +189,7 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 in[e] = static_cast<T>((float)in[e] + (float)add[e]);
-                q = fmaf((float)in[e], (float)in[e], q);
+                q = fma((double)(float)in[e], (double)(float)in[e], q);
             }
             store_raw<false, T, W>(h, c, a.width, in);       // (a lane reads back what it wrote)
         }
@@ -207,19 +198,10 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
             float v[W];
             load_part<T, W>(x, c, a.width, v);
 #pragma unroll
-            for (int e = 0; e < W; ++e) q = fmaf(v[e], v[e], q);
+            for (int e = 0; e < W; ++e) q = fma((double)v[e], (double)v[e], q);
         }
     }
-    const float rstd = rstd_of(row_sum<16>(q, sh), (float)a.width, a.eps, [&] {
-        float again = 0.0f;
-        for (int64_t c = c0; c < a.width; c += step) {
-            float v[W];
-            load_part<T, W>(from, c, a.width, v);
-#pragma unroll
-            for (int e = 0; e < W; ++e) again = fmaf(v[e] * 0x1p-80f, v[e] * 0x1p-80f, again);
-        }
-        return row_sum<16>(again, sh);
-    });
+    const float rstd = rstd_of(row_sum<16>(q, sh), a.width, a.eps);
     if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
     T* y = a.y != nullptr ? static_cast<T*>(a.y) + row * a.y_stride : nullptr;
     // (whole blocks: the lanes of one come to its codes together)

@@ -45,6 +45,24 @@ __device__ __forceinline__ float lanes_sum(float x)
     return from_bits(r[0]) + from_bits(r[1]);
 }
 
+__device__ __forceinline__ double lanes_sum(double x)
+{
+    auto moved = [](double x, auto move) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        return __builtin_bit_cast(double, (uint64_t)move((uint32_t)(u >> 32)) << 32 | move((uint32_t)u));
+    };
+    x += moved(x, [](uint32_t u) { return dpp<kXor1>(u); });
+    x += moved(x, [](uint32_t u) { return dpp<kXor2>(u); });
+    x += moved(x, [](uint32_t u) { return dpp<kHalfMirror>(u); });
+    x += moved(x, [](uint32_t u) { return dpp<kMirror>(u); });
+    const double a = moved(x, [](uint32_t u) { return (uint32_t)__builtin_amdgcn_permlane16_swap(u, u, false, false)[0]; });
+    const double b = moved(x, [](uint32_t u) { return (uint32_t)__builtin_amdgcn_permlane16_swap(u, u, false, false)[1]; });
+    x = a + b;
+    const double c = moved(x, [](uint32_t u) { return (uint32_t)__builtin_amdgcn_permlane32_swap(u, u, false, false)[0]; });
+    const double d = moved(x, [](uint32_t u) { return (uint32_t)__builtin_amdgcn_permlane32_swap(u, u, false, false)[1]; });
+    return c + d;
+}
+
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // Over LANES (16, 32 or 64) lanes that lie together, the same in each.

@@ -710,6 +710,98 @@ zero_status zero_vocab_loss(const zero_vocab_loss_desc* d, const void* hidden, c
     return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
 }
 
+zero_status zero_token_logprobs_workspace(int64_t tokens, int64_t vocab, int64_t width, int64_t max_tokens, int32_t top,
+                                          int32_t gradient, int64_t* bytes)
+{
+    const char* who = "zero_token_logprobs_workspace";
+    if (!bytes) return fail(ZERO_ERR_INVALID_ARG, "%s: bytes is NULL", who);
+    if (gradient != 0 && gradient != 1) return fail(ZERO_ERR_INVALID_ARG, "%s: gradient must be 0 or 1", who);
+    if (const zero_status s = check_loss_sizes(tokens, vocab, width, max_tokens, who)) return s;
+    if (!gradient && (top < 0 || top > zo::kMostAlternatives || top > vocab))
+        return fail(ZERO_ERR_INVALID_ARG, "%s: top outside [0, %d], or above vocab", who, zo::kMostAlternatives);
+    const int64_t most = max_tokens ? max_tokens : kDefaultTokens;
+    *bytes = gradient ? zo::logprob_grad_plan(tokens, vocab, width, most).bytes : zo::logprob_plan(tokens, vocab, width, most, top).bytes;
+    return ZERO_OK;
+}
+
+zero_status zero_token_logprobs(const zero_token_logprobs_desc* d, const void* hidden, const void* weight, const int64_t* ids,
+                                float* logprobs, float* lse, float* entropy, int64_t* top_ids, float* top_logprobs, void* workspace,
+                                int64_t workspace_bytes, void* stream)
+{
+    const char* who = "zero_token_logprobs";
+    if (!d) return fail(ZERO_ERR_INVALID_ARG, "%s: desc is NULL", who);
+    const int32_t t = enum_value(d->type);
+    if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
+    if (t == ZERO_FP32) return fail(ZERO_ERR_UNSUPPORTED, "%s: hidden states and weight are of a 2-byte type", who);
+    if (const zero_status s = check_loss_sizes(d->tokens, d->vocab, d->width, d->max_tokens, who)) return s;
+    if (d->top < 0 || d->top > zo::kMostAlternatives || d->top > d->vocab)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: top outside [0, %d], or above vocab", who, zo::kMostAlternatives);
+    if (d->tokens == 0) return ZERO_OK;
+    if (!hidden || !weight || !lse) return fail(ZERO_ERR_INVALID_ARG, "%s: hidden, weight or lse is NULL", who);
+    if ((ids != nullptr) != (logprobs != nullptr)) return fail(ZERO_ERR_INVALID_ARG, "%s: ids and logprobs are given both or neither (NULL)", who);
+    if ((top_ids != nullptr) != (d->top > 0) || (top_logprobs != nullptr) != (d->top > 0))
+        return fail(ZERO_ERR_INVALID_ARG, "%s: top_ids and top_logprobs go with top > 0, and only with it", who);
+    if (const zero_status s = check_stride(d->hidden_stride, d->tokens, d->width, "hidden", who)) return s;
+    if (const zero_status s = check_stride(d->weight_stride, d->vocab, d->width, "weight", who)) return s;
+    const zo::LogprobPlan plan = zo::logprob_plan(d->tokens, d->vocab, d->width, d->max_tokens ? d->max_tokens : kDefaultTokens, d->top);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %lld are needed", who,
+                    (long long)(workspace ? workspace_bytes : 0), (long long)plan.bytes);
+    const size_t n = (size_t)d->tokens;
+    const Array a[] = {table("hidden", hidden, d->tokens, d->width, d->hidden_stride, 2, false),
+                       table("weight", weight, d->vocab, d->width, d->weight_stride, 2, false),
+                       flat("ids", ids, n * 8, 8, false), flat("logprobs", logprobs, n * 4, 4, true), flat("lse", lse, n * 4, 4, true),
+                       flat("entropy", entropy, n * 4, 4, true), flat("top_ids", top_ids, n * d->top * 8, 8, true),
+                       flat("top_logprobs", top_logprobs, n * d->top * 4, 4, true), flat("workspace", workspace, (size_t)plan.bytes, 256, true)};
+    if (const zero_status s = check_arrays(a, 9, who)) return s;
+    if (const zero_status s = check_place(a, 9, stream, who)) return s;
+    const zo::Logprobs l{hidden, weight, ids, logprobs, lse, entropy, top_ids, top_logprobs, static_cast<char*>(workspace),
+                         d->hidden_stride, d->weight_stride, d->ignore_index};
+    const hipError_t err = zo::logprobs_forward(l, plan, t, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
+zero_status zero_token_logprobs_backward(const zero_token_logprobs_grad_desc* d, const void* hidden, const void* weight,
+                                         const int64_t* ids, const float* lse, const float* entropy, const float* dlogprobs,
+                                         const float* dentropy, void* dhidden, void* dweight, void* workspace, int64_t workspace_bytes,
+                                         void* stream)
+{
+    const char* who = "zero_token_logprobs_backward";
+    if (!d) return fail(ZERO_ERR_INVALID_ARG, "%s: desc is NULL", who);
+    const int32_t t = enum_value(d->type);
+    if (!known_type(t)) return fail(ZERO_ERR_INVALID_ARG, "%s: unknown type %d", who, (int)t);
+    if (t == ZERO_FP32) return fail(ZERO_ERR_UNSUPPORTED, "%s: hidden states and weight are of a 2-byte type", who);
+    if (const zero_status s = check_loss_sizes(d->tokens, d->vocab, d->width, d->max_tokens, who)) return s;
+    const bool some = d->tokens > 0;
+    if (!weight || !dweight || (some && (!hidden || !ids || !lse || !dlogprobs || !dhidden)))
+        return fail(ZERO_ERR_INVALID_ARG, "%s: hidden, weight, ids, lse, dlogprobs, dhidden or dweight is NULL", who);
+    if (some && dentropy && !entropy) return fail(ZERO_ERR_INVALID_ARG, "%s: dentropy without entropy (NULL)", who);
+    if (some) {
+        if (const zero_status s = check_stride(d->hidden_stride, d->tokens, d->width, "hidden", who)) return s;
+        if (const zero_status s = check_stride(d->dhidden_stride, d->tokens, d->width, "dhidden", who)) return s;
+    }
+    if (const zero_status s = check_stride(d->weight_stride, d->vocab, d->width, "weight", who)) return s;
+    if (const zero_status s = check_stride(d->dweight_stride, d->vocab, d->width, "dweight", who)) return s;
+    const zo::LogprobGradPlan plan = zo::logprob_grad_plan(d->tokens, d->vocab, d->width, d->max_tokens ? d->max_tokens : kDefaultTokens);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(ZERO_ERR_INVALID_ARG, "%s: the workspace has %lld bytes, %lld are needed", who,
+                    (long long)(workspace ? workspace_bytes : 0), (long long)plan.bytes);
+    const size_t n = (size_t)d->tokens;
+    const Array a[] = {table("hidden", hidden, d->tokens, d->width, d->hidden_stride, 2, false),
+                       table("weight", weight, d->vocab, d->width, d->weight_stride, 2, false),
+                       flat("ids", ids, n * 8, 8, false), flat("lse", lse, n * 4, 4, false), flat("entropy", dentropy ? entropy : nullptr, n * 4, 4, false),
+                       flat("dlogprobs", dlogprobs, n * 4, 4, false), flat("dentropy", dentropy, n * 4, 4, false),
+                       table("dhidden", dhidden, d->tokens, d->width, d->dhidden_stride, 2, true),
+                       table("dweight", dweight, d->vocab, d->width, d->dweight_stride, 2, true),
+                       flat("workspace", workspace, (size_t)plan.bytes, 256, true)};
+    if (const zero_status s = check_arrays(a, 10, who)) return s;
+    if (const zero_status s = check_place(a, 10, stream, who)) return s;
+    const zo::LogprobsGrad l{hidden, weight, ids, lse, entropy, dlogprobs, dentropy, dhidden, dweight, static_cast<char*>(workspace),
+                             d->hidden_stride, d->weight_stride, d->dhidden_stride, d->dweight_stride, d->ignore_index};
+    const hipError_t err = zo::logprobs_backward(l, plan, t, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
+}
+
 zero_status zero_adamw_init(const zero_adamw_tensor* tensors, int32_t n, const zero_adam_hparams* hp,
                             const zero_loss_scale_cfg* ls, const zero_adamw_cfg* cfg, zero_adamw_t* out)
 {

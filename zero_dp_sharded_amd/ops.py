@@ -1,6 +1,7 @@
 """The training operators of libzeroops.so (include/zero_ops.h): layer norm, RMS norm with
 the residual's addition, packing to 8 bits with scales and the product of what is packed, the softmax cross entropy over a
-vocabulary with its gradients, and AdamW over many tensors with moments in 32 or 8 bits.
+vocabulary with its gradients, log probabilities of tokens with entropy and alternatives, and
+AdamW over many tensors with moments in 32 or 8 bits.
 
 A thin ctypes binding, as the package's binding of libzeroshard.so is: functions
 carry the C names, tensors become device pointers, strides and types, and the
@@ -27,7 +28,8 @@ _ptr = ctypes.POINTER
 OPS_SYMBOLS = (
     "zero_layernorm_forward", "zero_layernorm_workspace", "zero_layernorm_backward",
     "zero_rmsnorm_forward", "zero_rmsnorm_workspace", "zero_rmsnorm_backward", "zero_scaled_pack",
-    "zero_scaled_unpack", "zero_scaled_product_workspace", "zero_scaled_product", "zero_vocab_loss_workspace", "zero_vocab_loss", "zero_adamw_init", "zero_adamw_set_grads",
+    "zero_scaled_unpack", "zero_scaled_product_workspace", "zero_scaled_product", "zero_vocab_loss_workspace", "zero_vocab_loss", "zero_token_logprobs_workspace", "zero_token_logprobs",
+    "zero_token_logprobs_backward", "zero_adamw_init", "zero_adamw_set_grads",
     "zero_adamw_step", "zero_adamw_result", "zero_adamw_get_counters", "zero_adamw_set_counters",
     "zero_adamw_destroy", "zero_moments_pack", "zero_moments_unpack", "zero_ops_last_error",
     "zero_ops_abi_version",
@@ -59,6 +61,18 @@ class ZeroVocabLossDesc(ctypes.Structure):
                 ("max_tokens", _i64), ("ignore_index", _i64), ("hidden_stride", _i64),
                 ("weight_stride", _i64), ("dhidden_stride", _i64), ("dweight_stride", _i64),
                 ("grad_scale", _f64)]
+
+
+class ZeroTokenLogprobsDesc(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("vocab", _i64), ("width", _i64), ("type", ctypes.c_int), ("top", _i32),
+                ("max_tokens", _i64), ("ignore_index", _i64), ("hidden_stride", _i64),
+                ("weight_stride", _i64)]
+
+
+class ZeroTokenLogprobsGradDesc(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("vocab", _i64), ("width", _i64), ("type", ctypes.c_int),
+                ("max_tokens", _i64), ("ignore_index", _i64), ("hidden_stride", _i64),
+                ("weight_stride", _i64), ("dhidden_stride", _i64), ("dweight_stride", _i64)]
 
 
 class ZeroAdamwTensor(ctypes.Structure):
@@ -104,6 +118,11 @@ def lib() -> ctypes.CDLL:
         L.zero_vocab_loss_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, _ptr(_i64)]
         L.zero_vocab_loss.argtypes = [_ptr(ZeroVocabLossDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp, _i64, _vp]
+        L.zero_token_logprobs_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32, _ptr(_i64)]
+        L.zero_token_logprobs.argtypes = [_ptr(ZeroTokenLogprobsDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _vp, _i64, _vp]
+        L.zero_token_logprobs_backward.argtypes = [_ptr(ZeroTokenLogprobsGradDesc), _vp, _vp, _vp, _vp,
+                                                   _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
         L.zero_adamw_init.argtypes = [_ptr(ZeroAdamwTensor), _i32, _ptr(ZeroAdamHParams),
                                       _ptr(ZeroLossScaleCfg), _ptr(ZeroAdamwCfg), _ptr(_vp)]
         L.zero_adamw_set_grads.argtypes = [_vp, _ptr(_vp), _i32, _vp]
@@ -451,6 +470,63 @@ def zero_vocab_loss(hidden, weight, targets, losses, lse, loss, dhidden=None, dw
         _flat("losses", losses, torch.float32, tokens), _flat("lse", lse, torch.float32, tokens),
         _flat("loss", loss, torch.float32, 1), dhp, dwp, sp, sn, _current(stream)),
         "zero_vocab_loss")
+
+
+# ------------------------------------------------------------------ log probabilities
+
+def zero_token_logprobs_workspace(tokens: int, vocab: int, width: int, *, top: int = 0, gradient: bool = False,
+                                  max_tokens: int = 0) -> int:
+    """Bytes of workspace for zero_token_logprobs, or (gradient) zero_token_logprobs_backward."""
+    n = _i64()
+    _check(lib().zero_token_logprobs_workspace(tokens, vocab, width, max_tokens, top, int(gradient),
+                                               ctypes.byref(n)), "zero_token_logprobs_workspace")
+    return n.value
+
+
+def zero_token_logprobs(hidden, weight, ids, logprobs, lse, entropy=None, top_ids=None, top_logprobs=None,
+                        workspace=None, *, ignore_index: int = -100, max_tokens: int = 0, stream=None) -> None:
+    """Log probabilities of ids [tokens] (int64; with logprobs, or neither) under the softmax of
+    hidden [tokens, width] against weight [vocab, width], and lse [tokens]; where given, the rows'
+    entropy [tokens], and the ids (int64) and log probabilities [tokens, top] of their largest logits, the
+    lower id first where they are alike.  workspace: uint8, zero_token_logprobs_workspace bytes."""
+    torch or _load()
+    (tokens, width), (vocab, _) = _matrix("hidden", hidden), _matrix("weight", weight)
+    top = 0 if top_ids is None else _matrix("top_ids", top_ids)[1]
+    d = ZeroTokenLogprobsDesc(tokens=tokens, vocab=vocab, width=width, type=_type_of("hidden", hidden), top=top,
+                              max_tokens=max_tokens, ignore_index=ignore_index)
+    hp, d.hidden_stride = _rows("hidden", hidden, hidden.dtype, tokens, width)
+    wp, d.weight_stride = _rows("weight", weight, hidden.dtype, vocab, width)
+    for name, t in (("top_ids", top_ids), ("top_logprobs", top_logprobs)):
+        if t is not None and t.shape != (tokens, top):
+            raise ValueError(f"{name}: expected shape ({tokens}, {top}), got {tuple(t.shape)}")
+    sp, sn = _space(workspace)
+    _check(lib().zero_token_logprobs(
+        ctypes.byref(d), hp, wp, _flat("ids", ids, torch.int64, tokens),
+        _flat("logprobs", logprobs, torch.float32, tokens), _flat("lse", lse, torch.float32, tokens),
+        _flat("entropy", entropy, torch.float32, tokens), _flat("top_ids", top_ids, torch.int64, tokens * top),
+        _flat("top_logprobs", top_logprobs, torch.float32, tokens * top), sp, sn, _current(stream)),
+        "zero_token_logprobs")
+
+
+def zero_token_logprobs_backward(hidden, weight, ids, lse, entropy, dlogprobs, dentropy, dhidden, dweight,
+                                 workspace=None, *, ignore_index: int = -100, max_tokens: int = 0,
+                                 stream=None) -> None:
+    """dhidden and dweight of sum(dlogprobs * logprobs) + sum(dentropy * entropy), with the lse and
+    entropy that zero_token_logprobs has given (entropy and dentropy may be None)."""
+    torch or _load()
+    (tokens, width), (vocab, _) = _matrix("hidden", hidden), _matrix("weight", weight)
+    d = ZeroTokenLogprobsGradDesc(tokens=tokens, vocab=vocab, width=width, type=_type_of("hidden", hidden),
+                                  max_tokens=max_tokens, ignore_index=ignore_index)
+    hp, d.hidden_stride = _rows("hidden", hidden, hidden.dtype, tokens, width)
+    wp, d.weight_stride = _rows("weight", weight, hidden.dtype, vocab, width)
+    dhp, d.dhidden_stride = _rows("dhidden", dhidden, hidden.dtype, tokens, width)
+    dwp, d.dweight_stride = _rows("dweight", dweight, hidden.dtype, vocab, width)
+    sp, sn = _space(workspace)
+    _check(lib().zero_token_logprobs_backward(
+        ctypes.byref(d), hp, wp, _flat("ids", ids, torch.int64, tokens), _flat("lse", lse, torch.float32, tokens),
+        _flat("entropy", entropy, torch.float32, tokens), _flat("dlogprobs", dlogprobs, torch.float32, tokens),
+        _flat("dentropy", dentropy, torch.float32, tokens), dhp, dwp, sp, sn, _current(stream)),
+        "zero_token_logprobs_backward")
 
 
 # ------------------------------------------------------------------ AdamW over tensors
