@@ -182,7 +182,7 @@ struct LogprobPlan {           // what a call's sizes settle
     int64_t chunk, vocab_ld, pieces, width_ld;     // as the loss's
     TileChoice tile;
     int top;
-    int64_t off_given, off_stats, off_weighted, off_logits, off_hidden, off_weight;
+    int64_t off_given, off_stats, off_weighted, off_least, off_logits, off_hidden, off_weight;
     int64_t bytes;
 };
 

@@ -31,9 +31,9 @@ namespace zo {
 namespace {
 
 // A die's workgroups walk the tiles of H W^T, and load the next one while they are at a tile's
-// results: out(i, j, acc).
+// results: out(i, j, acc).  Columns from tile j0 on.
 template <typename T, int NI, int NJ, typename Out>
-__device__ __forceinline__ void walk(const Operand& h, const Operand& w, uint32_t ti, uint32_t tj, char* smem, Out out)
+__device__ __forceinline__ void walk(const Operand& h, const Operand& w, uint32_t ti, uint32_t tj, uint32_t j0, char* smem, Out out)
 {
     using G = Gemm<T, kInner, kInner, NI, NJ>;
     const uint32_t die = blockIdx.x % kDies, mine = tiles_of(die, ti * tj);
@@ -44,6 +44,7 @@ __device__ __forceinline__ void walk(const Operand& h, const Operand& w, uint32_
     uint32_t at = blockIdx.x / kDies;
     if (at >= mine) return;
     tile_of(die, at, ti, tj, bi, bj);
+    bj += j0;
     g.begin(h, w, bi * G::kTileI, bj * G::kTileJ, 0, steps);
     for (;;) {
         f4 acc[NI][NJ];
@@ -52,6 +53,7 @@ __device__ __forceinline__ void walk(const Operand& h, const Operand& w, uint32_
         g.run(steps, acc, [&] {
             if (at >= mine) return;
             tile_of(die, at, ti, tj, bi, bj);
+            bj += j0;
             g.begin(h, w, bi * G::kTileI, bj * G::kTileJ, 0, steps);
         });
         out(i, j, acc);
@@ -68,12 +70,21 @@ struct ScoreArgs {
     float2* stats;              // [tokens][pieces]: maximum and sum
     float* weighted;            // the sums of exp(z - m)(z - m), or NULL
     float* logits;              // [tokens][vocab_ld], or NULL
+    const uint32_t* least;      // of a row, in order: pieces whose maxima are less are not written; or NULL
     int64_t count, vocab, vocab_ld, pieces;
-    uint32_t ti, tj;            // tiles
+    uint32_t ti, tj, j0;        // tiles, the first column of them
 };
 
+// Bits in the order of the values, NaN before all; -0 is 0.
+__device__ __forceinline__ uint32_t in_order(float x)
+{
+    if (x != x) return 0;
+    const uint32_t u = bits(x + 0.0f);
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+
 // From a tile's logits to the pieces' statistics.
-template <typename T, bool PAST, int NI, int NJ>
+template <typename T, int NI, int NJ>
 __device__ __forceinline__ void score_out(const ScoreArgs& a, int64_t bi, int64_t bj, f4 (&acc)[NI][NJ])
 {
     using G = Gemm<T, kInner, kInner, NI, NJ>;
@@ -132,18 +143,19 @@ __device__ __forceinline__ void score_out(const ScoreArgs& a, int64_t bi, int64_
             if (a.weighted != nullptr) a.weighted[piece] = weighted;
         }
         if (NJ == 4 && a.logits != nullptr) {
+            if (a.least != nullptr && in_order(m) < a.least[n]) continue;
             float* to = a.logits + n * a.vocab_ld + v;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) store_vec<float, 4, PAST>(to + 4 * q, acc[ti][q]);
+            for (int q = 0; q < 4; ++q) store_vec<float, 4>(to + 4 * q, acc[ti][q]);
         }
     }
 }
 
-template <typename T, bool PAST, int NI, int NJ>
+template <typename T, int NI, int NJ>
 __global__ __launch_bounds__(kGemmThreads, 2) void score_kernel(ScoreArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    walk<T, NI, NJ>(a.h, a.w, a.ti, a.tj, smem, [&](int64_t i, int64_t j, f4 (&acc)[NI][NJ]) { score_out<T, PAST, NI, NJ>(a, i, j, acc); });
+    walk<T, NI, NJ>(a.h, a.w, a.ti, a.tj, a.j0, smem, [&](int64_t i, int64_t j, f4 (&acc)[NI][NJ]) { score_out<T, NI, NJ>(a, i, j, acc); });
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -162,14 +174,6 @@ struct ScoreJoin {
     int64_t pieces, vocab, vocab_ld, ignore;
     int top;
 };
-
-// Bits in the order of the values, NaN before all; -0 is 0.
-__device__ __forceinline__ uint32_t in_order(float x)
-{
-    if (x != x) return 0;
-    const uint32_t u = bits(x + 0.0f);
-    return (u >> 31) ? ~u : u | 0x80000000u;
-}
 
 // An element of an order by value, the lower id first where they are alike.
 struct Ranked {
@@ -190,19 +194,11 @@ __device__ __forceinline__ Ranked first_of(const Ranked& mine)
     return Ranked{value, (int32_t)~lanes_max<64>(has ? ~(uint32_t)mine.id : 0u)};
 }
 
-// The next `most` in order of what the lanes have: item(k), k < items, gives a lane's k-th.  taken(r, e)
-// is called by all lanes.
-template <typename Item, typename Taken>
-__device__ __forceinline__ void in_turn(int most, int items, Item item, Taken taken)
+// The first `most` in order of what the lanes have, one after the other: next(e) is a lane's first behind
+// e.  taken(r, e) is called by all lanes.
+template <typename Next, typename Taken>
+__device__ __forceinline__ void in_turn(int most, Next next, Taken taken)
 {
-    auto next = [&](const Ranked& last) {
-        Ranked best{0, kNoId};
-        for (int k = 0; k < items; ++k) {
-            const Ranked e = item(k);
-            if (last.before(e) && e.before(best)) best = e;
-        }
-        return best;
-    };
     Ranked mine = next(Ranked{0xffffffffu, -1});
     for (int r = 0; r < most; ++r) {
         const Ranked e = first_of(mine);
@@ -212,16 +208,64 @@ __device__ __forceinline__ void in_turn(int most, int items, Item item, Taken ta
     }
 }
 
+__device__ __forceinline__ void sooner(Ranked& best, const Ranked& last, const Ranked& e)
+{
+    if (last.before(e) && e.before(best)) best = e;
+}
+
+// The k-th largest of the 64 lanes' values (k from 1 to 64), by counting.
+__device__ __forceinline__ uint32_t kth_of(uint32_t value, int k)
+{
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+#pragma unroll
+    for (int l = 0; l < 64; ++l) {
+        const uint32_t other = __builtin_amdgcn_readlane(value, l);
+        before += other > value || (other == value && l < lane);
+    }
+    const uint64_t who = __ballot(before == k - 1);
+    return __builtin_amdgcn_readlane(value, __ffsll((unsigned long long)who) - 1);
+}
+
+// A bound for the `top` largest logits of a row from the maxima of its pieces: the top-th largest of what
+// the lanes' shares of them (every 64th piece) reach.  So many elements are no less.
+__device__ __forceinline__ uint32_t bound_of(uint32_t reach, int top, int pieces) { return pieces < top ? 0 : kth_of(reach, top); }
+
+__global__ __launch_bounds__(64) void bound_kernel(const float2* stats, uint32_t* least, int64_t row_pieces, int pieces, int top)
+{
+    const float2* row = stats + (int64_t)blockIdx.x * row_pieces;
+    uint32_t reach = 0;
+    for (int p = threadIdx.x; p < pieces; p += 64) reach = larger(reach, in_order(row[p].x));
+    reach = bound_of(reach, top, pieces);
+    if (threadIdx.x == 0) least[blockIdx.x] = reach;
+}
+
+constexpr int kCandidates = 256;           // that are ranked by counting
+
+// Adds the lanes' items that `is` says to a list in LDS.
+__device__ __forceinline__ int append(int count, bool is, int lane)
+{
+    const uint64_t who = __ballot(is);
+    return count + __popcll(who & ((1ull << lane) - 1));
+}
+
 // A token.  FEW: up to 1024 pieces, whose maxima stay in registers.
+//
+// The alternatives: of the pieces whose maxima reach the bound (as many as are asked for, and a few more) the
+// logits that do are put into a list and ranked, each by how many are before it.  Where that
+// would be more than the list holds (many logits alike) the pieces are taken one after the
+// other in order, as many as are asked for, and then their logits.
 template <bool FEW>
 __global__ __launch_bounds__(64) void score_join_kernel(ScoreJoin a)
 {
     extern __shared__ float held[];            // [top][64] logits
+    __shared__ uint32_t values[kCandidates];
+    __shared__ int32_t ids[kCandidates];
     constexpr int K = FEW ? 16 : 1;
     const int64_t n = blockIdx.x;
     const int lane = threadIdx.x;
     const float2* row = a.stats + n * a.pieces;
-    const int pieces = (int)a.pieces, mine = (pieces - lane + 63) / 64;        // of this lane: lane, lane + 64, ...
+    const int pieces = (int)a.pieces;          // a lane has lane, lane + 64, ...
     float2 s[K];
     float m = -INFINITY;
     if constexpr (FEW) {
@@ -232,23 +276,27 @@ __global__ __launch_bounds__(64) void score_join_kernel(ScoreJoin a)
     } else {
         for (int p = lane; p < pieces; p += 64) m = fmaxf(m, row[p].x);
     }
+    const float reach = m;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
     const float base = m == -INFINITY ? 0.0f : m;
     double sum = 0.0, weighted = 0.0;
-    auto add = [&](float2 part, int p) {
+    auto add = [&](float2 part, float w) {
         // (a piece of -infinities adds nothing)
         const float d = part.x == -INFINITY ? 0.0f : part.x - base;
         const double f = part.x == -INFINITY ? 0.0 : (double)expf(d);
         sum += f * (double)part.y;
-        if (a.weighted != nullptr) weighted += f * ((double)a.weighted[n * a.pieces + p] + (double)part.y * (double)d);
+        weighted += f * ((double)w + (double)part.y * (double)d);
     };
     if constexpr (FEW) {
+        float w[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[k] = a.weighted != nullptr && k * 64 + lane < pieces ? a.weighted[n * a.pieces + k * 64 + lane] : 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (k * 64 + lane < pieces) add(s[k], k * 64 + lane);
+            if (k * 64 + lane < pieces) add(s[k], w[k]);
     } else {
-        for (int p = lane; p < pieces; p += 64) add(row[p], p);
+        for (int p = lane; p < pieces; p += 64) add(row[p], a.weighted != nullptr ? a.weighted[n * a.pieces + p] : 0.0f);
     }
     sum = lanes_sum(sum);
     weighted = lanes_sum(weighted);
@@ -263,30 +311,98 @@ __global__ __launch_bounds__(64) void score_join_kernel(ScoreJoin a)
         }
     }
     if (a.top == 0) return;
-    // the pieces that can hold an alternative, their logits beside each other in LDS (a lane's own column)
     const float* z = a.logits + n * a.vocab_ld;
-    const int wanted = a.top < pieces ? a.top : pieces;
-    __shared__ int32_t ids[64];
-    auto put = [&](int r, const Ranked& e) {
-        if (lane == 0) ids[r] = e.id * 64;
-        held[r * 64 + lane] = z[(int64_t)e.id * 64 + lane];
+    auto piece = [&](int k) {                   // the lane's k-th
+        const int p = k * 64 + lane;
+        if (p >= pieces) return Ranked{0u, kNoId};
+        if constexpr (FEW) return Ranked{in_order(s[k].x), p};
+        else return Ranked{in_order(row[p].x), p};
+    };
+    const int rounds = (pieces + 63) / 64;
+    const uint32_t bound = bound_of(lane < pieces ? in_order(reach) : 0u, a.top, pieces);
+    int count = 0;
+    auto collect = [&](int k) {
+        const Ranked e = piece(k);
+        const bool is = e.id != kNoId && e.value >= bound;
+        const int at = append(count, is, lane);
+        if (is && at < kCandidates) ids[at] = e.id;
+        count += __popcll(__ballot(is));
     };
     if constexpr (FEW) {
-        // (a chain of selections in place of an index into registers)
-        in_turn(wanted, K, [&](int k) {
-            float x = s[0].x;
 #pragma unroll
-            for (int q = 1; q < K; ++q) x = k == q ? s[q].x : x;
-            const bool is = k < mine;
-            return Ranked{is ? in_order(x) : 0u, is ? k * 64 + lane : kNoId};
-        }, put);
+        for (int k = 0; k < K; ++k) collect(k);
     } else {
-        in_turn(wanted, mine, [&](int k) { return Ranked{in_order(row[k * 64 + lane].x), k * 64 + lane}; }, put);
+        for (int k = 0; k < rounds; ++k) collect(k);
     }
     __syncthreads();
-    in_turn(a.top, wanted, [&](int k) {
-        const int32_t id = ids[k] + lane;
-        return id < a.vocab ? Ranked{in_order(held[k * 64 + lane]), id} : Ranked{0u, kNoId};
+    if (count <= kCandidates) {
+        // 16 pieces' logits at a time (their list is read before it is written over)
+        const int chosen = count;
+        int from[kCandidates / 64];
+#pragma unroll
+        for (int q = 0; q < kCandidates / 64; ++q) from[q] = q * 64 + lane < chosen ? ids[q * 64 + lane] : 0;
+        __syncthreads();
+        count = 0;
+        for (int c = 0; c < chosen; c += 16) {
+            float x[16];
+            int32_t id[16];
+            const int part = c >> 6;
+            const int mine = part == 0 ? from[0] : part == 1 ? from[1] : part == 2 ? from[2] : from[3];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                id[k] = __builtin_amdgcn_readlane(mine, (c + k) & 63) * 64 + lane;
+                x[k] = z[id[k]];
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t value = in_order(x[k]);
+                const bool is = c + k < chosen && id[k] < a.vocab && value >= bound;
+                const int at = append(count, is, lane);
+                if (is && at < kCandidates) {
+                    values[at] = value;
+                    ids[at] = id[k];
+                }
+                count += __popcll(__ballot(is));
+            }
+        }
+        __syncthreads();
+        if (count <= kCandidates) {
+            for (int c = lane; c < count; c += 64) {
+                const Ranked e{values[c], ids[c]};
+                int before = 0;
+#pragma unroll 8
+                for (int k = 0; k < count; ++k) before += Ranked{values[k], ids[k]}.before(e);
+                if (before < a.top) {
+                    a.top_ids[n * a.top + before] = e.id;
+                    a.top_logprobs[n * a.top + before] = (float)((double)z[e.id] - lse);
+                }
+            }
+            return;
+        }
+    }
+    __syncthreads();
+    const int wanted = a.top < pieces ? a.top : pieces;
+    in_turn(wanted, [&](const Ranked& last) {
+        Ranked best{0, kNoId};
+        if constexpr (FEW) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) sooner(best, last, piece(k));
+        } else {
+            for (int k = 0; k < rounds; ++k) sooner(best, last, piece(k));
+        }
+        return best;
+    }, [&](int r, const Ranked& e) {
+        if (lane == 0) ids[r] = e.id * 64;
+        held[r * 64 + lane] = z[(int64_t)e.id * 64 + lane];
+    });
+    __syncthreads();
+    in_turn(a.top, [&](const Ranked& last) {
+        Ranked best{0, kNoId};
+        for (int k = 0; k < wanted; ++k) {
+            const int32_t id = ids[k] + lane;
+            if (id < a.vocab) sooner(best, last, Ranked{in_order(held[k * 64 + lane]), id});
+        }
+        return best;
     }, [&](int r, const Ranked& e) {
         if (lane != 0) return;
         a.top_ids[n * a.top + r] = e.id;
@@ -452,7 +568,7 @@ template <typename T, int NI, int NJ>
 __global__ __launch_bounds__(kGemmThreads, 2) void dscore_kernel(DScoreArgs a)
 {
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    walk<T, NI, NJ>(a.h, a.w, a.ti, a.tj, smem, [&](int64_t i, int64_t j, f4 (&acc)[NI][NJ]) { dscore_out<T, NI, NJ>(a, i, j, acc); });
+    walk<T, NI, NJ>(a.h, a.w, a.ti, a.tj, 0, smem, [&](int64_t i, int64_t j, f4 (&acc)[NI][NJ]) { dscore_out<T, NI, NJ>(a, i, j, acc); });
 }
 
 // ------------------------------------------------------------------ launches
@@ -465,16 +581,20 @@ unsigned standing(uint32_t tiles)
     return tiles < stand ? tiles : stand;
 }
 
-template <typename T, bool PAST, int NI, int NJ>
+template <typename T, int NI, int NJ>
 hipError_t score(ScoreArgs a, hipStream_t s)
 {
     using G = Gemm<T, kInner, kInner, NI, NJ>;
-    static const hipError_t allowed = allow(score_kernel<T, PAST, NI, NJ>, G::kLds);
+    static const hipError_t allowed = allow(score_kernel<T, NI, NJ>, G::kLds);
     if (allowed != hipSuccess) return allowed;
-    a.ti = (uint32_t)ceil_div(a.count, G::kTileI);
-    a.tj = (uint32_t)ceil_div(a.vocab, G::kTileJ);
-    score_kernel<T, PAST, NI, NJ><<<dim3(standing<NI>(a.ti * a.tj)), kGemmThreads, G::kLds, s>>>(a);
+    score_kernel<T, NI, NJ><<<dim3(standing<NI>(a.ti * a.tj)), kGemmThreads, G::kLds, s>>>(a);
     return hipSuccess;
+}
+
+template <typename T>
+hipError_t score(const ScoreArgs& a, const TileChoice& tile, hipStream_t s)
+{
+    return tile.ni == 2 ? score<T, 2, 4>(a, s) : tile.nj == 5 ? score<T, 8, 5>(a, s) : score<T, 8, 4>(a, s);
 }
 
 template <typename T, int NI, int NJ>
@@ -520,6 +640,17 @@ void lay_out(const void* hidden, int64_t hidden_stride, const void* weight, int6
     });
 }
 
+// Tile columns whose logits are all written, so that their largest bound what has to be of the rest; 0: no
+// such beginning.  With a share f of P pieces before, some top / f of the rest reach the bound: f is
+// sqrt(top / P), in whole rounds of tiles over the card.
+uint32_t columns_before(uint32_t ti, uint32_t tj, int top)
+{
+    const double share = sqrt((double)top / (4.0 * tj));
+    const uint32_t rounds = (uint32_t)ceil(share * tj * ti / kCUs);
+    const uint32_t columns = rounds * kCUs / ti;
+    return ti < 4 || columns < 1 || columns > tj / 2 || columns * 4 < (uint32_t)top ? 0 : columns;
+}
+
 template <typename T>
 hipError_t logprobs(const Logprobs& a, const LogprobPlan& p, hipStream_t s)
 {
@@ -534,15 +665,22 @@ hipError_t logprobs(const Logprobs& a, const LogprobPlan& p, hipStream_t s)
     for (int64_t n0 = 0; n0 < p.tokens; n0 += p.chunk) {
         const int64_t n = p.tokens - n0 < p.chunk ? p.tokens - n0 : p.chunk;
         const int64_t* tokens = a.tokens != nullptr ? a.tokens + n0 : nullptr;
-        const ScoreArgs sa{Operand{h + n0 * h_ld, h_ld, n, p.width_ld}, Operand{w, w_ld, p.vocab, p.width_ld}, tokens, given_logit, stats, weighted,
-                           logits, n, p.vocab, p.vocab_ld, p.pieces, 0, 0};
-        // (logits of more than the last cache's 256 MiB go past the caches)
-        const bool past = logits != nullptr && n * p.vocab_ld * 4 > kLastCache;
-        hipError_t e;
-        if (p.tile.ni == 2) e = score<T, false, 2, 4>(sa, s);
-        else if (p.tile.nj == 5) e = score<T, false, 8, 5>(sa, s);
-        else if (past) e = score<T, true, 8, 4>(sa, s);
-        else e = score<T, false, 8, 4>(sa, s);
+        ScoreArgs sa{Operand{h + n0 * h_ld, h_ld, n, p.width_ld}, Operand{w, w_ld, p.vocab, p.width_ld}, tokens, given_logit, stats, weighted,
+                     logits, nullptr, n, p.vocab, p.vocab_ld, p.pieces, 0, 0, 0};
+        sa.ti = (uint32_t)ceil_div(n, 32 * p.tile.ni);
+        sa.tj = (uint32_t)ceil_div(p.vocab, 64 * p.tile.nj);
+        const uint32_t all = sa.tj, first = p.top > 0 ? columns_before(sa.ti, sa.tj, p.top) : 0;
+        if (first > 0) {
+            sa.tj = first;
+            hipError_t e = score<T>(sa, p.tile, s);
+            if (e != hipSuccess) return e;
+            uint32_t* least = reinterpret_cast<uint32_t*>(a.space + p.off_least);
+            bound_kernel<<<dim3((unsigned)n), 64, 0, s>>>(stats, least, p.pieces, (int)first * 4, p.top);
+            sa.least = least;
+            sa.j0 = first;
+            sa.tj = all - first;
+        }
+        const hipError_t e = score<T>(sa, p.tile, s);
         if (e != hipSuccess) return e;
         const ScoreJoin j{stats, weighted, logits, given_logit, tokens, a.logprobs != nullptr ? a.logprobs + n0 : nullptr, a.lse + n0,
                           a.entropy != nullptr ? a.entropy + n0 : nullptr, a.top_ids != nullptr ? a.top_ids + n0 * p.top : nullptr,
@@ -613,6 +751,7 @@ LogprobPlan logprob_plan(int64_t tokens, int64_t vocab, int64_t width, int64_t m
     p.off_given = take(p.chunk * 4);
     p.off_stats = take(p.chunk * p.pieces * 8);
     p.off_weighted = take(p.chunk * p.pieces * 4);
+    p.off_least = take(p.chunk * 4);
     p.off_logits = take(top > 0 ? p.chunk * p.vocab_ld * 4 : 0);
     p.off_hidden = take(tokens * p.width_ld * 2);
     p.off_weight = take(vocab * p.width_ld * 2);

@@ -4,7 +4,7 @@
 // both; and backward, with the gradient dh that comes down the residual's way:
 //     xhat = h rstd ;  g = dy w ;  dx = rstd (g - xhat mean(g xhat)) + dh
 //     dw = sum_rows dy xhat
-// All of it in fp32 (the sum of squares in 64 bits); h, y and the results are rounded once.  The norm is of h as it is
+// Backward in fp32, forward in 64 bits; h, y and the results are rounded once.  The norm is of h as it is
 // held: what the backward pass reads.
 //
 // Bound by memory, as the layer norm (ops_norm.hip), and laid out as it is: a row in
@@ -101,9 +101,12 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint8_t* exps, int64_t
     if (c % kScaleBlock == 0) exps[c / kScaleBlock] = (uint8_t)E;
 }
 
-// The sum of squares is in 64 bits: no square passes its range, and rstd is rounded once.  (A result in 8
-// bits changes by a whole step where y lies next to a middle: with fp32 sums twice as often.)
-__device__ __forceinline__ float rstd_of(double q, int64_t width, float eps) { return (float)(1.0 / sqrt(q / (double)width + (double)eps)); }
+// The sum of squares, rstd and y are in 64 bits before they are rounded: no square passes its range, and a
+// result in 8 bits, which changes by a whole step where y lies next to a middle, is as good as always the
+// definition's (the vector unit's 64-bit rate is its 32-bit one).
+__device__ __forceinline__ double rstd_of(double q, int64_t width, float eps) { return 1.0 / sqrt(q / (double)width + (double)eps); }
+
+__device__ __forceinline__ float scaled(float x, double rstd, float w) { return (float)((double)x * (rstd * (double)w)); }
 
 // ------------------------------------------------------------------ forward
 
@@ -146,8 +149,8 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_forward_kernel(Rm
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < W; ++e) q = fma((double)v[k][e], (double)v[k][e], q);
-    const float rstd = rstd_of(row_sum<NW>(q, sh), a.width, a.eps);
-    if (lane == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+    const double rstd = rstd_of(row_sum<NW>(q, sh), a.width, a.eps);
+    if (lane == 0 && a.rstd != nullptr) a.rstd[row] = (float)rstd;
     T* y = a.y != nullptr ? static_cast<T*>(a.y) + row * a.y_stride : nullptr;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -157,7 +160,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_forward_kernel(Rm
         for (int e = 0; e < W; ++e) w[e] = 1.0f;
         if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
 #pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = v[k][e] * rstd * w[e];
+        for (int e = 0; e < W; ++e) w[e] = scaled(v[k][e], rstd, w[e]);
         if (y != nullptr && c < a.width) store_part<PAST>(y, c, a.width, w);
         if (a.codes != nullptr) {
             // (past the width 0: inf or NaN as rstd make NaN of the zeros there)
@@ -201,8 +204,8 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
             for (int e = 0; e < W; ++e) q = fma((double)v[e], (double)v[e], q);
         }
     }
-    const float rstd = rstd_of(row_sum<16>(q, sh), a.width, a.eps);
-    if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+    const double rstd = rstd_of(row_sum<16>(q, sh), a.width, a.eps);
+    if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = (float)rstd;
     T* y = a.y != nullptr ? static_cast<T*>(a.y) + row * a.y_stride : nullptr;
     // (whole blocks: the lanes of one come to its codes together)
     for (int64_t c = c0; c < round_up(a.width, kScaleBlock); c += step) {
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
         for (int e = 0; e < W; ++e) w[e] = 1.0f;
         if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
 #pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = c + e < a.width ? v[e] * rstd * w[e] : 0.0f;
+        for (int e = 0; e < W; ++e) w[e] = c + e < a.width ? scaled(v[e], rstd, w[e]) : 0.0f;
         if (y != nullptr && c < a.width) store_part<PAST>(y, c, a.width, w);
         if (a.codes != nullptr) store_codes<W>(a.codes + row * a.codes_stride, a.exps + row * a.exps_stride, c, a.width, w);
     }
