@@ -29,7 +29,10 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr int kBlock = kScaleBlock;
-constexpr int kAllDone = 0x0070;        // s_waitcnt vmcnt(0) lgkmcnt(0)
+
+// s_waitcnt: all LDS reads done, and of the loads and stores to memory all but the last `left` (they end
+// in the order of their issue).
+constexpr int wait_for(int left) { return 0x0070 | (left & 15) | (left >> 4) << 14; }
 
 constexpr int kThreads = 256;
 
@@ -205,20 +208,17 @@ struct Tile {
         p.reader(smem, (wave >> 1) * 16 * NI, lane);
         q.reader(smem + PSide::kBytes, (wave & 1) * 128, lane);
     }
-    // The next step's loads have arrived, for every wave; and every wave has all that it reads
-    // of this stage.
-    __device__ __forceinline__ void turn()
+    // For every wave: what it has to have read of LDS it has, and its loads but the last LEFT have arrived.
+    template <int LEFT>
+    static __device__ __forceinline__ void turn()
     {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(kAllDone);      // (the builtin: the compiler counts on it)
+        __builtin_amdgcn_s_waitcnt(wait_for(LEFT));      // (the builtin: the compiler counts on it)
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     }
-    __device__ __forceinline__ void issue(uint32_t stage)
-    {
-        p.issue(smem + stage, wave);
-        q.issue(smem + stage + PSide::kBytes, wave);
-    }
+    static constexpr int kStageLoads = NI + NJ;          // a wave's, of a stage
+    static constexpr int kStores = 4 * NI;               // a wave's, of a whole tile, at least
     // Scales of 2 steps, of an even or an odd pair.
     __device__ __forceinline__ void issue_scales(int pair)
     {
@@ -256,9 +256,13 @@ struct Tile {
         if constexpr (SQUARE) qe.begin(t.b_exps + (j0 >> 7) * t.b_exps_ld + b0, t.b_exps_ld, j > 128 ? 2 : 1, t.blocks - b0, back, wave, row_j());
         else qe.begin(t.b_exps + j0 * t.b_exps_ld + b0, t.b_exps_ld, (int)(j < kTileJ ? j : kTileJ), t.blocks - b0, back, wave, row_j());
         issue_scales(0);
-        issue(back ? kStageBytes : 0);
-        if (steps > 1) issue(back ? 0 : kStageBytes);
         issue_scales(1);
+        const uint32_t stage = back ? kStageBytes : 0;
+        p.issue(smem + stage, wave);
+        q.issue(smem + stage + PSide::kBytes, wave);
+        if (steps == 1) return;
+        p.issue(smem + kStageBytes - stage, wave);
+        q.issue(smem + kStageBytes - stage + PSide::kBytes, wave);
     }
     // (Of the second stage, the last step's.)  The codes behind the depth's end, in the last block's chunk that it ends in, are other
     // rows': zeros instead.  (Both sides: 0 times NaN is none.)
@@ -329,16 +333,28 @@ struct Tile {
         read_scales<F>(s);
     }
     // A step, in quarters.  Each is multiplied while what the next one lacks is read: first what the
-    // step has, then its other half of A's rows, then of B's; behind the barrier the next step's
+    // step has, then its other half of A's rows, then of B's; behind the second barrier the next step's
     // first halves, each into registers that the quarter before has freed.  So the halves of A's
     // rows change places from step to step (F, the stage too).
-    template <int F, typename B>
+    //
+    // MORE: there are two steps more.  A's piece of the one after next is loaded behind the first quarter,
+    // when all have read this stage's; B's behind the second.  (Both behind the second: the loads of a
+    // step had all arrived when the next were started, 8192 x 8192 x 8192 453 us.)
+    template <int F, bool MORE, typename B>
     __device__ __forceinline__ void half_step(f4 (&acc)[NI][NJ], B behind)
     {
         constexpr uint32_t stage = F ? kStageBytes : 0;
         multiply<F, 0, F>(acc, [&](int k) { read_b<1 - F>(stage, k); });
+        if constexpr (MORE) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(kLgkmDone);
+            asm volatile("s_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            p.issue(smem + stage, wave);
+        }
         multiply<F, 0, 1 - F>(acc, [&](int k) { read_a<1>(stage, k); });
-        turn();
+        turn<MORE ? NI : 0>();
+        if constexpr (MORE) q.issue(smem + stage + PSide::kBytes, wave);
         behind();
     }
     template <int F>
@@ -350,16 +366,20 @@ struct Tile {
         multiply<F, 1, F>(acc, [&](int k) { read_b<1 - F>(other, k); });
     }
     // acc[ti][tj][e]: i = row_of(ti), j = column_of(tj) + e, within the tile.  `last` says whether the
-    // share's last block is the depth's.  `free` is called when both stages have been read.
+    // share's last block is the depth's, `stored` that a whole tile's results have been stored since begin().
+    // `free` is called when both stages have been read.
     // (No branch within the steps that repeat: with one the compiler keeps fewer sums in place.)
     template <typename N>
-    __device__ __forceinline__ void run(const TileArgs& t, int steps, bool last, f4 (&acc)[NI][NJ], N free)
+    __device__ __forceinline__ void run(const TileArgs& t, int steps, bool last, bool stored, f4 (&acc)[NI][NJ], N free)
     {
 #pragma unroll
         for (int ti = 0; ti < NI; ++ti)
 #pragma unroll
             for (int tj = 0; tj < NJ; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
-        turn();
+        // (the first stage; the second, and the stores, may still be under way)
+        if (steps == 1) turn<0>();
+        else if (stored) turn<kStageLoads + kStores>();
+        else turn<kStageLoads>();
         const bool ends = last && (t.depth & 15) != 0;
         const int back = steps & 1, pairs = (steps + 1) / 2;
         int pair = back;
@@ -367,31 +387,25 @@ struct Tile {
             if (ends && steps == 1) cut(t);
             first<1>(1);
             if (steps > 1) {
-                half_step<1>(acc, [&] {
-                    issue(kStageBytes);
-                    issue_scales(0);
-                });
+                half_step<1, true>(acc, [&] { issue_scales(0); });
                 other_half<1>(1, acc);
             }
         } else {
             first<0>(0);
         }
         for (; pair + 1 < pairs; ++pair) {
-            half_step<0>(acc, [&] { issue(0); });
+            half_step<0, true>(acc, [] {});
             other_half<0>(2 * pair, acc);
-            half_step<1>(acc, [&] {
-                issue(kStageBytes);
-                issue_scales(pair);                    // (of the pair two on)
-            });
+            half_step<1, true>(acc, [&] { issue_scales(pair); });      // (of the pair two on)
             other_half<1>(2 * pair + 1, acc);
         }
         if (steps > 1) {
-            half_step<0>(acc, [&] {
+            half_step<0, false>(acc, [&] {
                 if (ends) cut(t);
             });
             other_half<0>(2 * pair, acc);
         }
-        half_step<1>(acc, free);
+        half_step<1, false>(acc, free);
         multiply<1, 1, 0>(acc, [](int) {});
         multiply<1, 1, 1>(acc, [](int) {});
         settled(acc);
@@ -470,6 +484,7 @@ __global__ __launch_bounds__(kThreads, NI == 2 ? 2 : 1) void tile_kernel(TileArg
     G g(t, lds_address(smem));
     uint32_t bi = 0, bj = 0;
     int split = 0, b0 = 0, steps = 0;
+    bool stored = false;
     auto place = [&] {
         // (a die's share of all splits' tiles, one split after the other)
         const uint32_t n = die * q + (die < r ? die : r) + at;
@@ -486,10 +501,11 @@ __global__ __launch_bounds__(kThreads, NI == 2 ? 2 : 1) void tile_kernel(TileArg
         const int now = steps, part = split;
         const bool last = b0 + steps == t.blocks;
         at += stride;
-        g.run(t, now, last, acc, [&] {
+        g.run(t, now, last, stored, acc, [&] {
             if (at < mine) place();
         });
         tile_out<T, NI, SQUARE>(t, part, i, j, acc);
+        stored = (int64_t)(i + 1) * G::kTileI <= t.rows && (int64_t)(j + 1) * G::kTileJ <= t.cols;
         if (at >= mine) return;
     }
 }
