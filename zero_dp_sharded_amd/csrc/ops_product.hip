@@ -75,6 +75,18 @@ struct TileArgs {
     int splits;                // each at least one block
 };
 
+// A kernel's only argument, read again from where it lies: kept in registers from tile to tile its fields
+// would not leave enough.
+typedef const __attribute__((address_space(4))) TileArgs* ArgsAt;
+__device__ __forceinline__ ArgsAt args_at()
+{
+    ArgsAt t = (ArgsAt)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(t));
+    return t;
+}
+
+__device__ __forceinline__ int least_of(int64_t left, int most) { return left < most ? (int)left : most; }
+
 // One load of 256 bytes into LDS at byte address `lds`: the lane's 4 bytes at offset v.  As
 // load_to_lds.
 __device__ __forceinline__ void load_words_to_lds(uint32_t v, const u4& rsrc, uint32_t lds)
@@ -95,14 +107,15 @@ struct Scales {
     int skew;                  // of the rows that a lane needs: the first byte's place in its word
 
     // The steps from -back on (0 or 1).
-    __device__ __forceinline__ void begin(const uint8_t* x, int64_t ld, int rows, int64_t blocks, int back, int wave, int row)
+    // (row strides up to 2^22: every offset is below 2^30)
+    __device__ __forceinline__ void begin(const uint8_t* x, int ld, int rows, int blocks, int back, int wave, int row)
     {
         const int over = (int)(reinterpret_cast<uintptr_t>(x) & 3);
         piece.base = reinterpret_cast<const char*>(x) - over;
-        piece.left = whole_words(over + (rows - 1) * ld + blocks);
+        piece.left = (over + (rows - 1) * ld + blocks + 3) & ~3;
         const int mine = wave * 64 + (threadIdx.x & 63);
-        from = mine < rows ? (uint32_t)(over + mine * (int)ld - back) : kOutOfRange;
-        skew = over + row * (int)ld - back;
+        from = mine < rows ? (uint32_t)(over + mine * ld - back) : kOutOfRange;
+        skew = over + row * ld - back;
     }
     // The next 2 steps', to LDS at `lds`.
     __device__ __forceinline__ void issue(uint32_t lds, int wave)
@@ -132,36 +145,44 @@ template <int Q, bool RUNS>
 struct Rows {
     static constexpr int kBytes = Q * 32 * kBlock;
     Piece piece;
-    int64_t left;              // codes of a row from here on
+    int left;                  // codes of a row from here on
     uint32_t voff, apart, addr;
     int chunk;                 // a lane's, in 16 codes
 
     static __device__ __forceinline__ int key(int row) { return RUNS ? (row & 3) | ((row >> 4) & 1) << 2 : row & 7; }
-    __device__ __forceinline__ void lanes(int64_t ld, int wave, int lane)
+    // (row strides up to 2^22: every offset inside a tile is below 2^30)
+    __device__ __forceinline__ void lanes(int ld, int wave, int lane)
     {
         const int row = wave * 8 + (lane >> 3);            // (32 rows on the key is the same)
         chunk = ((lane & 7) ^ key(row)) * 16;
         voff = (uint32_t)(row * ld + chunk);
         apart = (uint32_t)(32 * ld);
     }
-    __device__ __forceinline__ void begin(const uint8_t* x, int64_t ld, int64_t row0, int64_t rows, int64_t k0, int64_t depth)
+    // x: the tile's first row at its first code; `rows` of them, `depth` codes.  No rows: zeros.
+    __device__ __forceinline__ void begin(const uint8_t* x, int ld, int rows, int depth)
     {
-        piece.base = reinterpret_cast<const char*>(x) + row0 * ld + k0;
-        const int64_t all = rows - row0 < Q * 32 ? rows - row0 : Q * 32;
-        piece.left = whole_words((all - 1) * ld + depth - k0);
+        piece.base = reinterpret_cast<const char*>(x);
+        piece.left = rows > 0 ? ((rows - 1) * ld + depth + 3) & ~3 : 0;
         piece.step = kBlock;
-        left = depth - k0;
+        left = rows > 0 ? depth : 0;
     }
-    __device__ __forceinline__ void issue(uint32_t lds, int wave)
+    // A stage's loads, Q of them, to LDS at `lds` (the wave's place there).
+    struct Loads {
+        u4 rsrc;
+        uint32_t first, by, lds;
+        __device__ __forceinline__ void issue(int q) const { load_to_lds(first + q * by, rsrc, lds + q * 4096); }
+    };
+    __device__ __forceinline__ Loads next(uint32_t lds, int wave)
     {
-        const u4 rsrc = piece.descriptor();
-        uint32_t first = chunk >= left ? kOutOfRange : voff;
-        const uint32_t by = chunk >= left ? 0 : apart;
-        asm volatile("" : "+v"(first));      // (added to here, not kept Q times in registers)
-#pragma unroll
-        for (int q = 0; q < Q; ++q) load_to_lds(first + q * by, rsrc, lds + (q * 4 + wave) * 1024);
+        Loads l;
+        l.rsrc = piece.descriptor();
+        l.first = chunk >= left ? kOutOfRange : voff;
+        l.by = chunk >= left ? 0 : apart;
+        l.lds = lds + wave * 1024;
+        asm volatile("" : "+v"(l.first));    // (added to there, not kept Q times in registers)
         piece.advance();
         left -= kBlock;
+        return l;
     }
     // first: the wave's first row
     __device__ __forceinline__ void reader(uint32_t lds, int first, int lane)
@@ -188,23 +209,28 @@ struct Tile {
     using QSide = Rows<NJ, true>;
     static constexpr int kStageBytes = PSide::kBytes + QSide::kBytes;
     static constexpr int kScaleBytes = 2 * Scales::kBytes;         // of both operands
-    static constexpr int kLds = 2 * (kStageBytes + kScaleBytes);
-    static constexpr int NQ = SQUARE ? 1 : NJ;     // scales of B that a lane needs (a wave's 128 rows are one square's)
+    static constexpr int kOutRow = 256 + 16;       // bytes of a row of results on their way out
+    static constexpr int kOutBytes = 16 * kOutRow; // a wave's
+    static constexpr int kLds = 2 * (kStageBytes + kScaleBytes) + 4 * kOutBytes;
+    // scales of B that a lane needs: a wave's 128 rows are one square's, this step's and the next
+    static constexpr int NQ = SQUARE ? 2 : NJ;
 
     PSide p;
     QSide q;
     Scales pe, qe;
     int wave;
     uint32_t smem, scales;                         // LDS: the stages, the scales
-    uint32_t ps[2][NI], qs[2][NQ];                 // of a step, and the next
+    int pair_left;                                 // of the two stages to come those that there are
+    uint32_t stage0;                               // the first of them
+    uint32_t ps[NI], qs[NQ];                       // scales, each half read when the last step's has been used
     v8i a[NJ], b[NI];
 
-    __device__ __forceinline__ Tile(const TileArgs& t, uint32_t lds) : smem(lds), scales(lds + 2 * kStageBytes)
+    __device__ __forceinline__ Tile(ArgsAt t, uint32_t lds) : smem(lds), scales(lds + 2 * kStageBytes)
     {
         const int lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        p.lanes(t.a_ld, wave, lane);
-        q.lanes(t.b_ld, wave, lane);
+        p.lanes((int)t->a_ld, wave, lane);
+        q.lanes((int)t->b_ld, wave, lane);
         p.reader(smem, (wave >> 1) * 16 * NI, lane);
         q.reader(smem + PSide::kBytes, (wave & 1) * 128, lane);
     }
@@ -233,42 +259,78 @@ struct Tile {
         const int r = threadIdx.x & 15;
         return SQUARE ? (wave & 1) : (wave & 1) * 128 + (r >> 2) * 16 + (r & 3);
     }
-    template <int F>
-    __device__ __forceinline__ void read_scales(int s)
+    // Of step s (at parity F) those of half I of A's rows, and of half J of B's.
+    template <int I>
+    __device__ __forceinline__ void read_ps(int s)
     {
-        const uint32_t from = scales + ((s >> 1) & 1) * kScaleBytes;
-        const uint32_t pa = pe.at(from, row_i(), s), qa = qe.at(from + Scales::kBytes, row_j(), s);
+        const uint32_t at = pe.at(scales + ((s >> 1) & 1) * kScaleBytes, row_i(), s);
 #pragma unroll
-        for (int k = 0; k < NI; ++k) ps[F][k] = byte_at(pa + k * 64);
+        for (int k = I * H; k < (I + 1) * H; ++k) ps[k] = byte_at(at + k * 64);
+    }
+    template <int F, int J>
+    __device__ __forceinline__ void read_qs(int s)
+    {
+        if (SQUARE && J == 1) return;
+        const uint32_t at = qe.at(scales + ((s >> 1) & 1) * kScaleBytes + Scales::kBytes, row_j(), s);
+        if constexpr (SQUARE) {
+            qs[F] = byte_at(at);
+        } else {
 #pragma unroll
-        for (int k = 0; k < NQ; ++k) qs[F][k] = byte_at(qa + (k >> 2) * 256 + (k & 3) * 16);
+            for (int k = J * HJ; k < (J + 1) * HJ; ++k) qs[k] = byte_at(at + (k >> 2) * 256 + (k & 3) * 16);
+        }
     }
     // Steps go in pairs, the first of a pair through the first stage; of an odd count the first is the
     // second of its pair.
-    // Start on the tile at (i0, j0), `steps` blocks from b0 on.
-    __device__ __forceinline__ void begin(const TileArgs& t, int64_t i0, int64_t j0, int b0, int steps)
+    // On to the tile at (i0, j0), `steps` blocks from b0 on: its scales are loaded, of its codes the first
+    // two stages by begin_loads.  The second of a single step is zeros.
+    __device__ __forceinline__ void begin(ArgsAt t, int64_t i0, int64_t j0, int b0, int steps)
     {
-        p.begin(t.a, t.a_ld, i0, t.rows, (int64_t)b0 * kBlock, t.depth);
-        q.begin(t.b, t.b_ld, j0, t.cols, (int64_t)b0 * kBlock, t.depth);
-        const int64_t i = t.rows - i0, j = t.cols - j0;
-        const int back = steps & 1;
-        pe.begin(t.a_exps + i0 * t.a_exps_ld + b0, t.a_exps_ld, (int)(i < kTileI ? i : kTileI), t.blocks - b0, back, wave, row_i());
-        if constexpr (SQUARE) qe.begin(t.b_exps + (j0 >> 7) * t.b_exps_ld + b0, t.b_exps_ld, j > 128 ? 2 : 1, t.blocks - b0, back, wave, row_j());
-        else qe.begin(t.b_exps + j0 * t.b_exps_ld + b0, t.b_exps_ld, (int)(j < kTileJ ? j : kTileJ), t.blocks - b0, back, wave, row_j());
+        const int depth = (int)t->depth - b0 * kBlock, blocks = t->blocks - b0, back = steps & 1;
+        const int i = least_of(t->rows - i0, kTileI), j = least_of(t->cols - j0, kTileJ);
+        p.begin(t->a + i0 * t->a_ld + b0 * kBlock, (int)t->a_ld, i, depth);
+        q.begin(t->b + j0 * t->b_ld + b0 * kBlock, (int)t->b_ld, j, depth);
+        pe.begin(t->a_exps + i0 * t->a_exps_ld + b0, (int)t->a_exps_ld, i, blocks, back, wave, row_i());
+        const uint8_t* x = t->b_exps + (SQUARE ? j0 >> 7 : j0) * t->b_exps_ld + b0;
+        qe.begin(x, (int)t->b_exps_ld, SQUARE ? (j > 128 ? 2 : 1) : j, blocks, back, wave, row_j());
         issue_scales(0);
         issue_scales(1);
-        const uint32_t stage = back ? kStageBytes : 0;
-        p.issue(smem + stage, wave);
-        q.issue(smem + stage + PSide::kBytes, wave);
-        if (steps == 1) return;
-        p.issue(smem + kStageBytes - stage, wave);
-        q.issue(smem + kStageBytes - stage + PSide::kBytes, wave);
+        pair_left = steps > 1 ? 2 : 1;
+        stage0 = back ? kStageBytes : 0;
+    }
+    // No tile: the loads of the next two stages bring zeros.
+    __device__ __forceinline__ void begin_none()
+    {
+        p.left = q.left = 0;
+        pair_left = 0;
+        stage0 = 0;
+    }
+    __device__ __forceinline__ typename PSide::Loads begin_p(int n)
+    {
+        if (n >= pair_left) p.left = 0;
+        return p.next(smem + (n ? kStageBytes - stage0 : stage0), wave);
+    }
+    __device__ __forceinline__ typename QSide::Loads begin_q(int n)
+    {
+        if (n >= pair_left) q.left = 0;
+        return q.next(smem + (n ? kStageBytes - stage0 : stage0) + PSide::kBytes, wave);
+    }
+    // The n-th of the two stages.
+    __device__ __forceinline__ void begin_loads(int n)
+    {
+        const auto lp = begin_p(n);
+        const auto lq = begin_q(n);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) lp.issue(k);
+#pragma unroll
+        for (int k = 0; k < NJ; ++k) lq.issue(k);
     }
     // (Of the second stage, the last step's.)  The codes behind the depth's end, in the last block's chunk that it ends in, are other
     // rows': zeros instead.  (Both sides: 0 times NaN is none.)
-    __device__ __forceinline__ void cut(const TileArgs& t)
+    __device__ __forceinline__ void cut()
     {
-        const int chunk = (int)((t.depth - 1) % kBlock) >> 4, tail = (int)(t.depth & 15);
+        const int depth = (int)args_at()->depth;
+        const int chunk = ((depth - 1) & (kBlock - 1)) >> 4, tail = depth & 15;
+#pragma nounroll
         for (int row = threadIdx.x; row < kTileI + kTileJ; row += kThreads) {
             const bool second = row >= kTileI;
             const int r = second ? row - kTileI : row;
@@ -289,18 +351,27 @@ struct Tile {
     // builtin's result may go to other registers, and with 256 of 512 of them sums the compiler
     // moves 100 a step.  (What it reads has been written by an s_nop 1 before at least; what it
     // writes is read by the next step's products, and by `settled`.)
-    template <int F, int J, int I, typename R>
-    __device__ __forceinline__ void multiply(f4 (&acc)[NI][NJ], R read)
+    template <int F, int J, int I, typename R, typename L>
+    __device__ __forceinline__ void multiply(f4 (&acc)[NI][NJ], R read, L load)
     {
 #pragma unroll
         for (int j = 0; j < HJ; ++j) {
             read(j);
 #pragma unroll
-            for (int i = I * H; i < (I + 1) * H; ++i)
+            for (int i = 0; i < H; ++i) {
                 asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                             : "+a"(acc[i][J * HJ + j])
-                             : "v"(a[J * HJ + j]), "v"(b[i]), "v"(qs[F][SQUARE ? 0 : J * HJ + j]), "v"(ps[F][i]));
+                             : "+a"(acc[I * H + i][J * HJ + j])
+                             : "v"(a[J * HJ + j]), "v"(b[I * H + i]), "v"(qs[SQUARE ? F : J * HJ + j]), "v"(ps[I * H + i]));
+                load(j * H + i);
+            }
         }
+    }
+    // Of n loads those that follow the k-th of a quarter's products.
+    template <typename Loads>
+    static __device__ __forceinline__ void spread(const Loads& l, int n, int k)
+    {
+#pragma unroll
+        for (int q = n * k / (H * HJ); q < n * (k + 1) / (H * HJ); ++q) l.issue(q);
     }
     // The sums can be read: an instruction of 16 passes writes its last 18 wait states on.
     static __device__ __forceinline__ void settled(f4 (&acc)[NI][NJ])
@@ -330,140 +401,172 @@ struct Tile {
         for (int k = 0; k < HJ; ++k) read_a<0>(stage, k);
 #pragma unroll
         for (int k = 0; k < H; ++k) read_b<F>(stage, k);
-        read_scales<F>(s);
+        read_ps<F>(s);
+        read_qs<F, 0>(s);
     }
     // A step, in quarters.  Each is multiplied while what the next one lacks is read: first what the
     // step has, then its other half of A's rows, then of B's; behind the second barrier the next step's
     // first halves, each into registers that the quarter before has freed.  So the halves of A's
     // rows change places from step to step (F, the stage too).
     //
-    // MORE: there are two steps more.  A's piece of the one after next is loaded behind the first quarter,
-    // when all have read this stage's; B's behind the second.  (Both behind the second: the loads of a
-    // step had all arrived when the next were started, 8192 x 8192 x 8192 453 us.)
+    // MORE: there are two steps more.  A's piece of the one after next is loaded during the second
+    // quarter, when all have read this stage's, B's during the third.  The loads go between the products: a
+    // wave that has its SIMD to itself waits for 8 loads in a row to be taken (512 cycles) while
+    // nothing is multiplied.
     template <int F, bool MORE, typename B>
-    __device__ __forceinline__ void half_step(f4 (&acc)[NI][NJ], B behind)
+    __device__ __forceinline__ void half_step(int s, f4 (&acc)[NI][NJ], B behind)
     {
         constexpr uint32_t stage = F ? kStageBytes : 0;
-        multiply<F, 0, F>(acc, [&](int k) { read_b<1 - F>(stage, k); });
+        read_ps<1 - F>(s);
+        multiply<F, 0, F>(acc, [&](int k) { read_b<1 - F>(stage, k); }, [](int) {});
         if constexpr (MORE) {
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(kLgkmDone);
             asm volatile("s_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
-            p.issue(smem + stage, wave);
+            const auto loads = p.next(smem + stage, wave);
+            read_qs<F, 1>(s);
+            multiply<F, 0, 1 - F>(acc, [&](int k) { read_a<1>(stage, k); }, [&](int k) { spread(loads, NI, k); });
+            turn<NI>();
+        } else {
+            read_qs<F, 1>(s);
+            multiply<F, 0, 1 - F>(acc, [&](int k) { read_a<1>(stage, k); }, [](int) {});
+            turn<0>();
         }
-        multiply<F, 0, 1 - F>(acc, [&](int k) { read_a<1>(stage, k); });
-        turn<MORE ? NI : 0>();
-        if constexpr (MORE) q.issue(smem + stage + PSide::kBytes, wave);
         behind();
     }
-    template <int F>
+    template <int F, bool MORE>
     __device__ __forceinline__ void other_half(int s, f4 (&acc)[NI][NJ])
     {
-        constexpr uint32_t other = F ? 0 : kStageBytes;
-        read_scales<1 - F>(s + 1);
-        multiply<F, 1, 1 - F>(acc, [&](int k) { read_a<0>(other, k); });
-        multiply<F, 1, F>(acc, [&](int k) { read_b<1 - F>(other, k); });
+        constexpr uint32_t stage = F ? kStageBytes : 0, other = kStageBytes - stage;
+        read_qs<1 - F, 0>(s + 1);
+        if constexpr (MORE) {
+            const auto loads = q.next(smem + stage + PSide::kBytes, wave);
+            multiply<F, 1, 1 - F>(acc, [&](int k) { read_a<0>(other, k); }, [&](int k) { spread(loads, NJ, k); });
+        } else {
+            multiply<F, 1, 1 - F>(acc, [&](int k) { read_a<0>(other, k); }, [](int) {});
+        }
+        read_ps<1 - F>(s + 1);
+        multiply<F, 1, F>(acc, [&](int k) { read_b<1 - F>(other, k); }, [](int) {});
     }
-    // acc[ti][tj][e]: i = row_of(ti), j = column_of(tj) + e, within the tile.  `last` says whether the
-    // share's last block is the depth's, `stored` that a whole tile's results have been stored since begin().
-    // `free` is called when both stages have been read.
+    // acc[ti][tj][e]: i = row_of(ti), j = column_of(tj) + e, within the tile, begun with what the sums begin with.
+    // `ends` says whether the last step is cut, `stored` that a whole tile's results have been stored since
+    // begin_loads().  `next` begins the next tile (or none) when this one's stages have been read.
     // (No branch within the steps that repeat: with one the compiler keeps fewer sums in place.)
     template <typename N>
-    __device__ __forceinline__ void run(const TileArgs& t, int steps, bool last, bool stored, f4 (&acc)[NI][NJ], N free)
+    __device__ __forceinline__ void run(int steps, bool ends, bool stored, f4 (&acc)[NI][NJ], N next)
     {
-#pragma unroll
-        for (int ti = 0; ti < NI; ++ti)
-#pragma unroll
-            for (int tj = 0; tj < NJ; ++tj) acc[ti][tj] = f4{0, 0, 0, 0};
         // (the first stage; the second, and the stores, may still be under way)
-        if (steps == 1) turn<0>();
-        else if (stored) turn<kStageLoads + kStores>();
+        if (stored) turn<kStageLoads + kStores>();
         else turn<kStageLoads>();
-        const bool ends = last && (t.depth & 15) != 0;
         const int back = steps & 1, pairs = (steps + 1) / 2;
         int pair = back;
         if (back) {
-            if (ends && steps == 1) cut(t);
+            if (ends && steps == 1) cut();
             first<1>(1);
             if (steps > 1) {
-                half_step<1, true>(acc, [&] { issue_scales(0); });
-                other_half<1>(1, acc);
+                half_step<1, true>(1, acc, [&] { issue_scales(0); });
+                other_half<1, true>(1, acc);
             }
         } else {
             first<0>(0);
         }
         for (; pair + 1 < pairs; ++pair) {
-            half_step<0, true>(acc, [] {});
-            other_half<0>(2 * pair, acc);
-            half_step<1, true>(acc, [&] { issue_scales(pair); });      // (of the pair two on)
-            other_half<1>(2 * pair + 1, acc);
+            half_step<0, true>(2 * pair, acc, [] {});
+            other_half<0, true>(2 * pair, acc);
+            half_step<1, true>(2 * pair + 1, acc, [&] { issue_scales(pair); });      // (of the pair two on)
+            other_half<1, true>(2 * pair + 1, acc);
         }
         if (steps > 1) {
-            half_step<0, false>(acc, [&] {
-                if (ends) cut(t);
+            half_step<0, false>(2 * pair, acc, [&] {
+                if (ends) cut();
             });
-            other_half<0>(2 * pair, acc);
+            other_half<0, false>(2 * pair, acc);
         }
-        half_step<1, false>(acc, free);
-        multiply<1, 1, 0>(acc, [](int) {});
-        multiply<1, 1, 1>(acc, [](int) {});
+        half_step<1, false>(steps > 1 ? 2 * pair + 1 : 1, acc, next);
+        // the last two quarters, and the next tile's first two stages
+        {
+            const auto lp = begin_p(0);
+            const auto lq = begin_q(0);
+            multiply<1, 1, 0>(acc, [](int) {}, [&](int k) {
+                spread(lp, NI, k);
+                spread(lq, NJ, k);
+            });
+        }
+        {
+            const auto lp = begin_p(1);
+            const auto lq = begin_q(1);
+            multiply<1, 1, 1>(acc, [](int) {}, [&](int k) {
+                spread(lp, NI, k);
+                spread(lq, NJ, k);
+            });
+        }
         settled(acc);
     }
     static __device__ __forceinline__ int column_of(int tj, int wave, int lane) { return (wave & 1) * 128 + (tj >> 2) * 64 + (lane >> 4) * 16 + (tj & 3) * 4; }
     static __device__ __forceinline__ int row_of(int ti, int wave, int lane) { return (wave >> 1) * 16 * NI + ti * 16 + (lane & 15); }
 };
 
-// A lane's 16 results of a row side by side, twice.
-template <typename T, int NI, bool SQUARE>
-__device__ __forceinline__ void tile_out(const TileArgs& t, int64_t split, int64_t bi, int64_t bj, f4 (&acc)[NI][8])
+// A wave's results, 16 rows at a time through LDS at `room`, to be written in runs of 256 bytes: to the element
+// `to` of the wave's first row and column, `rows` and `cols` of which there are from there on (WHOLE: all).
+template <bool WHOLE, typename O, int NI, bool SQUARE>
+__device__ __forceinline__ void put_tile(O* to, int64_t ld, int rows, int cols, uint32_t room, f4 (&acc)[NI][8])
 {
     using G = Tile<NI, SQUARE>;
+    constexpr int W = 16 / sizeof(O), RUNS = 4 / sizeof(O);        // runs of 64 columns in 256 bytes
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));      // (addresses are made here, and not kept in registers over the products)
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t in = room + (lane & 15) * G::kOutRow + (lane >> 4) * 16 * sizeof(O);
+    const uint32_t out = room + (lane >> 4) * G::kOutRow + (lane & 15) * 16;
+    to += (lane >> 4) * ld + (lane & 15) * W;
+    cols -= (lane & 15) * W;
+    rows -= lane >> 4;
 #pragma unroll
-    for (int run = 0; run < 2; ++run) {
-        const int64_t j = bj * G::kTileJ + G::column_of(4 * run, wave, lane);
-        if (j >= t.cols) continue;
-        const bool whole = j + 16 <= t.cols;
-        float bias[16];
+    for (int ti = 0; ti < NI; ++ti)
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            bias[k] = t.bias != nullptr && t.part == nullptr && j + k < t.cols ? (float)static_cast<const T*>(t.bias)[j + k] : 0.0f;
+        for (int part = 0; part < 2 / RUNS; ++part) {
+            // (what follows is not done ahead, for all rows at once)
 #pragma unroll
-        for (int ti = 0; ti < NI; ++ti) {
-            const int64_t i = bi * G::kTileI + G::row_of(ti, wave, lane);
-            if (i >= t.rows) continue;
-            if (t.part != nullptr) {
-                float* to = t.part + (split * t.rows + i) * t.cols + j;
-                if (whole) {
+            for (int k = 0; k < 4 * RUNS; ++k) asm volatile("" : "+a"(acc[ti][part * RUNS * 4 + k]));
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) store_vec<float, 4>(to + 4 * q, acc[ti][4 * run + q]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (j + k < t.cols) to[k] = acc[ti][4 * run + (k >> 2)][k & 3];
-                }
-                continue;
-            }
-            T* to = static_cast<T*>(t.out) + i * t.out_ld + j;
-            constexpr int W = Vec<T>::W;
-            if (whole) {
+            for (int run = 0; run < RUNS; ++run)
 #pragma unroll
                 for (int q = 0; q < 16 / W; ++q) {
-                    vec_t<T, W> y;
+                    vec_t<O, W> y;
 #pragma unroll
-                    for (int e = 0; e < W; ++e) y[e] = static_cast<T>(acc[ti][4 * run + ((q * W + e) >> 2)][e & 3] + bias[q * W + e]);
-                    store_vec<T, W>(to + q * W, y);
+                    for (int e = 0; e < W; ++e) y[e] = static_cast<O>(acc[ti][(part * RUNS + run) * 4 + ((q * W + e) >> 2)][e & 3]);
+                    *(ZO_LDS u4*)(uintptr_t)(in + run * 128 + q * 16) = __builtin_bit_cast(u4, y);
                 }
-            } else {
+            asm volatile("" ::: "memory");         // (LDS takes a wave's accesses in their order)
+            if constexpr (WHOLE) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (j + k < t.cols) to[k] = static_cast<T>(acc[ti][4 * run + (k >> 2)][k & 3] + bias[k]);
+                for (int k = 0; k < 4; ++k)
+                    store_vec<O, W>(to + (ti * 16 + k * 4) * ld + part * 64,
+                                    __builtin_bit_cast(vec_t<O, W>, *(ZO_LDS const u4*)(uintptr_t)(out + k * 4 * G::kOutRow)));
+            } else {
+                const int left = cols - part * 64;
+#pragma nounroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t at = out + k * 4 * G::kOutRow;
+                    O* p = to + (ti * 16 + k * 4) * ld + part * 64;
+                    if (ti * 16 + k * 4 >= rows) continue;
+                    if (left >= W) {
+                        store_vec<O, W>(p, __builtin_bit_cast(vec_t<O, W>, *(ZO_LDS const u4*)(uintptr_t)at));
+                    } else {
+#pragma nounroll
+                        for (int e = 0; e < left; ++e) p[e] = *(ZO_LDS const O*)(uintptr_t)(at + e * sizeof(O));
+                    }
+                }
             }
+            asm volatile("" ::: "memory");
         }
-    }
+}
+
+template <typename O, int NI, bool SQUARE>
+__device__ __forceinline__ void put_tile(O* to, int64_t ld, int rows, int cols, uint32_t room, f4 (&acc)[NI][8])
+{
+    if (rows == 16 * NI && cols == 128) put_tile<true, O, NI, SQUARE>(to, ld, rows, cols, room, acc);
+    else put_tile<false, O, NI, SQUARE>(to, ld, rows, cols, room, acc);
 }
 
 __device__ __forceinline__ uint32_t lds_address(char* smem) { return (uint32_t)(uintptr_t)(ZO_LDS char*)smem; }
@@ -471,43 +574,87 @@ __device__ __forceinline__ uint32_t lds_address(char* smem) { return (uint32_t)(
 // A die's workgroups walk its tiles (each tile once for every split of the depth), and load the
 // next while they store a tile's results.
 template <typename T, int NI, bool SQUARE>
-__global__ __launch_bounds__(kThreads, NI == 2 ? 2 : 1) void tile_kernel(TileArgs t)
+__global__ __launch_bounds__(kThreads, 1) void tile_kernel(TileArgs)
 {
     using G = Tile<NI, SQUARE>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    const uint32_t tiles = t.ti * t.tj, all = tiles * t.splits;
-    const uint32_t die = blockIdx.x % kDies, q = all / kDies, r = all % kDies;
-    const uint32_t mine = q + (die < r ? 1 : 0);
-    const uint32_t stride = (gridDim.x + kDies - 1 - die) / kDies;       // workgroups of the die
-    uint32_t at = blockIdx.x / kDies;
+    const uint32_t lds = lds_address(smem);
+    uint32_t at, mine, stride, n0;             // of the die's tiles: the next, all, to the one after; the first
+    {
+        const ArgsAt t = args_at();
+        const uint32_t all = t->ti * t->tj * t->splits;
+        const uint32_t die = blockIdx.x % kDies, q = all / kDies, r = all % kDies;
+        mine = q + (die < r ? 1 : 0);
+        n0 = die * q + (die < r ? die : r);
+        stride = (gridDim.x + kDies - 1 - die) / kDies;        // workgroups of the die
+        at = blockIdx.x / kDies;
+    }
     if (at >= mine) return;
-    G g(t, lds_address(smem));
+    G g(args_at(), lds);
     uint32_t bi = 0, bj = 0;
-    int split = 0, b0 = 0, steps = 0;
-    bool stored = false;
+    int split = 0, steps = 0;
+    bool ends = false, stored = false;
     auto place = [&] {
+        const ArgsAt t = args_at();
         // (a die's share of all splits' tiles, one split after the other)
-        const uint32_t n = die * q + (die < r ? die : r) + at;
-        split = __builtin_amdgcn_readfirstlane(n / tiles);
-        tile_at(n - (uint32_t)split * tiles, t.ti, t.tj, bi, bj);
-        b0 = (int)((int64_t)t.blocks * split / t.splits);
-        steps = (int)((int64_t)t.blocks * (split + 1) / t.splits) - b0;
+        uint32_t n = n0 + at;
+        split = 0;
+        if (t->splits > 1) {
+            const uint32_t tiles = t->ti * t->tj;
+            split = __builtin_amdgcn_readfirstlane(n / tiles);
+            n -= (uint32_t)split * tiles;
+        }
+        tile_at(n, t->ti, t->tj, bi, bj);
+        const int b0 = (int)((int64_t)t->blocks * split / t->splits);
+        steps = (int)((int64_t)t->blocks * (split + 1) / t->splits) - b0;
+        ends = b0 + steps == t->blocks && (t->depth & 15) != 0;
         g.begin(t, (int64_t)bi * G::kTileI, (int64_t)bj * G::kTileJ, b0, steps);
     };
     place();
+    g.begin_loads(0);
+    g.begin_loads(1);
+    const int lane = threadIdx.x & 63;
     for (;;) {
-        f4 acc[NI][8];
-        const uint32_t i = bi, j = bj;
+        // this tile; place() goes on to the next
+        const int64_t i = (int64_t)bi * G::kTileI, j = (int64_t)bj * G::kTileJ;
         const int now = steps, part = split;
-        const bool last = b0 + steps == t.blocks;
+        f4 acc[NI][8];
+        {
+            float first[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) first[k] = 0.0f;
+            const ArgsAt t = args_at();
+            if (t->bias != nullptr && t->part == nullptr) {
+                const T* bias = static_cast<const T*>(t->bias) + j + G::column_of(0, g.wave, lane);
+                const int left = least_of(t->cols - j, G::kTileJ) - G::column_of(0, g.wave, lane);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) first[k] = (k >> 4) * 64 + (k & 15) < left ? (float)bias[(k >> 4) * 64 + (k & 15)] : 0.0f;
+            }
+#pragma unroll
+            for (int ti = 0; ti < NI; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < 8; ++tj)
+                    acc[ti][tj] = f4{first[(tj >> 2) * 16 + (tj & 3) * 4], first[(tj >> 2) * 16 + (tj & 3) * 4 + 1],
+                                     first[(tj >> 2) * 16 + (tj & 3) * 4 + 2], first[(tj >> 2) * 16 + (tj & 3) * 4 + 3]};
+        }
         at += stride;
-        g.run(t, now, last, stored, acc, [&] {
+        g.run(now, ends, stored, acc, [&] {
             if (at < mine) place();
+            else g.begin_none();
         });
-        tile_out<T, NI, SQUARE>(t, part, i, j, acc);
-        stored = (int64_t)(i + 1) * G::kTileI <= t.rows && (int64_t)(j + 1) * G::kTileJ <= t.cols;
-        if (at >= mine) return;
+        {
+            const ArgsAt t = args_at();
+            const int64_t i1 = i + (g.wave >> 1) * 16 * NI, j1 = j + (g.wave & 1) * 128;
+            const int rows = least_of(t->rows - i1, 16 * NI), cols = least_of(t->cols - j1, 128);
+            const uint32_t room = lds + 2 * (G::kStageBytes + G::kScaleBytes) + g.wave * G::kOutBytes;
+            if (t->part != nullptr) put_tile<float, NI, SQUARE>(t->part + (part * t->rows + i1) * t->cols + j1, t->cols, rows, cols, room, acc);
+            else put_tile<T, NI, SQUARE>(static_cast<T*>(t->out) + i1 * t->out_ld + j1, t->out_ld, rows, cols, room, acc);
+            stored = rows == 16 * NI && cols == 128;
+        }
+        if (at >= mine) break;
     }
+    // (zeros on their way to LDS)
+    __builtin_amdgcn_s_waitcnt(wait_for(0));
 }
 
 // The parts of a split product, added in the order of the splits: W results a lane.
