@@ -1048,19 +1048,22 @@ ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type)
         p.bytes = 256;
         return p;
     }
-    // The tile and the parts of the depth by what they should take: a step of 256 x 256 x 128
-    // about 1.6 us, of 128 rows 0.9, of 64 0.6; in bf16 3.2 and, two to a CU, 1.6; a round's beginning and
-    // end 4; parts go through memory at 4 TB/s, and through a launch.
+    // The tile and the parts of the depth by what they should take, in us: a step of 256 x 256 x 128 1.2,
+    // of 128 rows 0.71, of 64 0.66, a round's beginning and end 9, 4 and 3 (measured: 8192 x 1600 x 1600 30.2, 32.9 and
+    // 49.5; 1024 x 6400 x 1600 26.1, 18.4 and 28.2; 512 x 6400 x 1600 24.7, 16.5 and 13.5); in bf16 2.8 and, two of 64 rows to a
+    // CU, 1.5.  Parts go through memory at 6 TB/s, and through a launch of 3 (1600 x 1600 x 8192: 128 rows in two
+    // parts 39.4, in one 52.3; 6400 x 1600 x 8192: 256 rows in one 91.8, in two 119.9).
     p.exact = type == 3;
     double best = 0.0;
     p.splits = 1;
     for (int ni = 8; ni >= 2; ni /= 2) {
         if (p.exact && ni == 4) continue;
         const int64_t tiles = ceil_div(m, 32 * ni) * ceil_div(n, 256), stand = kCUs * (p.exact && ni == 2 ? 2 : 1);
-        const double step = p.exact ? (ni == 8 ? 3.2 : 1.6) : ni == 8 ? 1.6 : ni == 4 ? 0.9 : 0.6;
-        const int64_t most = blocks / 4 > 1 ? blocks / 4 : 1;
+        const double step = p.exact ? (ni == 8 ? 2.8 : 1.5) : ni == 8 ? 1.2 : ni == 4 ? 0.71 : 0.66;
+        const double ends = p.exact ? 4.0 : ni == 8 ? 9.0 : ni == 4 ? 4.0 : 3.0;
+        const int64_t most = blocks / 2 > 1 ? blocks / 2 : 1;
         for (int64_t c = 1; c <= most && (c == 1 || tiles * c <= 4 * kCUs); ++c) {
-            const double t = ceil_div(tiles * c, stand) * (ceil_div(blocks, c) * step + 4.0) + (c > 1 ? 2.0 * c * m * n * 4 / 4e6 + 5.0 : 0.0);
+            const double t = ceil_div(tiles * c, stand) * (ceil_div(blocks, c) * step + ends) + (c > 1 ? 2.0 * c * m * n * 4 / 6e6 + 3.0 : 0.0);
             if (best == 0.0 || t < best) {
                 best = t;
                 p.ni = ni;
