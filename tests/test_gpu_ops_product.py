@@ -88,7 +88,7 @@ def test_types_and_padded_rows(m, n, k, kind):
         check(out, *reference(a, ae, b, be, TYPES[kind]))
 
 
-@pytest.mark.parametrize("m,n,k", [(8192, 1600, 6400), (4801, 1601, 4099), (6400, 1600, 8192), (2048, 20480, 300), (40, 50257, 1600)])
+@pytest.mark.parametrize("m,n,k", [(8192, 1600, 6400), (4801, 1601, 4099), (6400, 1600, 8192), (2048, 20480, 300), (40, 50257, 1600), (20, 20480, 5120), (3, 5120, 20480)])
 @pytest.mark.parametrize("square", [False, True])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_many_tiles(m, n, k, square, kind):

@@ -101,7 +101,7 @@ struct ProductPlan {           // what a product's sizes settle
     int64_t k_ld;              // the depth in whole chunks of 16
     bool exact;                // by bf16 products (fp32 results)
     int ni;                    // tiles of 32 ni x 256; 0: few rows, no tiles
-    int splits;                // parts of the depth (few rows: waves that share it)
+    int splits;                // parts of the depth
     int64_t off_part, off_a, off_b;        // byte offsets into the workspace
     int64_t bytes;
 };

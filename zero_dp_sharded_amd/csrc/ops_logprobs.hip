@@ -447,7 +447,7 @@ __global__ __launch_bounds__(1024) void factor_kernel(FactorArgs a)
     uint32_t most = 0;
     for (int64_t n = threadIdx.x; n < a.count; n += 1024) {
         const float d = given(a, n), e = a.dentropy != nullptr ? a.dentropy[n] : 0.0f;
-        most = larger(most, finite_size(fabsf(d) + a.spread * fabsf(e)));
+        most = with_size(most, fabsf(d) + a.spread * fabsf(e));
     }
     most = lanes_max<64>(most);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = most;

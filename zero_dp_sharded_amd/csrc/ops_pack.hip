@@ -6,6 +6,8 @@
 // along a column one in LDS, and 8 codes side by side are there in either
 // direction.  The transposed codes go through LDS, to be written in runs of 128 bytes.
 
+#include <type_traits>
+
 #include "ops_common.h"
 #include "ops_internal.h"
 #include "ops_scaled.h"
@@ -16,16 +18,135 @@ namespace {
 constexpr int kTile = kScaleBlock;
 constexpr int kRun = kTile + 16;           // bytes between columns of codes in LDS
 
+// 8 x 8 elements of a lane, two side by side in a word where they are of 2 bytes, with what the largest and
+// the codes are taken from: of a row the elements in turn, of a column the rows in turn.
 template <typename T>
-struct Block {                             // 8 x 8 elements as they lie in memory
-    vec_t<T, 8> row[8];
+struct Block {
+    typedef vec_t<T, 2> two;
+    typedef vec_t<uint16_t, 2> word;
+    static constexpr uint32_t kInfinite = std::is_same<T, _Float16>::value ? 0x7c00u : 0x7f80u;
+    two v[8][4];
+
+    __device__ __forceinline__ void load(const T* x, int64_t stride)
+    {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const vec_t<T, 8> r = load_vec<T, 8>(x + p * stride);
+            __builtin_memcpy(v[p], &r, 16);
+        }
+    }
+    __device__ __forceinline__ void set(int p, int k, T x) { v[p][k / 2][k % 2] = x; }
+    __device__ __forceinline__ float at(int p, int k) const { return (float)v[p][k / 2][k % 2]; }
+    static __device__ __forceinline__ word most(word a, word b) { return __builtin_elementwise_max(a, b); }
+    __device__ __forceinline__ word size(int p, int w) const { return __builtin_bit_cast(word, __builtin_bit_cast(uint32_t, v[p][w]) & 0x7fff7fffu); }
+    static __device__ __forceinline__ uint32_t as_float(uint32_t half)
+    {
+        if constexpr (std::is_same<T, _Float16>::value) return bits((float)__builtin_bit_cast(_Float16, (uint16_t)half));
+        else return half << 16;
+    }
+    // The largest of the rows and of the columns, as bits of fp32; false: something is not finite.
+    __device__ __forceinline__ bool largest(uint32_t (&along)[8], uint32_t (&down)[8]) const
+    {
+        word d[4], all = {0, 0};
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            word a = size(p, 0);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const word x = size(p, w);
+                a = most(a, x);
+                d[w] = p ? most(d[w], x) : x;
+            }
+            all = most(all, a);
+            along[p] = as_float(larger(a[0], a[1]));
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            down[2 * w] = as_float(d[w][0]);
+            down[2 * w + 1] = as_float(d[w][1]);
+        }
+        return larger(all[0], all[1]) < kInfinite;
+    }
+    __device__ __forceinline__ uint2 row_codes(int p, float scale) const
+    {
+        short2_t lo = {0, 0}, hi = {0, 0};
+        lo = two_codes<false>(lo, v[p][0], scale);
+        lo = two_codes<true>(lo, v[p][1], scale);
+        hi = two_codes<false>(hi, v[p][2], scale);
+        hi = two_codes<true>(hi, v[p][3], scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    }
+    __device__ __forceinline__ two pair(int p, int k) const { return two{v[p][k / 2][k % 2], v[p + 1][k / 2][k % 2]}; }
+    __device__ __forceinline__ uint2 column_codes(int k, float scale) const
+    {
+        short2_t lo = {0, 0}, hi = {0, 0};
+        lo = two_codes<false>(lo, pair(0, k), scale);
+        lo = two_codes<true>(lo, pair(2, k), scale);
+        hi = two_codes<false>(hi, pair(4, k), scale);
+        hi = two_codes<true>(hi, pair(6, k), scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    }
 };
 
-template <typename T>
-__device__ __forceinline__ vec_t<T, 8> load8(const T* p)
+template <>
+struct Block<float> {
+    float v[8][8];
+
+    __device__ __forceinline__ void load(const float* x, int64_t stride)
+    {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const vec_t<float, 4> lo = load_vec<float, 4>(x + p * stride), hi = load_vec<float, 4>(x + p * stride + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[p][k] = lo[k];
+                v[p][4 + k] = hi[k];
+            }
+        }
+    }
+    __device__ __forceinline__ void set(int p, int k, float x) { v[p][k] = x; }
+    __device__ __forceinline__ float at(int p, int k) const { return v[p][k]; }
+    __device__ __forceinline__ bool largest(uint32_t (&along)[8], uint32_t (&down)[8]) const
+    {
+        uint32_t all = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            along[p] = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t u = bits(v[p][k]) & 0x7fffffffu;
+                along[p] = larger(along[p], u);
+                down[k] = p ? larger(down[k], u) : u;
+            }
+            all = larger(all, along[p]);
+        }
+        return all < kNotFinite;
+    }
+    __device__ __forceinline__ uint2 row_codes(int p, float scale) const
+    {
+        short2_t lo = {0, 0}, hi = {0, 0};
+        lo = two_codes<false>(lo, v[p][0], v[p][1], scale);
+        lo = two_codes<true>(lo, v[p][2], v[p][3], scale);
+        hi = two_codes<false>(hi, v[p][4], v[p][5], scale);
+        hi = two_codes<true>(hi, v[p][6], v[p][7], scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    }
+    __device__ __forceinline__ uint2 column_codes(int k, float scale) const
+    {
+        short2_t lo = {0, 0}, hi = {0, 0};
+        lo = two_codes<false>(lo, v[0][k], v[1][k], scale);
+        lo = two_codes<true>(lo, v[2][k], v[3][k], scale);
+        hi = two_codes<false>(hi, v[4][k], v[5][k], scale);
+        hi = two_codes<true>(hi, v[6][k], v[7][k], scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    }
+};
+
+// 8 codes with their E.
+__device__ __forceinline__ uint2 topped(uint2 codes, uint32_t E)
 {
-    if constexpr (sizeof(T) == 2) return load_vec<T, 8>(p);
-    else return __builtin_shufflevector(load_vec<T, 4>(p), load_vec<T, 4>(p + 4), 0, 1, 2, 3, 4, 5, 6, 7);
+    if (E == kTopScale) codes = make_uint2(below_top(codes.x), below_top(codes.y));
+    return codes;
 }
 
 // 8 codes to p, or as many of them as `left` says.
@@ -52,26 +173,26 @@ __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t 
     const T* x = static_cast<const T*>(a.x) + r * a.x_stride + c;
     Block<T> b;
     if (c + 8 <= a.width && r + 8 <= a.rows) {
-#pragma unroll
-        for (int p = 0; p < 8; ++p) b.row[p] = load8<T>(x + p * a.x_stride);
+        b.load(x, a.x_stride);
     } else {
 #pragma unroll
         for (int p = 0; p < 8; ++p)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                b.row[p][k] = r + p < a.rows && c + k < a.width ? x[p * a.x_stride + k] : static_cast<T>(0.0f);
+                b.set(p, k, r + p < a.rows && c + k < a.width ? x[p * a.x_stride + k] : static_cast<T>(0.0f));
     }
     uint32_t along[8], down[8];            // the largest of the lane's rows, and of its columns
+    if (!b.largest(along, down)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) along[k] = down[k] = 0;
+        for (int k = 0; k < 8; ++k) along[k] = down[k] = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
+        for (int p = 0; p < 8; ++p)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t u = finite_size((float)b.row[p][k]);
-            along[p] = larger(along[p], u);
-            down[k] = larger(down[k], u);
-        }
+            for (int k = 0; k < 8; ++k) {
+                along[p] = with_size(along[p], b.at(p, k));
+                down[k] = with_size(down[k], b.at(p, k));
+            }
+    }
     uint32_t E = 0;
     if constexpr (SQUARE) {
         uint32_t all = 0;
@@ -94,10 +215,7 @@ __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t 
             if (r + p >= a.rows) continue;
             if (!SQUARE && lane == 0) a.exps[(r + p) * a.exps_stride + c0 / kTile] = (uint8_t)e;
             if (c >= a.width) continue;
-            const float inverse = inverse_scale(e);
-            const vec_t<T, 8>& v = b.row[p];
-            const uint2 out = make_uint2(codes_of((float)v[0], (float)v[1], (float)v[2], (float)v[3], inverse),
-                                         codes_of((float)v[4], (float)v[5], (float)v[6], (float)v[7], inverse));
+            const uint2 out = topped(b.row_codes(p, from_bits(e << 23)), e);
             put8(a.codes + (r + p) * a.codes_stride + c, out, a.width - c);
         }
     }
@@ -117,10 +235,7 @@ __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t 
             e = scale_of(m);
             if (band == 0 && c + k < a.width) a.exps_t[(c + k) * a.exps_t_stride + r0 / kTile] = (uint8_t)e;
         }
-        const float inverse = inverse_scale(e);
-        const uint2 out = make_uint2(
-            codes_of((float)b.row[0][k], (float)b.row[1][k], (float)b.row[2][k], (float)b.row[3][k], inverse),
-            codes_of((float)b.row[4][k], (float)b.row[5][k], (float)b.row[6][k], (float)b.row[7][k], inverse));
+        const uint2 out = topped(b.column_codes(k, from_bits(e << 23)), e);
         *reinterpret_cast<uint2*>(turned + (lane * 8 + k) * kRun + band * 8) = out;
     }
     __syncthreads();

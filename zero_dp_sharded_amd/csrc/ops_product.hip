@@ -847,17 +847,31 @@ __global__ __launch_bounds__(1024) void few_kernel(FewArgs f, int64_t first)
         acc[t] = f4{0, 0, 0, 0};
     }
     const int whole = (int)(f.depth / kBlock), blocks = (int)ceil_div(f.depth, kBlock);
-    for (int s = wave; s < whole; s += f.waves) {
-        v8i x;
-        __builtin_memcpy(&x, b + (int64_t)s * kBlock + g * 32, 32);
-        const uint32_t scale = be[s];
+    // U blocks at a time, all of their loads under way before the first product
+    auto blocks_from = [&](int s, auto count) {
+        constexpr int U = decltype(count)::value;
+        v8i x[U], y[U][MT];
+        uint32_t sx[U], sy[U][MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            v8i y;
-            __builtin_memcpy(&y, a[t] + (int64_t)s * kBlock + g * 32, 32);
-            acc[t] = product_of<EXACT>(x, y, acc[t], scale, ae[t][s]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = s + u * f.waves;
+            __builtin_memcpy(&x[u], b + at * kBlock + g * 32, 32);
+            sx[u] = be[at];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                __builtin_memcpy(&y[u][t], a[t] + at * kBlock + g * 32, 32);
+                sy[u][t] = ae[t][at];
+            }
         }
-    }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[t] = product_of<EXACT>(x[u], y[u][t], acc[t], sx[u], sy[u][t]);
+    };
+    constexpr int U = MT == 1 ? 4 : 2;
+    int s = wave;
+    for (; s + (U - 1) * f.waves < whole; s += U * f.waves) blocks_from(s, std::integral_constant<int, U>{});
+    for (; s < whole; s += f.waves) blocks_from(s, std::integral_constant<int, 1>{});
     if (blocks > whole && wave == whole % f.waves) {
         const int64_t k = (int64_t)whole * kBlock + g * 32;
         const v8i x = codes_at(b, k, f.depth);
@@ -882,7 +896,7 @@ __global__ __launch_bounds__(1024) void few_kernel(FewArgs f, int64_t first)
 
 // ------------------------------------------------------------------ launches
 
-// Rows up to which B goes straight to registers.
+// Rows up to which B may go straight to registers.
 constexpr int64_t kFewRows = 32;
 
 template <typename K>
@@ -968,12 +982,17 @@ hipError_t product(const ScaledProduct& a, const ProductPlan& p, hipStream_t s)
         join(0);
         return hipGetLastError();
     }
-    if (p.ni == 0) {
+    // (of few rows also what the tiles would have to copy first: bytes at any address are loaded here)
+    const bool as_it_is = loads_as_it_is(a.a, a.a_stride) && loads_as_it_is(a.b, a.b_stride);
+    if (p.ni == 0 || (p.m <= kFewRows && !as_it_is)) {
+        // waves of a workgroup, which share the depth: as many as find work, up to 16
+        int waves = 1;
+        while (waves < 16 && waves * 2 <= ceil_div(p.k, kBlock)) waves *= 2;
         const FewArgs f{a.a, a.b, a.a_exps, a.b_exps, a.a_stride, a.b_stride, a.a_exps_stride, a.b_exps_stride, p.m, p.n, p.k, a.out_stride,
-                        a.bias, a.out, p.splits, a.square};
-        in_launches(ceil_div(p.n, 16), p.splits * 64, [&](int64_t first, int64_t count) {
-            if (p.m <= 16) few_kernel<T, 1><<<dim3((unsigned)count), p.splits * 64, 0, s>>>(f, first);
-            else few_kernel<T, 2><<<dim3((unsigned)count), p.splits * 64, 0, s>>>(f, first);
+                        a.bias, a.out, waves, a.square};
+        in_launches(ceil_div(p.n, 16), waves * 64, [&](int64_t first, int64_t count) {
+            if (p.m <= 16) few_kernel<T, 1><<<dim3((unsigned)count), waves * 64, 0, s>>>(f, first);
+            else few_kernel<T, 2><<<dim3((unsigned)count), waves * 64, 0, s>>>(f, first);
         });
         return hipGetLastError();
     }
@@ -1041,13 +1060,6 @@ ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type)
     p.k = k;
     p.k_ld = round_up(k, 16);
     const int64_t blocks = ceil_div(k, kBlock);
-    if (m <= kFewRows) {
-        // waves of a workgroup, which share the depth: as many as find work, up to 16
-        p.splits = 1;
-        while (p.splits < 16 && p.splits * 2 <= blocks) p.splits *= 2;
-        p.bytes = 256;
-        return p;
-    }
     // The tile and the parts of the depth by what they should take, in us: a step of 256 x 256 x 128 1.2,
     // of 128 rows 0.71, of 64 0.66, a round's beginning and end 9, 4 and 3 (measured: 8192 x 1600 x 1600 30.2, 32.9 and
     // 49.5; 1024 x 6400 x 1600 26.1, 18.4 and 28.2; 512 x 6400 x 1600 24.7, 16.5 and 13.5); in bf16 2.8 and, two of 64 rows to a
@@ -1070,6 +1082,15 @@ ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type)
                 p.splits = (int)c;
             }
         }
+    }
+    // (the operands' values in bf16 first: 3 bytes a code at 5 TB/s, two launches)
+    if (p.exact) best += (double)(m + n) * k * 3 / 5e6 + 6.0;
+    // Few rows without tiles, where that should take less: what a wave reads of A grows with the rows (a row x 6400 x
+    // 1600 10.6 us, 32 rows 10.6, in tiles 13.6; a row x 20480 x 5120 21.9, 32 rows 45, in tiles 25.6).
+    if (m <= kFewRows && 8.5 + (double)n * k * 1e-6 * (0.145 + 0.0105 * m) < best + 5.0) {
+        p.ni = 0;
+        p.bytes = 256;
+        return p;
     }
     int64_t at = 0;
     auto take = [&](int64_t bytes) {

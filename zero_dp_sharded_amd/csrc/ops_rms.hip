@@ -84,13 +84,17 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint8_t* exps, int64_t
 {
     uint32_t big = 0;
 #pragma unroll
-    for (int k = 0; k < W; ++k) big = larger(big, finite_size(x[k]));
+    for (int k = 0; k < W; ++k) big = larger(big, bits(x[k]) & 0x7fffffffu);
+    if (big >= kNotFinite) {
+        big = 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k) big = with_size(big, x[k]);
+    }
     const uint32_t E = scale_of(lanes_max<kScaleBlock / W>(big));
     if (c >= width) return;
-    const float inverse = inverse_scale(E);
     vec_t<uint32_t, W / 4> v;
 #pragma unroll
-    for (int q = 0; q < W / 4; ++q) v[q] = codes_of(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3], inverse);
+    for (int q = 0; q < W / 4; ++q) v[q] = codes_of(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3], E);
     if (c + W <= width) {
         __builtin_memcpy(row + c, &v, W);
     } else {

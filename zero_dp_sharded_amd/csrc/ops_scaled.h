@@ -84,12 +84,14 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x)
     return x;
 }
 
-// What of x enters its block's largest, as the bits of |x| (which are in the order of the
-// values): 0 where x is not finite.
-__device__ __forceinline__ uint32_t finite_size(float x)
+constexpr uint32_t kNotFinite = 0x7f800000u;       // bits of |x| from there on
+
+// The larger of `most` and what of x enters its block's largest: the bits of |x|, which are in the order of
+// the values, or nothing where x is not finite.
+__device__ __forceinline__ uint32_t with_size(uint32_t most, float x)
 {
     const uint32_t a = bits(x) & 0x7fffffffu;
-    return a < 0x7f800000u ? a : 0u;
+    return a < kNotFinite ? larger(most, a) : most;
 }
 
 // E of a block whose largest finite value has the bits u: 2^(e - 8), or the next where the
@@ -100,9 +102,6 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t u)
     return e < (int)kLeastScale ? kLeastScale : (uint32_t)e;
 }
 
-// 2^(127 - E), by which a block's elements are multiplied (E as above: 27 to 247).
-__device__ __forceinline__ float inverse_scale(uint32_t E) { return from_bits((254 - E) << 23); }
-
 // 2^(E - 127) for every byte E.
 __device__ __forceinline__ float scale_value(uint32_t E)
 {
@@ -110,15 +109,45 @@ __device__ __forceinline__ float scale_value(uint32_t E)
     return from_bits(E == 0 ? 0x00400000u : E << 23);
 }
 
-// Four codes, of x * inverse, rounded to nearest even.
-__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float x2, float x3, float inverse)
+// Two codes in the half HI of `to`, rounded to nearest even from x 2^(127 - E).  (The conversions take the
+// scale, and make NaN of what is not finite; nothing here is above 448 of it.)
+typedef short short2_t __attribute__((ext_vector_type(2)));
+template <bool HI>
+__device__ __forceinline__ short2_t two_codes(short2_t to, float x0, float x1, float scale)
 {
-    auto one = [&](float x) {
-        const float most = 0x1.ep127f;
-        return fabsf(x) < INFINITY ? __builtin_amdgcn_fmed3f(x, -most, most) * inverse : __builtin_nanf("");
-    };
-    int r = __builtin_amdgcn_cvt_pk_fp8_f32(one(x0), one(x1), 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(one(x2), one(x3), r, true);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(to, x0, x1, scale, HI);
+}
+template <bool HI>
+__device__ __forceinline__ short2_t two_codes(short2_t to, vec_t<_Float16, 2> x, float scale)
+{
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(to, x, scale, HI);
+}
+template <bool HI>
+__device__ __forceinline__ short2_t two_codes(short2_t to, vec_t<__bf16, 2> x, float scale)
+{
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(to, x, scale, HI);
+}
+
+// The largest E is a block's whose largest is above 1.75 2^127: what is rounded to 2^128 there (code 0x78) is
+// held as the number below it.
+constexpr uint32_t kTopScale = 247;
+__device__ __forceinline__ uint32_t below_top(uint32_t codes)
+{
+#pragma unroll
+    for (int k = 0; k < 32; k += 8)
+        if ((codes >> k & 0x7f) == 0x78) codes -= 1u << k;
+    return codes;
+}
+
+// Four codes of x with E.
+__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float x2, float x3, uint32_t E)
+{
+    const float scale = from_bits(E << 23);
+    short2_t r = {0, 0};
+    r = two_codes<false>(r, x0, x1, scale);
+    r = two_codes<true>(r, x2, x3, scale);
+    const uint32_t c = __builtin_bit_cast(uint32_t, r);
+    return E == kTopScale ? below_top(c) : c;
 }
 
 }  // namespace zo
