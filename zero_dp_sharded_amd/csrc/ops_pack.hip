@@ -16,7 +16,10 @@ namespace zo {
 namespace {
 
 constexpr int kTile = kScaleBlock;
-constexpr int kRun = kTile + 16;           // bytes between columns of codes in LDS
+
+// Where 8 codes of a column lie in LDS, rows 8 band to + 7: a lane's 8 columns and its neighbours' are written
+// at once, and the exclusive or takes them to different banks.
+__device__ __forceinline__ int turned_at(int column, int band) { return column * kTile + ((band ^ (column >> 3)) & 15) * 8; }
 
 // 8 x 8 elements of a lane, two side by side in a word where they are of 2 bytes, with what the largest and
 // the codes are taken from: of a row the elements in turn, of a column the rows in turn.
@@ -164,9 +167,12 @@ __device__ __forceinline__ void put8(uint8_t* p, uint2 v, int64_t left)
 template <typename T, bool SQUARE>
 __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t first)
 {
-    __shared__ uint32_t big[16][kTile];
-    __shared__ __attribute__((aligned(16))) uint8_t turned[kTile * kRun];
-    const int64_t id = first + blockIdx.x;
+    __shared__ uint32_t big[4][kTile];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kTile * kTile], scales[kTile];
+    // (the dies, which workgroups go round, have runs of tiles: what tiles side by side share of a line, of the
+    // exponents above all, is in one L2.  4801 x 1601 fp32 squares 10.1 -> 7.8 us)
+    const uint32_t die = blockIdx.x % 8, per = gridDim.x / 8, rest = gridDim.x % 8;
+    const int64_t id = first + die * per + (die < rest ? die : rest) + blockIdx.x / 8;
     const int64_t r0 = id / a.tiles * kTile, c0 = id % a.tiles * kTile;
     const int lane = threadIdx.x & 15, band = threadIdx.x >> 4;       // columns 8 lane .., rows 8 band ..
     const int64_t c = c0 + lane * 8, r = r0 + band * 8;
@@ -220,23 +226,35 @@ __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t 
         }
     }
     if (a.codes_t == nullptr) return;
+    uint2 es = make_uint2(0, 0);           // E of the lane's 8 columns
     if constexpr (!SQUARE) {
+        // over a wave's 4 bands, then over the waves
 #pragma unroll
-        for (int k = 0; k < 8; ++k) big[band][lane * 8 + k] = down[k];
+        for (int k = 0; k < 8; ++k) {
+            auto r = __builtin_amdgcn_permlane16_swap(down[k], down[k], false, false);
+            down[k] = larger(r[0], r[1]);
+            r = __builtin_amdgcn_permlane32_swap(down[k], down[k], false, false);
+            down[k] = larger(r[0], r[1]);
+        }
+        if ((threadIdx.x & 48) == 0) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<uint4*>(&big[threadIdx.x >> 6][lane * 8 + q * 4]) = make_uint4(down[4 * q], down[4 * q + 1], down[4 * q + 2], down[4 * q + 3]);
+        }
         __syncthreads();
+        if (threadIdx.x < kTile) {
+            const int t = threadIdx.x;
+            const uint32_t e = scale_of(larger(larger(big[0][t], big[1][t]), larger(big[2][t], big[3][t])));
+            scales[t] = (uint8_t)e;
+            if (c0 + t < a.width) a.exps_t[(c0 + t) * a.exps_t_stride + r0 / kTile] = (uint8_t)e;
+        }
+        __syncthreads();
+        es = *reinterpret_cast<const uint2*>(scales + lane * 8);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        uint32_t e = E;
-        if constexpr (!SQUARE) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) m = larger(m, big[q][lane * 8 + k]);
-            e = scale_of(m);
-            if (band == 0 && c + k < a.width) a.exps_t[(c + k) * a.exps_t_stride + r0 / kTile] = (uint8_t)e;
-        }
-        const uint2 out = topped(b.column_codes(k, from_bits(e << 23)), e);
-        *reinterpret_cast<uint2*>(turned + (lane * 8 + k) * kRun + band * 8) = out;
+        const uint32_t e = SQUARE ? E : ((k < 4 ? es.x : es.y) >> (8 * (k % 4))) & 0xff;
+        *reinterpret_cast<uint2*>(turned + turned_at(lane * 8 + k, band)) = topped(b.column_codes(k, from_bits(e << 23)), e);
     }
     __syncthreads();
     // 8 lanes a column, 16 codes each
@@ -245,7 +263,10 @@ __global__ __launch_bounds__(256) void scaled_pack_kernel(ScaledPack a, int64_t 
     for (int q = 0; q < 4; ++q) {
         const int column = q * 32 + (threadIdx.x >> 3);
         if (c0 + column >= a.width || at >= a.rows) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(turned + column * kRun + (threadIdx.x & 7) * 16);
+        // (a pair of 8 lies in one 16, its halves changed over where the column says so)
+        const bool over = (column >> 3) & 1;
+        const uint4 u = *reinterpret_cast<const uint4*>(turned + (turned_at(column, (threadIdx.x & 7) * 2) & ~15));
+        const uint4 v = over ? make_uint4(u.z, u.w, u.x, u.y) : u;
         uint8_t* to = a.codes_t + (c0 + column) * a.codes_t_stride + at;
         if (at + 16 <= a.rows) {
             __builtin_memcpy(to, &v, 16);
