@@ -728,14 +728,14 @@ struct ExactArgs {
 };
 
 template <int NI, int NJ>
-__global__ __launch_bounds__(kGemmThreads, 2) void exact_kernel(ExactArgs t)
+__global__ __launch_bounds__(kGemmThreads, 2) void exact_kernel(ExactArgs t, int64_t first)
 {
     using G = Gemm<__bf16, kInner, kInner, NI, NJ>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    const uint32_t tiles = t.ti * t.tj;
-    const int64_t split = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles);
+    const uint32_t tiles = t.ti * t.tj, id = (uint32_t)first + blockIdx.x;
+    const int64_t split = __builtin_amdgcn_readfirstlane(id / tiles);
     uint32_t bi, bj;
-    tile_of(blockIdx.x % tiles, tiles, t.ti, t.tj, bi, bj);
+    tile_of(id % tiles, tiles, t.ti, t.tj, bi, bj);
     const int64_t s0 = t.steps * split / t.splits, s1 = t.steps * (split + 1) / t.splits;
     f4 acc[NI][NJ];
     G g(t.a, t.b, lds_address(smem));
@@ -938,7 +938,9 @@ hipError_t exact(ExactArgs t, hipStream_t s)
     if (allowed != hipSuccess) return allowed;
     t.ti = (uint32_t)ceil_div(t.rows, G::kTileI);
     t.tj = (uint32_t)ceil_div(t.cols, G::kTileJ);
-    exact_kernel<NI, NJ><<<dim3(t.ti * t.tj * t.splits), kGemmThreads, G::kLds, s>>>(t);
+    in_launches((int64_t)t.ti * t.tj * t.splits, kGemmThreads, [&](int64_t first, int64_t count) {
+        exact_kernel<NI, NJ><<<dim3((unsigned)count), kGemmThreads, G::kLds, s>>>(t, first);
+    });
     return hipSuccess;
 }
 
