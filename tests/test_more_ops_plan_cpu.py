@@ -60,8 +60,8 @@ def test_every_form_of_the_product_is_among_the_tests_sizes(plans):
     two = {plans[("b", *s)] for s in PRODUCTS}
     four = {plans[("f", *s)] for s in PRODUCTS}
     assert {ni for ni, _, exact in two if not exact} == {0, 2, 4, 8}
-    assert {ni for ni, _, exact in four if ni} == {2, 8} and all(exact for ni, _, exact in four if ni) and 0 in {ni for ni, _, _ in four}
-    for forms, tiles in ((two, (2, 4, 8)), (four, (2, 8))):
+    assert {ni for ni, _, exact in four if ni} == {2, 6, 8} and all(exact for ni, _, exact in four if ni) and 0 in {ni for ni, _, _ in four}
+    for forms, tiles in ((two, (2, 4, 8)), (four, (2, 6, 8))):
         for ni in tiles:
             parts = {splits > 1 for n, splits, _ in forms if n == ni}
             assert False in parts, ni

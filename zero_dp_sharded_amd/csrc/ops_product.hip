@@ -963,7 +963,7 @@ hipError_t exact(const ScaledProduct& a, const ProductPlan& p, float* part, hipS
     t.out_ld = p.splits > 1 ? p.n : a.out_stride;
     t.split_ld = p.m * p.n;
     t.bias = p.splits > 1 ? nullptr : static_cast<const float*>(a.bias);
-    return p.ni == 8 ? exact<8, 4>(t, s) : exact<2, 4>(t, s);
+    return p.ni == 8 ? exact<8, 4>(t, s) : p.ni == 6 ? exact<6, 4>(t, s) : exact<2, 4>(t, s);
 }
 
 template <typename T>
@@ -1064,16 +1064,17 @@ ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type)
     const int64_t blocks = ceil_div(k, kBlock);
     // The tile and the parts of the depth by what they should take, in us: a step of 256 x 256 x 128 1.2,
     // of 128 rows 0.71, of 64 0.66, a round's beginning and end 9, 4 and 3 (measured: 8192 x 1600 x 1600 30.2, 32.9 and
-    // 49.5; 1024 x 6400 x 1600 26.1, 18.4 and 28.2; 512 x 6400 x 1600 24.7, 16.5 and 13.5); in bf16 2.8 and, two of 64 rows to a
-    // CU, 1.5.  Parts go through memory at 6 TB/s, and through a launch of 3 (1600 x 1600 x 8192: 128 rows in two
-    // parts 39.4, in one 52.3; 6400 x 1600 x 8192: 256 rows in one 91.8, in two 119.9).
+    // 49.5; 1024 x 6400 x 1600 26.1, 18.4 and 28.2; 512 x 6400 x 1600 24.7, 16.5 and 13.5); in bf16 2.8, of 192 rows
+    // 2.2, of 64, two to a CU, 1.5 (4801 x 1601 x 4099: 256 rows 146.7, 192, in one round too, 116.6, 64 159.7;
+    // 4000 x 4000 x 4000: 142.2, 194.3, 177.3).  Parts go through memory at 6 TB/s, and through a launch of 3 (1600 x
+    // 1600 x 8192: 128 rows in two parts 39.4, in one 52.3; 6400 x 1600 x 8192: 256 rows in one 91.8, in two 119.9).
     p.exact = type == 3;
     double best = 0.0;
     p.splits = 1;
-    for (int ni = 8; ni >= 2; ni /= 2) {
-        if (p.exact && ni == 4) continue;
+    for (int ni = 8; ni >= 2; ni -= 2) {
+        if (ni == (p.exact ? 4 : 6)) continue;
         const int64_t tiles = ceil_div(m, 32 * ni) * ceil_div(n, 256), stand = kCUs * (p.exact && ni == 2 ? 2 : 1);
-        const double step = p.exact ? (ni == 8 ? 2.8 : 1.5) : ni == 8 ? 1.2 : ni == 4 ? 0.71 : 0.66;
+        const double step = p.exact ? (ni == 8 ? 2.8 : ni == 6 ? 2.2 : 1.5) : ni == 8 ? 1.2 : ni == 4 ? 0.71 : 0.66;
         const double ends = p.exact ? 4.0 : ni == 8 ? 9.0 : ni == 4 ? 4.0 : 3.0;
         const int64_t most = blocks / 2 > 1 ? blocks / 2 : 1;
         for (int64_t c = 1; c <= most && (c == 1 || tiles * c <= 4 * kCUs); ++c) {
