@@ -11,7 +11,7 @@
  *  - log probabilities of given tokens with entropy and top alternatives, from hidden states
  *    and the output weight, and their gradients;
  *  - AdamW over the tensors of a model at once, with moments in 32 or in 8 bits.
- * The gradients that the first two write are what a rank contributes to
+ * The gradients that they write are what a rank contributes to
  * zero_bucket_reduce (in the storage format, carrying the loss scale), or what
  * zero_adamw_step applies where a model's tensors are not one flat shard.
  *
@@ -89,8 +89,8 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
  *     h = x + residual, rounded to type            (residual NULL: h is x, and the
  *                                                   argument h NULL)
  *     rstd = 1 / sqrt(sum(h^2) / width + eps) ;  y = h * rstd * weight
- * in fp32.  The result is y, rounded to type once; or codes and exps, y in 8 bits as
- * zero_scaled_pack holds it (rounded once, from fp32); or both.  At least one is given.
+ * The sum, rstd and y are taken in 64 bits, and y to fp32.  The result is that, rounded to type; or
+ * codes and exps, it in 8 bits as zero_scaled_pack holds it; or both.  At least one is given.
  * Row r of an array begins at element r * its stride; exps has a byte for every 128
  * elements of a row, ceil(width / 128) in all.  affine is the storage of weight: type or
  * ZERO_FP32; weight NULL is 1.  rstd (fp32, one a row) may be NULL.  h may be x or residual,

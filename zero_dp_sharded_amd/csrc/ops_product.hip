@@ -11,10 +11,16 @@
 // operands' pieces straight to LDS, double buffered.  A wave has 16 NI x 128 results, and
 // with NI = 8 a SIMD's registers to itself: what is read from LDS is two thirds of what 8 waves
 // would read.  (Which of a row's chunks stands at which k of an instruction does not
-// matter, as long as both operands agree.)
+// matter, as long as both operands agree.)  With a wave alone on its SIMD nothing hides what it waits for:
+// loads go between the products one by one, and the next tile's are under way before this one's
+// results are written.  8192 x 8192 x 8192 to bf16 397 us, 2770 TFLOP/s (the library's fp8 product without
+// scales 2600 here); 8192 x 20480 x 5120 648 to 738 by the card's clock (668), bound by the power it may take.
+// Few tiles, or tiles that end badly in rounds of the card: lower ones, or parts of the depth (product_plan).
+// fp32 results: exact_kernel.
 //
 // Few rows: B is what costs.  A wave takes 16 of its rows straight to registers, the waves of a
-// workgroup share the depth and add their sums in LDS: one launch, no workspace.
+// workgroup share the depth and add their sums in LDS: one launch, no workspace.  A row x 6400 x 1600 5.7 us, of
+// which 1.6 are B's bytes: the launch, one trip to memory and the sums are the rest.
 
 #include <type_traits>
 
@@ -281,6 +287,7 @@ struct Tile {
     }
     // Steps go in pairs, the first of a pair through the first stage; of an odd count the first is the
     // second of its pair.
+    //
     // On to the tile at (i0, j0), `steps` blocks from b0 on: its scales are loaded, of its codes the first
     // two stages by begin_loads.  The second of a single step is zeros.
     __device__ __forceinline__ void begin(ArgsAt t, int64_t i0, int64_t j0, int b0, int steps)
@@ -324,8 +331,8 @@ struct Tile {
 #pragma unroll
         for (int k = 0; k < NJ; ++k) lq.issue(k);
     }
-    // (Of the second stage, the last step's.)  The codes behind the depth's end, in the last block's chunk that it ends in, are other
-    // rows': zeros instead.  (Both sides: 0 times NaN is none.)
+    // Of the second stage, the last step's: the codes behind the depth's end, in the chunk that it ends
+    // in, are other rows'.  Zeros instead.  (Both sides: 0 times NaN is none.)
     __device__ __forceinline__ void cut()
     {
         const int depth = (int)args_at()->depth;
@@ -715,7 +722,8 @@ __global__ __launch_bounds__(256) void recode_kernel(Recode a, Recode b, int64_t
 // Of a 2-byte result that is a hundredth or a tenth of its rounding, of one in fp32 a hundred
 // times its own; so those are summed by bf16 instructions, whose products are exact.  The operands'
 // values, which bf16 holds, are written out first: 3 bytes a code in 5 TB/s, against the
-// products' 2 operations for each of 256 results it meets.
+// products' 2 operations for each of 256 results it meets.  4801 x 1601 x 4099: 21 us for the values,
+// 100 for the product; its 182 tiles of 192 rows are one round of the 256 CUs.
 
 struct ExactArgs {
     Operand a, b;
