@@ -119,6 +119,15 @@ __device__ __forceinline__ void score_out(const ScoreArgs& a, int64_t bi, int64_
         for (int k = 1; k < R; ++k) m = fmaxf(m, acc[ti][k >> 2][k & 3]);
         m = fmaxf(m, __shfl_xor(m, 16, kWave));
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        if (NJ == 4 && (bj + 1) * G::kTileJ > a.vocab && m == -INFINITY) {
+            // (what lies behind the vocabulary is no element: a piece with NaN alone before it has that for its largest)
+            int some = 0;
+#pragma unroll
+            for (int k = 0; k < R; ++k) some |= v + k < a.vocab && acc[ti][k >> 2][k & 3] == acc[ti][k >> 2][k & 3];
+            some |= __shfl_xor(some, 16, kWave);
+            some |= __shfl_xor(some, 32, kWave);
+            if (!some) m = __builtin_nanf("");
+        }
         const int64_t token = a.tokens != nullptr && n < a.count ? a.tokens[n] : -1;
         const bool near = token >= v && token < v + 16;
         if (near || (NJ == 5 && token >= far + 16 && token < far + 20)) {
@@ -284,7 +293,6 @@ __global__ __launch_bounds__(64) void score_join_kernel(ScoreJoin a)
     } else {
         for (int p = lane; p < pieces; p += 64) m = fmaxf(m, row[p].x);
     }
-    const float reach = m;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
     const float base = m == -INFINITY ? 0.0f : m;
@@ -327,7 +335,14 @@ __global__ __launch_bounds__(64) void score_join_kernel(ScoreJoin a)
         else return Ranked{in_order(row[p].x), p};
     };
     const int rounds = (pieces + 63) / 64;
-    const uint32_t bound = bound_of(lane < pieces ? in_order(reach) : 0u, a.top, pieces);
+    uint32_t reach = 0;                         // (of NaN alone 0: a bound of 0, which all reach)
+    if constexpr (FEW) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) reach = larger(reach, piece(k).value);
+    } else {
+        for (int k = 0; k < rounds; ++k) reach = larger(reach, piece(k).value);
+    }
+    const uint32_t bound = bound_of(reach, a.top, pieces);
     int count = 0;
     auto collect = [&](int k) {
         const Ranked e = piece(k);
