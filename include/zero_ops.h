@@ -95,9 +95,9 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
  * elements of a row, ceil(width / 128) in all.  affine is the storage of weight: type or
  * ZERO_FP32; weight NULL is 1.  rstd (fp32, one a row) may be NULL.  h may be x or residual,
  * and y may be x (same address and stride).  rows = 0 does nothing.
- * Errors: INVALID_ARG (as zero_layernorm_forward; codes without exps or the reverse, h without
- * residual or the reverse, neither y nor codes), UNSUPPORTED (width > 2^24 or rows > 2^31 - 1),
- * HIP.
+ * Errors: INVALID_ARG (as zero_layernorm_forward, and eps above fp32's range; codes without exps
+ * or the reverse, h without residual or the reverse, neither y nor codes), UNSUPPORTED (width >
+ * 2^24 or rows > 2^31 - 1), HIP.
  */
 typedef struct {
     int64_t rows, width;

@@ -51,7 +51,7 @@ struct RmsForward {
     uint8_t* codes;        // NULL: y alone
     uint8_t* exps;
     int64_t rows, width, x_stride, residual_stride, h_stride, y_stride, codes_stride, exps_stride;
-    float eps;
+    double eps;
 };
 
 struct RmsBackward {

@@ -114,7 +114,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint8_t* exps, int64_t
 // The sum of squares, rstd and y are in 64 bits before they are rounded: no square passes its range, and a
 // result in 8 bits, which changes by a whole step where y lies next to a middle, is as good as always the
 // definition's (the vector unit's 64-bit rate is its 32-bit one).
-__device__ __forceinline__ double rstd_of(double q, int64_t width, float eps) { return 1.0 / sqrt(q / (double)width + (double)eps); }
+__device__ __forceinline__ double rstd_of(double q, int64_t width, double eps) { return 1.0 / sqrt(q / (double)width + eps); }
 
 __device__ __forceinline__ float scaled(float x, double rstd, float w) { return (float)((double)x * (rstd * (double)w)); }
 

@@ -484,7 +484,7 @@ zero_status zero_rmsnorm_forward(const zero_rmsnorm_desc* d, const void* x, cons
     if (const zero_status s = check_arrays(a, 8, who, {{0, 2}, {1, 2}, {0, 3}})) return s;
     if (const zero_status s = check_place(a, 8, stream, who)) return s;
     const zo::RmsForward f{x, residual, weight, h, y, rstd, codes, exps, rows, width, d->x_stride, d->residual_stride, d->h_stride,
-                           d->y_stride, d->codes_stride, d->exps_stride, (float)d->eps};
+                           d->y_stride, d->codes_stride, d->exps_stride, d->eps};
     const hipError_t err = zo::rms_forward(f, t, at, static_cast<hipStream_t>(stream));
     return err == hipSuccess ? ZERO_OK : hip_fail(err, who);
 }
