@@ -302,8 +302,9 @@ zero_status zero_token_logprobs(const zero_token_logprobs_desc* desc, const void
  *     dhidden = G weight ;  dweight = G^T hidden
  * dentropy may be NULL (then entropy may be too).  dlogprobs of a row whose id is ignore_index is not
  * used; a row with neither gradient enters nothing, whatever its hidden state holds.  A row
- * whose id is another outside [0, vocab) has NaN gradients.  Both results are written, not added to,
- * and carry what scale dlogprobs and dentropy carry; dweight is zeros with tokens = 0.
+ * whose id is another outside [0, vocab) has NaN gradients, and makes all of dweight NaN.  Both
+ * results are written, not added to, and carry what scale dlogprobs and dentropy carry; dweight is
+ * zeros with tokens = 0.
  * G is held in 2 bytes between the products, with the power of two that brings the largest row's
  * |dlogprobs| + |dentropy| (1 + log vocab) to the top of the range: in fp16 entries below 2^-39 of
  * that are lost.

@@ -566,8 +566,8 @@ __device__ __forceinline__ void dscore_out(const DScoreArgs& a, int64_t bi, int6
             const float u = acc[ti][k >> 2][k & 3] - f.lse;
             const float p = __builtin_amdgcn_exp2f(u * kLog2e);
             const float own = -f.d * (at == k ? rest : p);
-            float g = f.e != 0.0f ? fmaf(-f.e * p, u + f.entropy, own) : own;
-            if (p == 0.0f && at != k) g = 0.0f;                // (of -infinity too)
+            // (p log p is 0 where p is, of -infinity too; d and e that are not finite stay so)
+            float g = f.e != 0.0f ? fmaf(-f.e * p, p == 0.0f ? 0.0f : u + f.entropy, own) : own;
             if (none) g = 0.0f;
             high[k >> 2][k & 3] = static_cast<T>(g);
             if constexpr (NI == 2) low[k >> 2][k & 3] = static_cast<T>(g - (float)high[k >> 2][k & 3]);
