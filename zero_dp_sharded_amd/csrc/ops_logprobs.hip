@@ -467,21 +467,24 @@ template <typename T>
 __global__ __launch_bounds__(1024) void factor_kernel(FactorArgs a)
 {
     __shared__ uint32_t sh[16];
+    constexpr float kPart = 0x1p-8f;           // the sum passes fp32, not this part of it: spread is below 16
     uint32_t most = 0;
     for (int64_t n = threadIdx.x; n < a.count; n += 1024) {
         const float d = given(a, n), e = a.dentropy != nullptr ? a.dentropy[n] : 0.0f;
-        most = with_size(most, fabsf(d) + a.spread * fabsf(e));
+        most = with_size(most, kPart * fabsf(d) + kPart * a.spread * fabsf(e));
     }
     most = lanes_max<64>(most);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = most;
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int k = 1; k < 16; ++k) most = larger(most, sh[k]);
-    // (within what both factors can be in fp32)
-    int up = 0;
-    if (most != 0) (void)frexpf(from_bits(most), &up);
-    const int low = -126 + (int)kHoldLog2<T>, high = 126;
-    up = most == 0 ? 0 : up < low ? low : up > high ? high : up;
+    // (up to 133; not below what both factors can be in fp32)
+    const int low = -126 + (int)kHoldLog2<T>;
+    int up = low;
+    if (most != 0) {
+        (void)frexpf(from_bits(most), &up);
+        up = up + 8 < low ? low : up + 8;
+    }
     a.alpha[0] = ldexpf(1.0f, up - (int)kHoldLog2<T>);
     a.alpha[1] = ldexpf(1.0f, (int)kHoldLog2<T> - up);
 }
