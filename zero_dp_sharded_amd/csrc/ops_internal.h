@@ -118,6 +118,8 @@ struct ScaledProduct {
     bool square;               // b's scales
 };
 
+// Workgroups of a product's tiles of 32 ni x 256 that stand in a CU at once (by the LDS that they take).
+constexpr int product_tiles_in_cu(bool exact, int ni) { return exact && ni == 2 ? 2 : 1; }
 ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type);
 hipError_t scaled_product(const ScaledProduct& a, const ProductPlan& p, int type, hipStream_t s);
 

@@ -913,15 +913,19 @@ hipError_t allow(K kernel, int lds)
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
 }
 
+// LDS of a CU.
+constexpr int kCuLds = 160 << 10;
+
 template <typename T, int NI, bool SQUARE>
 hipError_t tiles(TileArgs t, hipStream_t s)
 {
     using G = Tile<NI, SQUARE>;
+    static_assert(product_tiles_in_cu(false, NI) == kCuLds / G::kLds, "a launch and its plan count the same workgroups to a CU");
     static const hipError_t allowed = allow(tile_kernel<T, NI, SQUARE>, G::kLds);
     if (allowed != hipSuccess) return allowed;
     t.ti = (uint32_t)ceil_div(t.rows, G::kTileI);
     t.tj = (uint32_t)ceil_div(t.cols, G::kTileJ);
-    const int64_t all = (int64_t)t.ti * t.tj * t.splits, stand = kCUs * (NI == 2 ? 2 : 1);
+    const int64_t all = (int64_t)t.ti * t.tj * t.splits, stand = kCUs * product_tiles_in_cu(false, NI);
     tile_kernel<T, NI, SQUARE><<<dim3((unsigned)(all < stand ? all : stand)), kThreads, G::kLds, s>>>(t);
     return hipSuccess;
 }
@@ -942,6 +946,7 @@ template <int NI, int NJ>
 hipError_t exact(ExactArgs t, hipStream_t s)
 {
     using G = Gemm<__bf16, kInner, kInner, NI, NJ>;
+    static_assert(product_tiles_in_cu(true, NI) == kCuLds / G::kLds, "the plan counts the workgroups that a CU holds");
     static const hipError_t allowed = allow(exact_kernel<NI, NJ>, G::kLds);
     if (allowed != hipSuccess) return allowed;
     t.ti = (uint32_t)ceil_div(t.rows, G::kTileI);
@@ -1081,7 +1086,7 @@ ProductPlan product_plan(int64_t m, int64_t n, int64_t k, int type)
     p.splits = 1;
     for (int ni = 8; ni >= 2; ni -= 2) {
         if (ni == (p.exact ? 4 : 6)) continue;
-        const int64_t tiles = ceil_div(m, 32 * ni) * ceil_div(n, 256), stand = kCUs * (p.exact && ni == 2 ? 2 : 1);
+        const int64_t tiles = ceil_div(m, 32 * ni) * ceil_div(n, 256), stand = kCUs * product_tiles_in_cu(p.exact, ni);
         const double step = p.exact ? (ni == 8 ? 2.8 : ni == 6 ? 2.2 : 1.5) : ni == 8 ? 1.2 : ni == 4 ? 0.71 : 0.66;
         const double ends = p.exact ? 4.0 : ni == 8 ? 9.0 : ni == 4 ? 4.0 : 3.0;
         const int64_t most = blocks / 2 > 1 ? blocks / 2 : 1;
