@@ -1,5 +1,6 @@
 // One tile of C[i][j] = sum_k P(i,k) Q(j,k) with 2-byte operands and fp32 sums, for
-// the three products of the vocabulary loss.
+// the products of the vocabulary loss and of the log probabilities, and for the scaled product's
+// fp32 results.
 //
 // A workgroup of 8 waves (2 by 4) takes 32 NI x 64 NJ results, 64 deep at a time:
 // both operands' pieces go from memory straight to LDS, double buffered, and each
@@ -62,8 +63,9 @@ template <> struct Mfma<_Float16> {
 };
 
 // Where an operand lies: `rows` i (or j) by `depth` k, 2-byte elements.  kInner:
-// element (i, k) at i * ld + k; kOuter: at k * ld + i.  Base 4-byte aligned, ld even,
-// ld <= 2^21 (an offset inside a tile stays below 2^31 - 16 bytes).
+// element (i, k) at i * ld + k; kOuter: at k * ld + i.  Base 4-byte aligned, ld even.
+// ld <= 2^21, or 2^22 where no tile has more than 256 rows of it: an offset inside a tile, its last row's at
+// most 255 * 2^23 + 112 bytes, stays below what a descriptor reaches (2^31 - 256).
 // Loads are of 8 elements: a kInner depth is a multiple of 8; what a kOuter tile reads
 // beyond `rows` goes into results that are none.
 struct Operand {
@@ -117,7 +119,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t v, const u4& rsrc, uint32_t
 }
 
 // kInner operand of 64 C rows: rows of 64 k (128 bytes) in LDS, 8 chunks each; a wave
-// loads C times 8 rows.  C is 1 (64 rows), 4 or 5.
+// loads C times 8 rows.  C is 1 (64 rows) to 5; 5 and RUNS are 256 rows and 64 beside them.
 //
 // Fragments: lane l has row l % 16 and the 8 k from (l / 16) * 8.  Product t of a wave
 // takes rows w0 + 16 t + r; with RUNS products 0 to 3 take rows w0 + 16 (r / 4) + 4 t + r % 4
