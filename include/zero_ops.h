@@ -89,8 +89,9 @@ zero_status zero_layernorm_backward(const void* dy, int64_t dy_stride, const voi
  *     h = x + residual, rounded to type            (residual NULL: h is x, and the
  *                                                   argument h NULL)
  *     rstd = 1 / sqrt(sum(h^2) / width + eps) ;  y = h * rstd * weight
- * The sum, rstd and y are taken in 64 bits, and y to fp32.  The result is that, rounded to type; or
- * codes and exps, it in 8 bits as zero_scaled_pack holds it; or both.  At least one is given.
+ * The sum, rstd and y are taken in 64 bits.  The result is y, rounded to fp32 and that to type; or
+ * codes and exps, y in 8 bits as zero_scaled_pack holds numbers, rounded to them once; or both.  At least
+ * one is given.
  * Row r of an array begins at element r * its stride; exps has a byte for every 128
  * elements of a row, ceil(width / 128) in all.  affine is the storage of weight: type or
  * ZERO_FP32; weight NULL is 1.  rstd (fp32, one a row) may be NULL.  h may be x or residual,

@@ -4,8 +4,8 @@
 // both; and backward, with the gradient dh that comes down the residual's way:
 //     xhat = h rstd ;  g = dy w ;  dx = rstd (g - xhat mean(g xhat)) + dh
 //     dw = sum_rows dy xhat
-// Backward in fp32, forward in 64 bits; h, y and the results are rounded once.  The norm is of h as it is
-// held: what the backward pass reads.
+// Backward in fp32, forward in 64 bits; h, the codes and the gradients are rounded once, y by way of fp32.  The norm
+// is of h as it is held: what the backward pass reads.
 //
 // Bound by memory, as the layer norm (ops_norm.hip), and laid out as it is: a row in
 // the registers of one to 16 waves between its sum and its results, rows of more than 16384
@@ -112,16 +112,61 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint8_t* exps, int64_t
 }
 
 // The sum of squares, rstd and y are in 64 bits before they are rounded: no square passes its range, and a
-// result in 8 bits, which changes by a whole step where y lies next to a middle, is as good as always the
+// result in 8 bits, which changes by a whole step where y lies next to a middle, is the
 // definition's (the vector unit's 64-bit rate is its 32-bit one).
 __device__ __forceinline__ double rstd_of(double q, int64_t width, double eps) { return 1.0 / sqrt(q / (double)width + eps); }
 
-__device__ __forceinline__ float scaled(float x, double rstd, float w) { return (float)((double)x * (rstd * (double)w)); }
+// y in fp32, which storage takes (2 bytes are rounded again: off by 2^-24 of y more than half a step at most).
+// ODD: rounded to odd, for codes: 24 bits of which the last says whether any was lost, so that none comes to lie on a
+// middle that is not there already, and the second rounding is of y itself.  (To the nearest twice, 15 to 23 of 8192 x
+// 5120 codes were a step off; 56 us then, 58 so.  Done only where fp32 looks like a middle it keeps more in registers: 62.)
+template <bool ODD>
+__device__ __forceinline__ float scaled(float x, double rstd, float w)
+{
+    const double y = (double)x * (rstd * (double)w);
+    if constexpr (!ODD) return (float)y;
+    constexpr uint32_t kLost = (1u << 29) - 1;             // of the 52 bits of a mantissa the last 29
+    const uint64_t u = __builtin_bit_cast(uint64_t, y);
+    const uint32_t low = (uint32_t)u, kept = (low | ((low & kLost) + kLost)) & ~kLost;
+    return (float)__builtin_bit_cast(double, (u >> 32) << 32 | kept);
+}
 
 // ------------------------------------------------------------------ forward
 
+template <typename A, int W>
+__device__ __forceinline__ void load_weight(const RmsForward& a, int64_t c, float (&w)[W])
+{
+#pragma unroll
+    for (int e = 0; e < W; ++e) w[e] = 1.0f;
+    if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
+}
+
+// x[0..W) of column c, normed: to y, or (CODED) as codes, and to y where that is given too.  All lanes of a block's group
+// come here together.
+template <bool PAST, bool CODED, typename A, typename T, int W>
+__device__ __forceinline__ void put_results(const RmsForward& a, int64_t row, T* y, int64_t c, const float (&x)[W], double rstd)
+{
+    float r[W];
+    if (!CODED || y != nullptr) {
+        load_weight<A>(a, c, r);
+#pragma unroll
+        for (int e = 0; e < W; ++e) r[e] = scaled<false>(x[e], rstd, r[e]);
+        if (c < a.width) store_part<PAST>(y, c, a.width, r);
+    }
+    if constexpr (CODED) {
+        load_weight<A>(a, c, r);
+#pragma unroll
+        for (int e = 0; e < W; ++e) r[e] = scaled<true>(x[e], rstd, r[e]);
+        // (past the width 0: inf or NaN as rstd make NaN of the zeros there)
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (c + e >= a.width) r[e] = 0.0f;
+        store_codes<W>(a.codes + row * a.codes_stride, a.exps + row * a.exps_stride, c, a.width, r);
+    }
+}
+
 // NW waves a row, K vectors a lane; with NW == 1 a workgroup has 4 rows.
-template <typename T, typename A, bool PAST, int NW, int K>
+template <typename T, typename A, bool PAST, bool CODED, int NW, int K>
 __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_forward_kernel(RmsForward a)
 {
     constexpr int W = Vec<T>::W;
@@ -165,25 +210,12 @@ __global__ __launch_bounds__(NW == 1 ? 256 : NW * 64) void rms_forward_kernel(Rm
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int64_t c = (int64_t)(k * NW * 64 + lane) * W;
-        float w[W];
-#pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = 1.0f;
-        if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
-#pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = scaled(v[k][e], rstd, w[e]);
-        if (y != nullptr && c < a.width) store_part<PAST>(y, c, a.width, w);
-        if (a.codes != nullptr) {
-            // (past the width 0: inf or NaN as rstd make NaN of the zeros there)
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                if (c + e >= a.width) w[e] = 0.0f;
-            store_codes<W>(a.codes + row * a.codes_stride, a.exps + row * a.exps_stride, c, a.width, w);
-        }
+        put_results<PAST, CODED, A>(a, row, y, c, v[k], rstd);
     }
 }
 
 // Rows too long for registers: 16 waves walk the row twice.
-template <typename T, typename A, bool PAST>
+template <typename T, typename A, bool PAST, bool CODED>
 __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
 {
     constexpr int W = Vec<T>::W;
@@ -219,15 +251,9 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
     T* y = a.y != nullptr ? static_cast<T*>(a.y) + row * a.y_stride : nullptr;
     // (whole blocks: the lanes of one come to its codes together)
     for (int64_t c = c0; c < round_up(a.width, kScaleBlock); c += step) {
-        float v[W], w[W];
+        float v[W];
         load_part<T, W>(from, c, a.width, v);
-#pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = 1.0f;
-        if (a.weight != nullptr) load_part<A, W>(static_cast<const A*>(a.weight), c, a.width, w);
-#pragma unroll
-        for (int e = 0; e < W; ++e) w[e] = c + e < a.width ? scaled(v[e], rstd, w[e]) : 0.0f;
-        if (y != nullptr && c < a.width) store_part<PAST>(y, c, a.width, w);
-        if (a.codes != nullptr) store_codes<W>(a.codes + row * a.codes_stride, a.exps + row * a.exps_stride, c, a.width, w);
+        put_results<PAST, CODED, A>(a, row, y, c, v, rstd);
     }
 }
 
@@ -515,7 +541,7 @@ RmsBackward from_row(RmsBackward a, int64_t first)
     return a;
 }
 
-template <typename T, typename A, bool PAST>
+template <typename T, typename A, bool PAST, bool CODED>
 hipError_t forward_rows(const RmsForward& a, hipStream_t s)
 {
     constexpr int W = Vec<T>::W;
@@ -528,14 +554,14 @@ hipError_t forward_rows(const RmsForward& a, hipStream_t s)
         });
     };
     constexpr int M = 8 / W;               // vectors of a lane in 8 elements
-    if (lanes <= 64 * M) run(rms_forward_kernel<T, A, PAST, 1, M>, 256, 4);
-    else if (lanes <= 128 * M) run(rms_forward_kernel<T, A, PAST, 1, 2 * M>, 256, 4);
-    else if (lanes <= 256 * M) run(rms_forward_kernel<T, A, PAST, 1, 4 * M>, 256, 4);
-    else if (lanes <= 512 * M) run(rms_forward_kernel<T, A, PAST, 4, 2 * M>, 256, 1);
-    else if (lanes <= 768 * M) run(rms_forward_kernel<T, A, PAST, 4, 3 * M>, 256, 1);
-    else if (lanes <= 1024 * M) run(rms_forward_kernel<T, A, PAST, 4, 4 * M>, 256, 1);
-    else if (lanes <= 2048 * M) run(rms_forward_kernel<T, A, PAST, 16, 2 * M>, 1024, 1);
-    else run(rms_forward_long_kernel<T, A, PAST>, 1024, 1);
+    if (lanes <= 64 * M) run(rms_forward_kernel<T, A, PAST, CODED, 1, M>, 256, 4);
+    else if (lanes <= 128 * M) run(rms_forward_kernel<T, A, PAST, CODED, 1, 2 * M>, 256, 4);
+    else if (lanes <= 256 * M) run(rms_forward_kernel<T, A, PAST, CODED, 1, 4 * M>, 256, 4);
+    else if (lanes <= 512 * M) run(rms_forward_kernel<T, A, PAST, CODED, 4, 2 * M>, 256, 1);
+    else if (lanes <= 768 * M) run(rms_forward_kernel<T, A, PAST, CODED, 4, 3 * M>, 256, 1);
+    else if (lanes <= 1024 * M) run(rms_forward_kernel<T, A, PAST, CODED, 4, 4 * M>, 256, 1);
+    else if (lanes <= 2048 * M) run(rms_forward_kernel<T, A, PAST, CODED, 16, 2 * M>, 1024, 1);
+    else run(rms_forward_long_kernel<T, A, PAST, CODED>, 1024, 1);
     return hipGetLastError();
 }
 
@@ -583,7 +609,9 @@ hipError_t backward_rows(const RmsBackward& a, hipStream_t s)
 template <typename T, typename A>
 hipError_t forward(const RmsForward& a, hipStream_t s)
 {
-    return a.rows * a.width * (int64_t)sizeof(T) > kCaches ? forward_rows<T, A, true>(a, s) : forward_rows<T, A, false>(a, s);
+    const bool past = a.rows * a.width * (int64_t)sizeof(T) > kCaches;
+    if (a.codes != nullptr) return past ? forward_rows<T, A, true, true>(a, s) : forward_rows<T, A, false, true>(a, s);
+    return past ? forward_rows<T, A, true, false>(a, s) : forward_rows<T, A, false, false>(a, s);
 }
 
 template <typename T, typename A>
