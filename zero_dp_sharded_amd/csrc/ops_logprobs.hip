@@ -14,18 +14,21 @@
 // chunk of tokens, and the wave reads only the pieces that can hold them: those whose
 // maxima are the `top` largest (a piece below has as many elements before each of its own).  And only those
 // are written: the first columns of tiles give each row a bound (columns_before), pieces below it stay
-// where they are.  8192 x 50257 x 1600 bf16 with entropy and 5 alternatives 1275 us: 1320 in the products
-// under a profiler (1000 TFLOP/s with their epilogue), 7 for the bounds, 52 for the join; 16 tokens with 20 alternatives
-// 61: 32 in the product, which reads W at 5 TB/s, 19 in the join, a wave's chain of sums and rankings.
+// where they are.  8192 x 50257 x 1600 bf16 with entropy and 5 alternatives 1270 us call after call; under a
+// profiler, whose launches stand apart, 140 for the first columns, 1243 for the others (950 TFLOP/s with their
+// epilogue), 7 for the bounds, 53 for the join.  Without alternatives, by tiles of 256 x 320, 1119, and 314 for 2048
+// tokens.  16 tokens with 20 alternatives 61: 32 in the product, which reads W at 5 TB/s by 197 workgroups, and 19 in
+// the join, a wave's chain of sums and rankings.
 //
 // Backward, the forward's lse and entropy make G in the epilogue of the same product: no pass over
 // it lies between, as the loss has (ops_loss.hip), whose two other products follow.  What is held
 // is G times a power of two that brings the largest |d| + |e| (1 + log vocab) to the top of the
-// type's range (fp16: 2^15 of it), taken back in the products' epilogues.  2048 x 50257 x 1600 fp16 900 us: 335
-// for G, 343 for each gradient.
+// type's range (fp16: 2^15 of it), taken back in the products' epilogues.  2048 x 50257 x 1600 fp16 916 us: 343
+// for G, 348 for each gradient.
 //
-// The 4 waves to a tile of the 8-bit product do not pay here: with 25 steps to a tile, 8192 tokens took 1222 us
-// for 1277, and G of 2048 tokens, whose 256 x 320 tiles end better in rounds of the card, 380 for 335.
+// By the 4 waves to a tile of the 8-bit product, with 25 steps to a tile, 8192 tokens took 1222 us for 1277, and G of
+// 2048 tokens, whose 256 x 320 tiles end better in rounds of the card, 380 for 335.  Both kernels have this one form: the
+// forward's alone could have that.
 
 #include <type_traits>
 

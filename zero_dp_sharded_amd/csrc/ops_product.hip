@@ -13,13 +13,15 @@
 // would read.  (Which of a row's chunks stands at which k of an instruction does not
 // matter, as long as both operands agree.)  With a wave alone on its SIMD nothing hides what it waits for:
 // loads go between the products one by one, and the next tile's are under way before this one's
-// results are written.  8192 x 8192 x 8192 to bf16 397 us, 2770 TFLOP/s (the library's fp8 product without
-// scales 2600 here); 8192 x 20480 x 5120 648 to 738 by the card's clock (668), bound by the power it may take.
+// results are written.  8192 x 8192 x 8192 to bf16 390 us, 2820 TFLOP/s (the library's fp8 product without
+// scales 2640 here); 8192 x 20480 x 5120 650 call after call (the library 693), 684 to 810 among a profiler's passes:
+// bound by the power that the card may take.  With scales by rows on B's side too, 8 bytes of them a step for one, 3 to
+// 7% more: 8192 x 8192 x 8192 415, 20480 x 5120 x 8192 712 to 737 for 680.
 // Few tiles, or tiles that end badly in rounds of the card: lower ones, or parts of the depth (product_plan).
 // fp32 results: exact_kernel.
 //
 // Few rows: B is what costs.  A wave takes 16 of its rows straight to registers, the waves of a
-// workgroup share the depth and add their sums in LDS: one launch, no workspace.  A row x 6400 x 1600 5.7 us, of
+// workgroup share the depth and add their sums in LDS: one launch, no workspace.  A row x 6400 x 1600 5.5 us, of
 // which 1.6 are B's bytes: the launch, one trip to memory and the sums are the rest.
 
 #include <type_traits>
@@ -723,7 +725,8 @@ __global__ __launch_bounds__(256) void recode_kernel(Recode a, Recode b, int64_t
 // times its own; so those are summed by bf16 instructions, whose products are exact.  The operands'
 // values, which bf16 holds, are written out first: 3 bytes a code in 5 TB/s, against the
 // products' 2 operations for each of 256 results it meets.  4801 x 1601 x 4099: 21 us for the values,
-// 100 for the product; its 182 tiles of 192 rows are one round of the 256 CUs.
+// 106 for the product under a profiler (call after call 117 in all); its 182 tiles of 192 rows are one round of
+// the 256 CUs, of which 74 have none.
 
 struct ExactArgs {
     Operand a, b;

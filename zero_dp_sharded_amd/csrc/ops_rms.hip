@@ -7,15 +7,18 @@
 // Backward in fp32, forward in 64 bits; h, the codes and the gradients are rounded once, y by way of fp32.  The norm
 // is of h as it is held: what the backward pass reads.
 //
-// Bound by memory, as the layer norm (ops_norm.hip), and laid out as it is: a row in
-// the registers of one to 16 waves between its sum and its results, rows of more than 16384
-// elements read again from cache.  Sums over a wave are moves within the vector unit.
-// 8192 x 5120 bf16 with a residual into 8 bits 56 us, 5.3 TB/s; 4099 x 1601 fp16 12 (odd rows: loads and
-// stores at any element); a row of 1600 5.
+// Bound by memory where rows are whole vectors of its waves, as the layer norm (ops_norm.hip), and laid
+// out as it is: a row in the registers of one to 16 waves between its sum and its results, rows of more
+// than 16384 elements read again from cache.  Sums over a wave are moves within the vector unit.  8192 x 5120
+// bf16 with a residual into 8 bits 58 us, 5.1 TB/s.
+//
+// Where a row ends within a vector of its waves, or before it (1600, 1601 elements of 2 bytes), load_raw's branch for single
+// elements, which waits for every load before it, makes a chain of the loads: x's, then the residual's, then, behind
+// the sum, the weight's.  4099 x 1601 fp16 13 us, of which its bytes are 8; a row of 1600 5.5.
 //
 // Backward, a workgroup walks rows and keeps its sums for dw, which a second kernel adds in
-// order; what bounds it is the chain of a row's sum behind its loads.  16384 x 1600 bf16 with dh 40 us,
-// 5.2 TB/s, and 4.5 for the sums.
+// order.  The next row is asked for before this one's sum; at widths as those the branch waits for it there, and
+// the loads hide behind nothing but other waves.  16384 x 1600 bf16 with dh 40 us, 5.2 TB/s, and 4.5 for the sums.
 
 #include "ops_common.h"
 #include "ops_internal.h"
@@ -260,7 +263,7 @@ __global__ __launch_bounds__(1024) void rms_forward_long_kernel(RmsForward a)
 // ------------------------------------------------------------------ backward
 
 // A workgroup of WAVES waves, NW to a row, walks rows blockIdx, blockIdx + grid, ... (in
-// groups of WAVES / NW), reads the next row while it is at one, and keeps its sums for dw.
+// groups of WAVES / NW), asks for the next row before it is at one, and keeps its sums for dw.
 // With one wave a row the weight is kept in LDS, to have the registers for that.
 template <typename T, typename A, bool PAST, int NW, int WAVES, int K>
 __global__ __launch_bounds__(WAVES * 64) void rms_backward_kernel(RmsBackward a)
